@@ -854,4 +854,354 @@ ep_status_t ep_dispatch_ranked_backward(const void* const* grad_recv_x,
     return EP_SUCCESS;
 }
 
+// ---- router, row movement, 4-bit products
+
+static size_t dtype_bytes(int dtype) { return dtype == EP_FP32 ? 4 : 2; }
+static bool off_by(const void* p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
+
+static ep_status_t check_dtype(int dtype, bool fp32)
+{
+    if (dtype == EP_BF16 || dtype == EP_FP16 || (fp32 && dtype == EP_FP32)) return EP_SUCCESS;
+    return fail(EP_INVALID_ARGUMENT, "dtype %d must be EP_BF16%s", dtype,
+                fp32 ? ", EP_FP16 or EP_FP32" : " or EP_FP16");
+}
+
+static ep_status_t check_router(int dtype, int64_t num_tokens, int num_experts, int64_t ld_logits,
+                                int num_topk, int score)
+{
+    ep_status_t st = check_dtype(dtype, true);
+    if (st) return st;
+    st = check_tokens(num_tokens, num_topk);
+    if (st) return st;
+    if (num_experts < 1 || num_experts > EP_MAX_EXPERTS)
+        return fail(EP_INVALID_ARGUMENT, "num_experts %d outside [1, %d]", num_experts, EP_MAX_EXPERTS);
+    if (ld_logits < num_experts)
+        return fail(EP_INVALID_ARGUMENT, "ld_logits %lld < num_experts %d", (long long)ld_logits,
+                    num_experts);
+    if (score != EP_SCORE_SOFTMAX && score != EP_SCORE_SIGMOID)
+        return fail(EP_INVALID_ARGUMENT, "unknown score %d", score);
+    return EP_SUCCESS;
+}
+
+ep_status_t ep_router(const void* logits, int dtype, int64_t num_tokens, int num_experts,
+                      int64_t ld_logits, int num_topk, int score, const float* bias,
+                      int num_groups, int topk_groups, int group_top, int renormalize, float scale,
+                      int64_t* topk_idx, float* topk_weights, float* probs, void* stream)
+{
+    g_last_error[0] = '\0';
+    ep_status_t st = check_router(dtype, num_tokens, num_experts, ld_logits, num_topk, score);
+    if (st) return st;
+    if (num_groups < 1 || num_groups > EP_MAX_GROUPS || num_experts % num_groups != 0)
+        return fail(EP_INVALID_ARGUMENT, "num_groups %d must divide num_experts %d and be at most %d",
+                    num_groups, num_experts, EP_MAX_GROUPS);
+    if (topk_groups < 1 || topk_groups > num_groups)
+        return fail(EP_INVALID_ARGUMENT, "topk_groups %d outside [1, %d]", topk_groups, num_groups);
+    if (group_top < 1 || group_top > 2)
+        return fail(EP_INVALID_ARGUMENT, "group_top %d must be 1 or 2", group_top);
+    if (num_topk > num_experts / num_groups * topk_groups)
+        return fail(EP_INVALID_ARGUMENT, "num_topk %d exceeds the %d experts of %d groups", num_topk,
+                    num_experts / num_groups * topk_groups, topk_groups);
+    if (num_tokens == 0) return EP_SUCCESS;
+    if (!logits || !topk_idx || !topk_weights)
+        return fail(EP_INVALID_ARGUMENT, "logits, topk_idx and topk_weights are required");
+    if (off_by(logits, dtype_bytes(dtype)) || off_by(bias, 4) || off_by(topk_idx, 8) ||
+        off_by(topk_weights, 4) || off_by(probs, 16))
+        return fail(EP_INVALID_ARGUMENT, "logits, bias, topk_idx and topk_weights must be aligned to "
+                                         "their elements, probs to 16 bytes");
+    const ep::RouterArgs a = {logits, num_tokens, ld_logits, num_experts, num_topk,
+                              score == EP_SCORE_SOFTMAX, bias, num_groups, topk_groups, group_top,
+                              renormalize != 0, scale, topk_idx, topk_weights, probs};
+    return from_hip(ep::launch_router(dtype, a, static_cast<hipStream_t>(stream)), "ep_router launch");
+}
+
+ep_status_t ep_router_backward(const void* logits, int dtype, int64_t num_tokens, int num_experts,
+                               int64_t ld_logits, int num_topk, int score, int renormalize,
+                               float scale, const int64_t* topk_idx, const float* grad_weights,
+                               const float* grad_probs, void* grad_logits, void* stream)
+{
+    g_last_error[0] = '\0';
+    ep_status_t st = check_router(dtype, num_tokens, num_experts, ld_logits, num_topk, score);
+    if (st) return st;
+    if (num_tokens == 0) return EP_SUCCESS;
+    if (!logits || !topk_idx || !grad_weights || !grad_logits)
+        return fail(EP_INVALID_ARGUMENT,
+                    "logits, topk_idx, grad_weights and grad_logits are required");
+    if (off_by(logits, dtype_bytes(dtype)) || off_by(topk_idx, 8) || off_by(grad_weights, 4) ||
+        off_by(grad_probs, 4) || off_by(grad_logits, dtype_bytes(dtype)))
+        return fail(EP_INVALID_ARGUMENT, "every argument must be aligned to its element");
+    const ep::RouterBackwardArgs a = {logits, num_tokens, ld_logits, num_experts, num_topk,
+                                      score == EP_SCORE_SOFTMAX, renormalize != 0, scale, topk_idx,
+                                      grad_weights, grad_probs, grad_logits};
+    return from_hip(ep::launch_router_backward(dtype, a, static_cast<hipStream_t>(stream)),
+                    "ep_router_backward launch");
+}
+
+static ep_status_t check_rows(int dtype, int64_t num_tokens, int hidden, int num_topk,
+                              int64_t num_rows)
+{
+    ep_status_t st = check_dtype(dtype, true);
+    if (st) return st;
+    st = check_tokens(num_tokens, num_topk);
+    if (st) return st;
+    st = check_hidden(hidden, 1);
+    if (st) return st;
+    if (num_rows < 0 || num_rows >= ((int64_t)1 << 31))
+        return fail(EP_INVALID_ARGUMENT, "num_rows %lld outside [0, 2^31)", (long long)num_rows);
+    if (ep::move_rows_max_blocks(dtype, num_tokens, hidden, num_topk) > INT32_MAX)
+        return fail(EP_UNSUPPORTED, "num_tokens * hidden needs more than 2^31 workgroups");
+    return EP_SUCCESS;
+}
+
+static ep_status_t check_matrix(const void* p, int64_t ld, int hidden, int dtype, const char* name)
+{
+    if (!p) return fail(EP_INVALID_ARGUMENT, "%s is required", name);
+    if (off_by(p, dtype_bytes(dtype)))
+        return fail(EP_INVALID_ARGUMENT, "%s must be aligned to its element", name);
+    if (ld < hidden)
+        return fail(EP_INVALID_ARGUMENT, "the row stride %lld of %s is below hidden %d", (long long)ld,
+                    name, hidden);
+    return EP_SUCCESS;
+}
+
+static ep_status_t check_pairs(const int32_t* slot, const float* w, const float* grad_w)
+{
+    if (!slot) return fail(EP_INVALID_ARGUMENT, "slot is required");
+    if (off_by(slot, 4) || off_by(w, 4) || off_by(grad_w, 4))
+        return fail(EP_INVALID_ARGUMENT, "slot, topk_weights and grad_weights must be 4-byte aligned");
+    return EP_SUCCESS;
+}
+
+static ep_status_t check_clear(const int32_t* counts, const int32_t* offsets, int num_experts)
+{
+    if ((counts != nullptr) != (offsets != nullptr))
+        return fail(EP_INVALID_ARGUMENT, "counts and offsets go together");
+    if (counts == nullptr) return EP_SUCCESS;
+    if (num_experts < 1 || num_experts > EP_MAX_EXPERTS)
+        return fail(EP_INVALID_ARGUMENT, "num_experts %d outside [1, %d]", num_experts, EP_MAX_EXPERTS);
+    if (off_by(counts, 4) || off_by(offsets, 4))
+        return fail(EP_INVALID_ARGUMENT, "counts and offsets must be 4-byte aligned");
+    return EP_SUCCESS;
+}
+
+ep_status_t ep_permute(const void* x, int dtype, int64_t num_tokens, int hidden, int64_t ld_x,
+                       int num_topk, const int32_t* slot, const float* topk_weights, void* rows,
+                       int64_t ld_rows, int64_t num_rows, const int32_t* counts,
+                       const int32_t* offsets, int num_experts, void* stream)
+{
+    g_last_error[0] = '\0';
+    ep_status_t st = check_rows(dtype, num_tokens, hidden, num_topk, num_rows);
+    if (st) return st;
+    st = check_clear(counts, offsets, num_experts);
+    if (st) return st;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (num_rows > 0) {
+        st = check_matrix(rows, ld_rows, hidden, dtype, "rows");
+        if (st) return st;
+    }
+    if (num_tokens > 0) {
+        st = check_matrix(x, ld_x, hidden, dtype, "x");
+        if (st) return st;
+        st = check_pairs(slot, topk_weights, nullptr);
+        if (st) return st;
+    }
+    if (num_rows == 0) return EP_SUCCESS;
+    if (counts) {
+        st = from_hip(ep::launch_clear_rows(dtype, counts, offsets, num_experts, rows, ld_rows,
+                                            num_rows, hidden, s),
+                      "ep_permute launch (clear)");
+        if (st) return st;
+    }
+    const ep::MoveArgs a = {false, x, ld_x, nullptr, 0, rows, ld_rows, num_tokens, num_rows, hidden,
+                            num_topk, slot, topk_weights, nullptr};
+    return from_hip(ep::launch_move_rows(dtype, a, s), "ep_permute launch");
+}
+
+ep_status_t ep_permute_backward(const void* grad_rows, int dtype, int64_t num_tokens, int hidden,
+                                int64_t ld_grad_rows, int64_t num_rows, int num_topk,
+                                const int32_t* slot, const float* topk_weights, const void* x,
+                                int64_t ld_x, void* grad_x, int64_t ld_grad_x, float* grad_weights,
+                                void* stream)
+{
+    g_last_error[0] = '\0';
+    ep_status_t st = check_rows(dtype, num_tokens, hidden, num_topk, num_rows);
+    if (st) return st;
+    if (num_tokens == 0) return EP_SUCCESS;
+    if (num_rows > 0) {
+        st = check_matrix(grad_rows, ld_grad_rows, hidden, dtype, "grad_rows");
+        if (st) return st;
+    }
+    st = check_matrix(grad_x, ld_grad_x, hidden, dtype, "grad_x");
+    if (st) return st;
+    st = check_pairs(slot, topk_weights, grad_weights);
+    if (st) return st;
+    if (grad_weights) {
+        st = check_matrix(x, ld_x, hidden, dtype, "x (with grad_weights)");
+        if (st) return st;
+    }
+    const ep::MoveArgs a = {true, grad_weights ? x : nullptr, grad_weights ? ld_x : 0,
+                            num_rows > 0 ? grad_rows : nullptr, num_rows > 0 ? ld_grad_rows : 0,
+                            grad_x, ld_grad_x, num_tokens, num_rows, hidden, num_topk, slot,
+                            topk_weights, grad_weights};
+    return from_hip(ep::launch_move_rows(dtype, a, static_cast<hipStream_t>(stream)),
+                    "ep_permute_backward launch");
+}
+
+ep_status_t ep_unpermute(const void* rows, int dtype, int64_t num_tokens, int hidden,
+                         int64_t ld_rows, int64_t num_rows, int num_topk, const int32_t* slot,
+                         const float* topk_weights, void* out, int64_t ld_out, void* stream)
+{
+    g_last_error[0] = '\0';
+    ep_status_t st = check_rows(dtype, num_tokens, hidden, num_topk, num_rows);
+    if (st) return st;
+    if (num_tokens == 0) return EP_SUCCESS;
+    if (num_rows > 0) {
+        st = check_matrix(rows, ld_rows, hidden, dtype, "rows");
+        if (st) return st;
+    }
+    st = check_matrix(out, ld_out, hidden, dtype, "out");
+    if (st) return st;
+    st = check_pairs(slot, topk_weights, nullptr);
+    if (st) return st;
+    const ep::MoveArgs a = {true, nullptr, 0, num_rows > 0 ? rows : nullptr,
+                            num_rows > 0 ? ld_rows : 0, out, ld_out, num_tokens, num_rows, hidden,
+                            num_topk, slot, topk_weights, nullptr};
+    return from_hip(ep::launch_move_rows(dtype, a, static_cast<hipStream_t>(stream)),
+                    "ep_unpermute launch");
+}
+
+ep_status_t ep_unpermute_backward(const void* grad_out, int dtype, int64_t num_tokens, int hidden,
+                                  int64_t ld_grad_out, int num_topk, const int32_t* slot,
+                                  const float* topk_weights, const void* rows, int64_t ld_rows,
+                                  void* grad_rows, int64_t ld_grad_rows, int64_t num_rows,
+                                  float* grad_weights, const int32_t* counts,
+                                  const int32_t* offsets, int num_experts, void* stream)
+{
+    g_last_error[0] = '\0';
+    ep_status_t st = check_rows(dtype, num_tokens, hidden, num_topk, num_rows);
+    if (st) return st;
+    st = check_clear(counts, offsets, num_experts);
+    if (st) return st;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (num_rows > 0) {
+        st = check_matrix(grad_rows, ld_grad_rows, hidden, dtype, "grad_rows");
+        if (st) return st;
+        if (grad_weights) {
+            st = check_matrix(rows, ld_rows, hidden, dtype, "rows (with grad_weights)");
+            if (st) return st;
+        }
+    }
+    if (num_tokens > 0) {
+        st = check_matrix(grad_out, ld_grad_out, hidden, dtype, "grad_out");
+        if (st) return st;
+        st = check_pairs(slot, topk_weights, grad_weights);
+        if (st) return st;
+    }
+    if (counts && num_rows > 0) {
+        st = from_hip(ep::launch_clear_rows(dtype, counts, offsets, num_experts, grad_rows,
+                                            ld_grad_rows, num_rows, hidden, s),
+                      "ep_unpermute_backward launch (clear)");
+        if (st) return st;
+    }
+    const bool dots = grad_weights != nullptr && num_rows > 0;
+    const ep::MoveArgs a = {false, grad_out, ld_grad_out, dots ? rows : nullptr, dots ? ld_rows : 0,
+                            num_rows > 0 ? grad_rows : nullptr, num_rows > 0 ? ld_grad_rows : 0,
+                            num_tokens, num_rows, hidden, num_topk, slot, topk_weights, grad_weights};
+    return from_hip(ep::launch_move_rows(dtype, a, s), "ep_unpermute_backward launch");
+}
+
+static ep_status_t check_w4(int num_experts, int out_features, int in_features, int group_size,
+                            int gated)
+{
+    if (num_experts < 1 || num_experts > EP_MAX_EXPERTS)
+        return fail(EP_INVALID_ARGUMENT, "num_experts %d outside [1, %d]", num_experts, EP_MAX_EXPERTS);
+    if (out_features < 1 || out_features > EP_MAX_W4_ROWS || (gated && out_features % 2 != 0))
+        return fail(EP_INVALID_ARGUMENT, "out_features %d outside [1, %d], or odd and gated",
+                    out_features, EP_MAX_W4_ROWS);
+    if (in_features < 32 || in_features > EP_MAX_HIDDEN || in_features % 32 != 0)
+        return fail(EP_INVALID_ARGUMENT, "in_features %d must be a positive multiple of 32, at most %d",
+                    in_features, EP_MAX_HIDDEN);
+    if (group_size != 32 && group_size != 64 && (group_size < 128 || group_size % 128 != 0))
+        return fail(EP_INVALID_ARGUMENT, "group_size %d must be 32, 64 or a multiple of 128",
+                    group_size);
+    return EP_SUCCESS;
+}
+
+size_t ep_w4_packed_size(int num_experts, int out_features, int in_features, int group_size,
+                         int has_zeros, int gated)
+{
+    if (check_w4(num_experts, out_features, in_features, group_size, gated)) {
+        g_last_error[0] = '\0';
+        return 0;
+    }
+    return (size_t)ep::w4_shape(num_experts, out_features, in_features, group_size, has_zeros != 0,
+                                gated != 0).bytes;
+}
+
+ep_status_t ep_w4_pack(const void* codes, const void* scales, const void* zeros, int dtype,
+                       int num_experts, int out_features, int in_features, int group_size,
+                       int gated, void* packed, size_t packed_bytes, void* stream)
+{
+    g_last_error[0] = '\0';
+    ep_status_t st = check_dtype(dtype, false);
+    if (st) return st;
+    st = check_w4(num_experts, out_features, in_features, group_size, gated);
+    if (st) return st;
+    if (!codes || !scales || !packed)
+        return fail(EP_INVALID_ARGUMENT, "codes, scales and packed are required");
+    if (off_by(scales, 2) || off_by(packed, 256))
+        return fail(EP_INVALID_ARGUMENT, "scales must be 2-byte, packed 256-byte aligned");
+    const size_t need = ep_w4_packed_size(num_experts, out_features, in_features, group_size,
+                                          zeros != nullptr, gated);
+    if (packed_bytes < need)
+        return fail(EP_INVALID_ARGUMENT, "packed holds %zu bytes, needs %zu", packed_bytes, need);
+    if (need / 4 / 256 > (size_t)INT32_MAX)
+        return fail(EP_UNSUPPORTED, "the weights need more than 2^31 workgroups");
+    return from_hip(ep::launch_w4_pack(dtype, static_cast<const uint8_t*>(codes), scales,
+                                       static_cast<const uint8_t*>(zeros), num_experts, out_features,
+                                       in_features, group_size, gated != 0, packed,
+                                       static_cast<hipStream_t>(stream)),
+                    "ep_w4_pack launch");
+}
+
+ep_status_t ep_expert_matmul_w4(const void* x, int dtype, int64_t ld_x, int64_t num_x_rows,
+                                const int32_t* src, const void* packed, size_t packed_bytes,
+                                int num_experts, int out_features, int in_features, int group_size,
+                                int has_zeros, int gated, const int32_t* offsets,
+                                const int32_t* counts, int64_t num_rows, void* out, int64_t ld_out,
+                                void* stream)
+{
+    g_last_error[0] = '\0';
+    ep_status_t st = check_dtype(dtype, false);
+    if (st) return st;
+    st = check_w4(num_experts, out_features, in_features, group_size, gated);
+    if (st) return st;
+    if (num_rows < 0 || num_rows >= ((int64_t)1 << 31))
+        return fail(EP_INVALID_ARGUMENT, "num_rows %lld outside [0, 2^31)", (long long)num_rows);
+    if (!offsets && (num_experts != 1 || counts))
+        return fail(EP_INVALID_ARGUMENT, "offsets is required with more than one expert or counts");
+    if (num_rows == 0) return EP_SUCCESS;
+    st = check_matrix(x, ld_x, in_features, dtype, "x");
+    if (st) return st;
+    st = check_matrix(out, ld_out, gated ? out_features / 2 : out_features, dtype, "out");
+    if (st) return st;
+    if (num_x_rows < 1 || (!src && num_x_rows < num_rows))
+        return fail(EP_INVALID_ARGUMENT, "x has %lld rows for %lld rows of the product",
+                    (long long)num_x_rows, (long long)num_rows);
+    if (!packed || off_by(packed, 256))
+        return fail(EP_INVALID_ARGUMENT, "packed must be non-NULL and 256-byte aligned");
+    if (off_by(src, 4) || off_by(offsets, 4) || off_by(counts, 4))
+        return fail(EP_INVALID_ARGUMENT, "src, offsets and counts must be 4-byte aligned");
+    const size_t need = ep_w4_packed_size(num_experts, out_features, in_features, group_size,
+                                          has_zeros, gated);
+    if (packed_bytes < need)
+        return fail(EP_INVALID_ARGUMENT, "packed holds %zu bytes, needs %zu", packed_bytes, need);
+    const ep::W4Args a = {x, ld_x, num_x_rows, src, packed, num_experts, out_features, in_features,
+                          group_size, has_zeros != 0, gated != 0, offsets, counts, num_rows, out,
+                          ld_out};
+    if (ep::w4_max_blocks(a) > INT32_MAX)
+        return fail(EP_UNSUPPORTED, "the product needs more than 2^31 workgroups");
+    return from_hip(ep::launch_w4(dtype, a, static_cast<hipStream_t>(stream)),
+                    "ep_expert_matmul_w4 launch");
+}
+
 }  // extern "C"

@@ -1,0 +1,486 @@
+// ep_w4.hip -- the experts' products with 4-bit weights: for each row r of
+// expert e, out[r, n] = sum_k scale[e, n, k / G] * (code[e, n, k] -
+// zero[e, n, k / G]) * x[r, k], for few rows per expert, optionally with the
+// gated activation out = silu(gate) * up over the two halves of n.
+//
+// What bounds it: with few rows per expert every weight is used for a few
+// products only, so the time is that of streaming the chosen experts'
+// weights.  At half a byte per weight the vector unit has about 2.4
+// operations per weight while a weight arrives, too few to unpack, scale and
+// multiply-add each one; so the matrix cores take the products (a 16-row
+// tile costs the same for 1 and for 16 tokens) and the unpacking is kept
+// below one operation per weight:
+//
+//   * a code n enters the matrix core as the 16-bit float 16 + n, made by
+//     setting four mantissa bits under a constant exponent: one rotate and
+//     one and-or for two weights;
+//   * the 16 and the zero point leave again per group, by
+//     sum (16 + n) x - (16 + z) sum x, with sum x from the same matrix
+//     instruction on a row of ones.  Codes, 16 + n and ones are exact in 16
+//     bits and all sums are fp32; the subtraction costs at most 5 of fp32's
+//     24 bits, against 8 or 11 in the result;
+//   * the scale is applied once per group, to the fp32 sum.
+//
+// Layout of the packed weights (made once by ep_w4_pack): tiles of 16 rows
+// by 128 k, 1 KiB each, in the order a wavefront reads them: lane l holds 16
+// bytes, whose word i has the 8 codes k = 32 i + 8 (l / 16) .. + 7 of row
+// l % 16 -- the matrix instruction's operand once unpacked, and one group of
+// 32 a word index, so that groups of 32 and 64 also end between
+// instructions.  Tiles of one row block follow one another along k, so a
+// workgroup streams consecutive memory.  With the gated activation the row
+// blocks of the two halves alternate.  Scales and zero points are held per
+// row block as [group][16 rows].  Rows are padded to 16 (scale 0), k to 128
+// (the kernel takes x as 0 there).
+//
+// Split: a workgroup makes RT row blocks (16 RT outputs) for up to 16 CT
+// rows of one expert, its wavefronts take turns at the k tiles and are
+// joined through LDS in a fixed order: the few outputs of a single token
+// still fill the chip, x is read once per workgroup, and results do not
+// depend on timing.
+
+#include "ep_device.h"
+#include "ep_internal.h"
+#include "ep_types.h"
+
+namespace ep {
+namespace {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 fp16x8_t __attribute__((ext_vector_type(8)));
+
+// 16 + n as a 16-bit float: the code's place in the mantissa, the exponent
+// of 16, and the float 1.0 (twice each: two weights a word).
+template <typename T>
+struct Code;
+template <>
+struct Code<Bf16> {
+    static constexpr int kShift = 3;
+    static constexpr uint32_t kMask = 0x00780078u, kBase = 0x41804180u, kOnes = 0x3F803F80u;
+};
+template <>
+struct Code<Fp16> {
+    static constexpr int kShift = 6;
+    static constexpr uint32_t kMask = 0x03C003C0u, kBase = 0x4C004C00u, kOnes = 0x3C003C00u;
+};
+
+__device__ __forceinline__ f32x4_t mma(const uint4& a, const uint4& b, f32x4_t c, const Bf16*)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                   __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4_t mma(const uint4& a, const uint4& b, f32x4_t c, const Fp16*)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(fp16x8_t, a),
+                                                  __builtin_bit_cast(fp16x8_t, b), c, 0, 0, 0);
+}
+
+// Eight codes of a packed word as eight 16-bit floats 16 + n.
+template <typename T>
+__device__ __forceinline__ uint4 decode(uint32_t w)
+{
+    using C = Code<T>;
+    uint4 d;
+    d.x = (w & C::kMask) | C::kBase;
+    d.y = (__builtin_amdgcn_alignbit(w, w, 4) & C::kMask) | C::kBase;
+    d.z = (__builtin_amdgcn_alignbit(w, w, 8) & C::kMask) | C::kBase;
+    d.w = (__builtin_amdgcn_alignbit(w, w, 12) & C::kMask) | C::kBase;
+    return d;
+}
+
+template <typename T>
+__device__ __forceinline__ f32x4_t four(const uint2& s)
+{
+    f32x4_t f;
+    f.x = to_float(T{(uint16_t)(s.x & 0xFFFFu)});
+    f.y = to_float(T{(uint16_t)(s.x >> 16)});
+    f.z = to_float(T{(uint16_t)(s.y & 0xFFFFu)});
+    f.w = to_float(T{(uint16_t)(s.y >> 16)});
+    return f;
+}
+
+// The item-th (expert, block of TM rows) pair in expert order, found by a
+// whole wavefront: each lane counts the blocks of `per` consecutive experts.
+struct Item {
+    int expert, first, rows;
+};
+__device__ __forceinline__ Item find_item(const int32_t* offsets, const int32_t* counts, int E,
+                                          int num_rows, int TM, int item)
+{
+    const int lane = threadIdx.x & 63;
+    if (offsets == nullptr) {         // one expert, all rows
+        const int left = num_rows - item * TM;
+        return Item{0, item * TM, left < TM ? left : TM};
+    }
+    const int per = (E + 63) >> 6;
+    const int e0 = lane * per;
+    int blocks = 0;
+    for (int i = 0; i < per; ++i) {
+        const int e = e0 + i;
+        const int n = e >= E ? 0 : counts != nullptr ? counts[e] : offsets[e + 1] - offsets[e];
+        blocks += (n + TM - 1) / TM;
+    }
+    int upto = blocks;
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+        const int o = __shfl_up(upto, s, 64);
+        upto += lane >= s ? o : 0;
+    }
+    const uint64_t past = __ballot(upto > item);
+    if (past == 0) return Item{0, 0, 0};
+    int expert = 0, first = 0, rows = 0;
+    int before = upto - blocks;
+    for (int i = 0; i < per; ++i) {
+        const int e = e0 + i;
+        if (e < E) {
+            const int n = counts != nullptr ? counts[e] : offsets[e + 1] - offsets[e];
+            const int b = (n + TM - 1) / TM;
+            if (item >= before && item < before + b) {
+                const int skip = (item - before) * TM;
+                expert = e;
+                first = offsets[e] + skip;
+                rows = n - skip < TM ? n - skip : TM;
+            }
+            before += b;
+        }
+    }
+    const int at = __ffsll((unsigned long long)past) - 1;
+    Item it;
+    it.expert = __builtin_amdgcn_readlane(expert, at);
+    it.first = __builtin_amdgcn_readlane(first, at);
+    it.rows = __builtin_amdgcn_readlane(rows, at);
+    // never past the rows the caller gave, whatever the offsets say
+    if (it.first < 0 || it.first >= num_rows) it.rows = 0;
+    else if (it.rows > num_rows - it.first) it.rows = num_rows - it.first;
+    return it;
+}
+
+// GS: groups that end inside a 128-wide k tile (1 for groups of 128 and
+// more); RT row blocks and CT blocks of 16 rows per workgroup.
+template <typename T, int GS, bool ZEROS, bool GLU, int RT, int CT, int MAXT>
+__global__ __launch_bounds__(MAXT)
+void w4_kernel(const T* __restrict__ x, int64_t ldx, int64_t x_rows, const int32_t* __restrict__ src,
+               const uint4* __restrict__ weights, const uint2* __restrict__ scales,
+               const uint32_t* __restrict__ zeros, const int32_t* __restrict__ offsets,
+               const int32_t* __restrict__ counts, int E, int num_rows, int K, int half_n,
+               int row_blocks, int k_tiles, int groups, int tiles_per_group, int units,
+               T* __restrict__ out, int64_t ldo)
+{
+    extern __shared__ f32x4_t part[];       // [wave][2][CT][64]
+    const int unit = blockIdx.x % units;
+    const Item it = find_item(offsets, counts, E, num_rows, CT * 16, (int)(blockIdx.x / units));
+    if (it.rows <= 0) return;
+    const int lane = threadIdx.x & 63;
+    const int wave = threadIdx.x >> 6;
+    const int waves = blockDim.x >> 6;
+    const int col = lane & 15;              // row of x within a block of 16, row of a weight tile
+    const int quad = lane >> 4;
+
+    // rows past the item's repeat its first row; their results are dropped
+    const T* xr[CT];
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+        const int in = c * 16 + col;
+        int64_t r = it.first + (in < it.rows ? in : 0);
+        if (src != nullptr) {
+            r = src[r];
+            if (r < 0 || r >= x_rows) r = 0;
+        }
+        xr[c] = x + r * ldx + quad * 8;
+    }
+
+    const int64_t block0 = (int64_t)it.expert * row_blocks + (int64_t)unit * RT;
+    int last = row_blocks - unit * RT - 1;  // the last unit may hold fewer row blocks
+    if (last > RT - 1) last = RT - 1;
+    const uint4* wp[RT];
+    const uint2* sp[RT];
+    const uint32_t* zp[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        const int64_t b = block0 + (r < last ? r : last);
+        wp[r] = weights + b * k_tiles * 64 + lane;
+        sp[r] = scales + b * groups * 4 + quad;
+        zp[r] = zeros + b * groups * 4 + quad;
+    }
+
+    f32x4_t acc[RT][CT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) acc[r][c] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    const uint4 ones = make_uint4(Code<T>::kOnes, Code<T>::kOnes, Code<T>::kOnes, Code<T>::kOnes);
+
+    uint4 next[RT];
+    if (wave < k_tiles) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) next[r] = wp[r][(int64_t)wave * 64];
+    }
+    for (int kt = wave; kt < k_tiles; kt += waves) {
+        uint4 cur[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) cur[r] = next[r];
+        const int kn = kt + waves < k_tiles ? kt + waves : kt;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) next[r] = wp[r][(int64_t)kn * 64];
+
+        uint4 xv[CT][4];
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = kt * 128 + i * 32;
+                // K is a multiple of 32: a step is inside or outside as a whole
+                xv[c][i] = k < K ? __builtin_bit_cast(uint4, (u32x4)*reinterpret_cast<
+                                       const typename Unaligned16<T>::type*>(xr[c] + k))
+                                 : make_uint4(0u, 0u, 0u, 0u);
+            }
+        const int g0 = GS > 1 ? kt * GS : kt / tiles_per_group;
+#pragma unroll
+        for (int g = 0; g < GS; ++g) {
+            f32x4_t sum[CT];
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                sum[c] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < 4 / GS; ++i)
+                    sum[c] = mma(ones, xv[c][g * (4 / GS) + i], sum[c], static_cast<const T*>(nullptr));
+            }
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const f32x4_t s = four<T>(sp[r][(int64_t)(g0 + g) * 4]);
+                f32x4_t off;
+                if constexpr (ZEROS) {
+                    const uint32_t z = zp[r][(int64_t)(g0 + g) * 4];
+                    off.x = 16.0f + (float)(z & 255u);
+                    off.y = 16.0f + (float)((z >> 8) & 255u);
+                    off.z = 16.0f + (float)((z >> 16) & 255u);
+                    off.w = 16.0f + (float)(z >> 24);
+                } else {
+                    off = f32x4_t{24.0f, 24.0f, 24.0f, 24.0f};
+                }
+                const uint32_t words[4] = {cur[r].x, cur[r].y, cur[r].z, cur[r].w};
+                f32x4_t d[CT];
+#pragma unroll
+                for (int c = 0; c < CT; ++c) d[c] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < 4 / GS; ++i) {
+                    const uint4 a = decode<T>(words[g * (4 / GS) + i]);
+#pragma unroll
+                    for (int c = 0; c < CT; ++c)
+                        d[c] = mma(a, xv[c][g * (4 / GS) + i], d[c], static_cast<const T*>(nullptr));
+                }
+#pragma unroll
+                for (int c = 0; c < CT; ++c) {
+                    const float sx = sum[c].x;
+                    acc[r][c].x = __builtin_fmaf(s.x, __builtin_fmaf(-off.x, sx, d[c].x), acc[r][c].x);
+                    acc[r][c].y = __builtin_fmaf(s.y, __builtin_fmaf(-off.y, sx, d[c].y), acc[r][c].y);
+                    acc[r][c].z = __builtin_fmaf(s.z, __builtin_fmaf(-off.z, sx, d[c].z), acc[r][c].z);
+                    acc[r][c].w = __builtin_fmaf(s.w, __builtin_fmaf(-off.w, sx, d[c].w), acc[r][c].w);
+                }
+            }
+        }
+    }
+
+    // join the wavefronts, two row blocks at a time, and store
+    constexpr int kJoin = RT < 2 ? 1 : 2;
+#pragma unroll
+    for (int r0 = 0; r0 < RT; r0 += kJoin) {
+        if (r0 > 0) __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kJoin; ++j)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) part[((wave * kJoin + j) * CT + c) * 64 + lane] = acc[r0 + j][c];
+        __syncthreads();
+        constexpr int kOut = GLU ? 1 : kJoin;      // output blocks of this step
+        for (int o = threadIdx.x; o < kOut * CT * 64; o += blockDim.x) {
+            const int ol = o & 63;
+            const int c = (o >> 6) % CT;
+            const int j = (o >> 6) / CT;
+            f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f}, u = v;
+            for (int w = 0; w < waves; ++w) {
+                v += part[((w * kJoin + j) * CT + c) * 64 + ol];
+                if constexpr (GLU) u += part[((w * kJoin + 1) * CT + c) * 64 + ol];
+            }
+            float f[4] = {v.x, v.y, v.z, v.w};
+            if constexpr (GLU) {
+                const float up[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = f[i] / (1.0f + expf(-f[i])) * up[i];
+            }
+            const int blk = GLU ? (unit * RT + r0) / 2 : unit * RT + r0 + j;
+            const int n = blk * 16 + (ol >> 4) * 4;
+            const int in = c * 16 + (ol & 15);
+            if (in < it.rows && r0 + j <= last && n < half_n) {
+                T* p = out + (int64_t)(it.first + in) * ldo + n;
+                T q[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q[i] = from_float<T>(f[i]);
+                if (n + 4 <= half_n) {
+                    __builtin_memcpy(p, q, 8);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (n + i < half_n) p[i] = q[i];
+                }
+            }
+        }
+    }
+}
+
+// ---- packing, one thread per word of the tiles, then per scale
+
+__device__ __forceinline__ int row_of_block(int b, int i, int halves, int half_n)
+{
+    // row blocks of the halves alternate; -1 for a padded row
+    const int n = b / halves * 16 + i;
+    return n < half_n ? (b % halves) * half_n + n : -1;
+}
+
+__global__ __launch_bounds__(256)
+void w4_pack_codes_kernel(const uint8_t* __restrict__ codes, int N, int K, int halves, int half_n,
+                          int row_blocks, int k_tiles, int shift, int64_t words,
+                          uint32_t* __restrict__ out)
+{
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (at >= words) return;
+    const int i = (int)(at & 3), lane = (int)(at >> 2) & 63;
+    const int64_t tile = at >> 8;
+    const int kt = (int)(tile % k_tiles);
+    const int64_t eb = tile / k_tiles;
+    const int n = row_of_block((int)(eb % row_blocks), lane & 15, halves, half_n);
+    const int k = kt * 128 + i * 32 + (lane >> 4) * 8;
+    uint32_t w = 0;
+    if (n >= 0 && k < K) {
+        const uint8_t* p = codes + ((eb / row_blocks * N + n) * (int64_t)K + k) / 2;
+        uint32_t c;
+        __builtin_memcpy(&c, p, 4);
+        // even codes to the low half, odd ones to the high half, then turned
+        // so that the first pair lies in the mantissas
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            w |= ((c >> (8 * q)) & 15u) << (4 * q);
+            w |= ((c >> (8 * q + 4)) & 15u) << (16 + 4 * q);
+        }
+        w = (w << shift) | (w >> (32 - shift));
+    }
+    out[at] = w;
+}
+
+__global__ __launch_bounds__(256)
+void w4_pack_scales_kernel(const uint16_t* __restrict__ scales, const uint8_t* __restrict__ zeros,
+                           int N, int in_groups, int groups, int halves, int half_n, int row_blocks,
+                           int64_t total, uint16_t* __restrict__ out_s, uint8_t* __restrict__ out_z)
+{
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (at >= total) return;
+    const int64_t bg = at >> 4;
+    const int g = (int)(bg % groups);
+    const int64_t eb = bg / groups;
+    const int n = row_of_block((int)(eb % row_blocks), (int)(at & 15), halves, half_n);
+    const bool in = n >= 0 && g < in_groups;
+    const int64_t from = (eb / row_blocks * N + n) * (int64_t)in_groups + g;
+    out_s[at] = in ? scales[from] : (uint16_t)0;
+    if (out_z != nullptr) out_z[at] = in && zeros != nullptr ? zeros[from] : (uint8_t)0;
+}
+
+}  // namespace
+
+W4Shape w4_shape(int num_experts, int n, int k, int group, bool zeros, bool glu)
+{
+    W4Shape s;
+    s.halves = glu ? 2 : 1;
+    s.half_n = n / s.halves;
+    s.row_blocks = (s.half_n + 15) / 16 * s.halves;
+    s.k_tiles = (k + 127) / 128;
+    s.groups = group >= 128 ? (k + group - 1) / group : s.k_tiles * (128 / group);
+    const int64_t blocks = (int64_t)num_experts * s.row_blocks;
+    s.scales_at = blocks * s.k_tiles * 1024;
+    s.zeros_at = (s.scales_at + blocks * s.groups * 32 + 255) / 256 * 256;
+    s.bytes = zeros ? (s.zeros_at + blocks * s.groups * 16 + 255) / 256 * 256 : s.zeros_at;
+    return s;
+}
+
+hipError_t launch_w4_pack(int dtype, const uint8_t* codes, const void* scales, const uint8_t* zeros,
+                          int num_experts, int n, int k, int group, bool glu, void* packed,
+                          hipStream_t stream)
+{
+    const W4Shape s = w4_shape(num_experts, n, k, group, zeros != nullptr, glu);
+    char* base = static_cast<char*>(packed);
+    const int64_t words = s.scales_at / 4;
+    hipLaunchKernelGGL(w4_pack_codes_kernel, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, stream,
+                       codes, n, k, s.halves, s.half_n, s.row_blocks, s.k_tiles,
+                       dtype == 0 ? Code<Bf16>::kShift : Code<Fp16>::kShift, words,
+                       reinterpret_cast<uint32_t*>(base));
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    const int64_t total = (int64_t)num_experts * s.row_blocks * s.groups * 16;
+    hipLaunchKernelGGL(w4_pack_scales_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, stream,
+                       static_cast<const uint16_t*>(scales), zeros, n, (k + group - 1) / group, s.groups,
+                       s.halves, s.half_n, s.row_blocks, total,
+                       reinterpret_cast<uint16_t*>(base + s.scales_at),
+                       zeros != nullptr ? reinterpret_cast<uint8_t*>(base + s.zeros_at) : nullptr);
+    return hipGetLastError();
+}
+
+namespace {
+
+template <typename T, int GS, bool ZEROS, bool GLU, int RT, int CT, int MAXT>
+hipError_t w4_launch(const W4Args& a, const W4Shape& s, int64_t items, int waves, hipStream_t stream)
+{
+    const int units = (s.row_blocks + RT - 1) / RT;
+    const char* base = static_cast<const char*>(a.packed);
+    const size_t lds = (size_t)waves * (RT < 2 ? 1 : 2) * CT * 1024;
+    hipLaunchKernelGGL((w4_kernel<T, GS, ZEROS, GLU, RT, CT, MAXT>), dim3((unsigned)(items * units)),
+                       dim3(waves * 64), lds, stream, static_cast<const T*>(a.x), a.ld_x, a.x_rows,
+                       a.src, reinterpret_cast<const uint4*>(base),
+                       reinterpret_cast<const uint2*>(base + s.scales_at),
+                       reinterpret_cast<const uint32_t*>(base + s.zeros_at), a.offsets, a.counts,
+                       a.num_experts, (int)a.num_rows, a.k, s.half_n, s.row_blocks, s.k_tiles, s.groups,
+                       a.group >= 128 ? a.group / 128 : 1, units, static_cast<T*>(a.out), a.ld_out);
+    return hipGetLastError();
+}
+
+template <typename T, int GS, bool ZEROS, bool GLU>
+hipError_t w4_sized(const W4Args& a, const W4Shape& s, hipStream_t stream)
+{
+    // blocks of rows: at most one per expert holding rows, and one more for
+    // every full block
+    const int64_t hold = a.num_rows < a.num_experts ? a.num_rows : a.num_experts;
+    const int64_t mean = a.num_rows / hold;
+    auto items = [&](int tm) { return hold + a.num_rows / tm; };
+    if (mean <= 16) return w4_launch<T, GS, ZEROS, GLU, 2, 1, 256>(a, s, items(16), 4, stream);
+    return w4_launch<T, GS, ZEROS, GLU, 4, 4, 256>(a, s, items(64), 4, stream);
+}
+
+template <typename T, int GS>
+hipError_t w4_typed(const W4Args& a, const W4Shape& s, hipStream_t stream)
+{
+    if (a.zeros) return a.glu ? w4_sized<T, GS, true, true>(a, s, stream) : w4_sized<T, GS, true, false>(a, s, stream);
+    return a.glu ? w4_sized<T, GS, false, true>(a, s, stream) : w4_sized<T, GS, false, false>(a, s, stream);
+}
+
+template <typename T>
+hipError_t w4_grouped(const W4Args& a, const W4Shape& s, hipStream_t stream)
+{
+    if (a.group == 32) return w4_typed<T, 4>(a, s, stream);
+    if (a.group == 64) return w4_typed<T, 2>(a, s, stream);
+    return w4_typed<T, 1>(a, s, stream);
+}
+
+}  // namespace
+
+// Workgroups of the smallest tiles: what the grid has to hold at most.
+int64_t w4_max_blocks(const W4Args& a)
+{
+    const W4Shape s = w4_shape(a.num_experts, a.n, a.k, a.group, a.zeros, a.glu);
+    const int64_t hold = a.num_rows < a.num_experts ? a.num_rows : a.num_experts;
+    return (hold + a.num_rows / 16) * ((s.row_blocks + 1) / 2);
+}
+
+hipError_t launch_w4(int dtype, const W4Args& a, hipStream_t stream)
+{
+    if (a.num_rows == 0) return hipSuccess;
+    const W4Shape s = w4_shape(a.num_experts, a.n, a.k, a.group, a.zeros, a.glu);
+    return dtype == 0 ? w4_grouped<Bf16>(a, s, stream) : w4_grouped<Fp16>(a, s, stream);
+}
+
+}  // namespace ep

@@ -18,7 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -42,6 +42,10 @@ EP_MAX_TOPK = 64
 EP_MAX_HIDDEN = 65536
 EP_MAX_ALIGNMENT = 4096
 EP_MAX_RANKS = 64
+EP_MAX_GROUPS = 64
+EP_MAX_W4_ROWS = 1 << 20
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # ep_dtype_t
+_SCORES = {"softmax": 0, "sigmoid": 1}
 
 # every symbol include/ep.h declares
 SYMBOLS = ("ep_version", "ep_status_string", "ep_last_error", "ep_layout_workspace_size",
@@ -52,7 +56,9 @@ SYMBOLS = ("ep_version", "ep_status_string", "ep_last_error", "ep_layout_workspa
            "ep_dispatch_ranked_prequantized", "ep_dispatch_ranked_fp8", "ep_dispatch_fused_permute",
            "ep_dispatch_fused_permute_prequantized", "ep_combine_ranked",
            "ep_dispatch_ranked_backward", "ep_dispatch_colmajor_workspace_size",
-           "ep_dispatch_colmajor_scales", "ep_dispatch_prequantized_colmajor")
+           "ep_dispatch_colmajor_scales", "ep_dispatch_prequantized_colmajor",
+           "ep_router", "ep_router_backward", "ep_permute", "ep_permute_backward", "ep_unpermute",
+           "ep_unpermute_backward", "ep_w4_packed_size", "ep_w4_pack", "ep_expert_matmul_w4")
 
 
 class EpError(RuntimeError):
@@ -134,6 +140,29 @@ def lib() -> ctypes.CDLL:
         L.ep_dispatch_ranked_backward.argtypes = [P, P, i64, P, P, i64, i32, i32, i32, i32, P, P,
                                                   P]
         L.ep_dispatch_ranked_backward.restype = i32
+        f32 = ctypes.c_float
+        L.ep_router.argtypes = [P, i32, i64, i32, i64, i32, i32, P, i32, i32, i32, i32, f32, P, P,
+                                P, P]
+        L.ep_router.restype = i32
+        L.ep_router_backward.argtypes = [P, i32, i64, i32, i64, i32, i32, i32, f32, P, P, P, P, P]
+        L.ep_router_backward.restype = i32
+        L.ep_permute.argtypes = [P, i32, i64, i32, i64, i32, P, P, P, i64, i64, P, P, i32, P]
+        L.ep_permute.restype = i32
+        L.ep_permute_backward.argtypes = [P, i32, i64, i32, i64, i64, i32, P, P, P, i64, P, i64, P,
+                                          P]
+        L.ep_permute_backward.restype = i32
+        L.ep_unpermute.argtypes = [P, i32, i64, i32, i64, i64, i32, P, P, P, i64, P]
+        L.ep_unpermute.restype = i32
+        L.ep_unpermute_backward.argtypes = [P, i32, i64, i32, i64, i32, P, P, P, i64, P, i64, i64,
+                                            P, P, P, i32, P]
+        L.ep_unpermute_backward.restype = i32
+        L.ep_w4_packed_size.argtypes = [i32, i32, i32, i32, i32, i32]
+        L.ep_w4_packed_size.restype = sz
+        L.ep_w4_pack.argtypes = [P, P, P, i32, i32, i32, i32, i32, i32, P, sz, P]
+        L.ep_w4_pack.restype = i32
+        L.ep_expert_matmul_w4.argtypes = [P, i32, i64, i64, P, P, sz, i32, i32, i32, i32, i32, i32,
+                                          P, P, i64, P, i64, P]
+        L.ep_expert_matmul_w4.restype = i32
         _lib = L
     return _lib
 
@@ -1016,6 +1045,379 @@ def ep_dispatch_ranked_backward(sparse_to_dense: torch.Tensor, num_experts: int,
     _check(st, "ep_dispatch_ranked_backward")
     return (grad_x if xtab is not None else None,
             grad_topk_weights if wtab is not None else None)
+
+
+# -------------------------------------- router, row movement, 4-bit products --
+# Outputs that are not given are allocated with torch on the stream of the
+# call; every tensor of a call lives on one device, which need not be the
+# current one.
+
+def _rows_of(t: torch.Tensor, name: str, dtype: Optional[torch.dtype] = None,
+             cols: Optional[int] = None, device=None) -> int:
+    """The row stride of a 2-D device tensor whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} must be {dtype or 'bfloat16, float16 or float32'}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    n, h = t.shape
+    if cols is not None and h != cols:
+        raise ValueError(f"{name} must have {cols} columns, has {h}")
+    if n <= 1 and (h <= 1 or t.stride(1) == 1):
+        return h
+    if (h > 1 and t.stride(1) != 1) or t.stride(0) < h:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap (strides "
+                         f"{tuple(t.stride())})")
+    return t.stride(0)
+
+
+def _need_on(t, name, dtype, device, numel=None):
+    _need(t, name, dtype, numel)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+class _On:
+    """The device and stream of a call: ``empty`` allocates for that stream,
+    ``call`` launches on it."""
+
+    __slots__ = ("device", "stream", "ctx")
+
+    def __init__(self, device, stream):
+        self.device = device
+        self.ctx = None
+        if stream is None:
+            self.stream = torch.cuda.current_stream(device).cuda_stream
+        else:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            self.stream = stream.cuda_stream
+            self.ctx = stream
+
+    def empty(self, shape, dtype):
+        if self.ctx is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.ctx):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def call(self, where, fn, *args):
+        if self.device.index == torch.cuda.current_device():
+            st = fn(*args, self.stream)
+        else:
+            with torch.cuda.device(self.device):
+                st = fn(*args, self.stream)
+        if st != EP_SUCCESS:
+            _check(st, where)
+
+
+def _score(score: str) -> int:
+    if score not in _SCORES:
+        raise ValueError(f"unknown score {score!r} (softmax or sigmoid)")
+    return _SCORES[score]
+
+
+def ep_router(logits: torch.Tensor, num_topk: int, *, score: str = "softmax",
+              bias: Optional[torch.Tensor] = None, num_groups: int = 1, topk_groups: int = 1,
+              group_top: int = 1, renormalize: bool = True, scale: float = 1.0,
+              topk_idx=None, topk_weights=None, probs=None, want_probs: bool = False, stream=None):
+    """Choose ``num_topk`` experts per token from ``logits`` (bf16 / fp16 /
+    fp32 [T, E], rows may be strided; -inf masks an expert).
+
+    ``score`` is "softmax" or "sigmoid"; ``bias`` (fp32 [E]) is added to the
+    scores for the choice only; with ``num_groups`` > 1 the choice is among
+    the ``topk_groups`` groups whose ``group_top`` (1 or 2) best values sum
+    highest.  Weights are the chosen scores, divided by their sum with
+    ``renormalize``, times ``scale``.
+
+    Returns (topk_idx int64 [T, k], -1 where no expert is left, topk_weights
+    fp32 [T, k], probs fp32 [T, E] or None).
+    """
+    ld = _rows_of(logits, "logits")
+    T, E = logits.shape
+    k = int(num_topk)
+    dev = logits.device
+    on = _On(dev, stream)
+    if k < 1:
+        raise ValueError("num_topk must be positive")
+    if topk_idx is None:
+        topk_idx = on.empty((T, k), torch.int64)
+    else:
+        _need_on(topk_idx, "topk_idx", torch.int64, dev, T * k)
+    if topk_weights is None:
+        topk_weights = on.empty((T, k), torch.float32)
+    else:
+        _need_on(topk_weights, "topk_weights", torch.float32, dev, T * k)
+    if probs is not None:
+        _need_on(probs, "probs", torch.float32, dev, T * E)
+    elif want_probs:
+        probs = on.empty((T, E), torch.float32)
+    if bias is not None:
+        _need_on(bias, "bias", torch.float32, dev, E)
+    on.call("ep_router", lib().ep_router, logits.data_ptr(), _DTYPES[logits.dtype], T, E, ld, k,
+            _score(score), _ptr(bias), int(num_groups), int(topk_groups), int(group_top),
+            int(bool(renormalize)), float(scale), topk_idx.data_ptr(), topk_weights.data_ptr(),
+            _ptr(probs))
+    return topk_idx, topk_weights, probs
+
+
+def ep_router_backward(logits: torch.Tensor, topk_idx: torch.Tensor, grad_weights: torch.Tensor,
+                       grad_probs: Optional[torch.Tensor] = None, *, score: str = "softmax",
+                       renormalize: bool = True, scale: float = 1.0, grad_logits=None, stream=None):
+    """Gradient of ep_router's weights (and probs) back to the logits, the
+    choice ``topk_idx`` held constant; ``score``, ``renormalize`` and ``scale``
+    as given to ep_router.  Returns grad_logits [T, E] in the logits' type."""
+    ld = _rows_of(logits, "logits")
+    T, E = logits.shape
+    dev = logits.device
+    _need_on(topk_idx, "topk_idx", torch.int64, dev)
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+        raise ValueError("topk_idx must be 2-D [num_tokens, num_topk]")
+    k = topk_idx.shape[1]
+    _need_on(grad_weights, "grad_weights", torch.float32, dev, T * k)
+    if grad_probs is not None:
+        _need_on(grad_probs, "grad_probs", torch.float32, dev, T * E)
+    on = _On(dev, stream)
+    if grad_logits is None:
+        grad_logits = on.empty((T, E), logits.dtype)
+    else:
+        _need_on(grad_logits, "grad_logits", logits.dtype, dev, T * E)
+    on.call("ep_router_backward", lib().ep_router_backward, logits.data_ptr(),
+            _DTYPES[logits.dtype], T, E, ld, k, _score(score), int(bool(renormalize)), float(scale),
+            topk_idx.data_ptr(), grad_weights.data_ptr(), _ptr(grad_probs), grad_logits.data_ptr())
+    return grad_logits
+
+
+def _pairs_of(slot, topk_weights, T, device):
+    _need_on(slot, "slot", torch.int32, device)
+    if slot.dim() != 2 or (T is not None and slot.shape[0] != T):
+        raise ValueError("slot must be 2-D [num_tokens, num_topk]")
+    if topk_weights is not None:
+        _need_on(topk_weights, "topk_weights", torch.float32, device, slot.numel())
+    return slot.shape
+
+
+def _clear_of(clear, device):
+    if clear is None:
+        return None, None, 0
+    counts, offsets = clear
+    _need_on(counts, "counts", torch.int32, device)
+    E = counts.numel()
+    _need_on(offsets, "offsets", torch.int32, device, E + 1)
+    return counts.data_ptr(), offsets.data_ptr(), E
+
+
+def ep_permute(x: torch.Tensor, slot: torch.Tensor, topk_weights: Optional[torch.Tensor] = None, *,
+               rows: Optional[int] = None, out=None, clear=None, stream=None):
+    """Rows sorted by expert: ``out[slot[t, j]] = topk_weights[t, j] * x[t]``
+    (unit weights without ``topk_weights``).  ``x`` is bf16 / fp16 / fp32
+    [T, H], of any width, rows may be strided.
+
+    ``rows`` (T*k by default) is the layout's row bound.  ``clear`` =
+    (counts, offsets) of the layout clears the rows that no slot names; else
+    they are not written.  Returns out [rows, H]."""
+    ld = _rows_of(x, "x")
+    T, H = x.shape
+    dev = x.device
+    _, k = _pairs_of(slot, topk_weights, T, dev)
+    on = _On(dev, stream)
+    if out is None:
+        out = on.empty((T * k if rows is None else int(rows), H), x.dtype)
+    ld_out = _rows_of(out, "out", x.dtype, H, dev)
+    if rows is not None and out.shape[0] < rows:
+        raise ValueError(f"out has {out.shape[0]} rows, needs {rows}")
+    R = out.shape[0]
+    c, o, E = _clear_of(clear, dev)
+    on.call("ep_permute", lib().ep_permute, x.data_ptr(), _DTYPES[x.dtype], T, H, ld, k,
+            slot.data_ptr(), _ptr(topk_weights), out.data_ptr(), ld_out, R, c, o, E)
+    return out
+
+
+def ep_permute_backward(grad_rows: torch.Tensor, slot: torch.Tensor,
+                        topk_weights: Optional[torch.Tensor] = None,
+                        x: Optional[torch.Tensor] = None, *, grad_x=None, grad_weights=None,
+                        stream=None):
+    """Backward of ep_permute: (grad_x [T, H], grad_weights fp32 [T, k]); the
+    latter None unless ``topk_weights`` and ``x`` are given."""
+    ld = _rows_of(grad_rows, "grad_rows")
+    R, H = grad_rows.shape
+    dev, dt = grad_rows.device, grad_rows.dtype
+    T, k = _pairs_of(slot, topk_weights, None, dev)
+    on = _On(dev, stream)
+    ld_x = 0
+    if topk_weights is None or x is None:
+        x = grad_weights = None
+    else:
+        ld_x = _rows_of(x, "x", dt, H, dev)
+        if x.shape[0] != T:
+            raise ValueError(f"x has {x.shape[0]} rows, slot {T}")
+        if grad_weights is None:
+            grad_weights = on.empty((T, k), torch.float32)
+        else:
+            _need_on(grad_weights, "grad_weights", torch.float32, dev, T * k)
+    if grad_x is None:
+        grad_x = on.empty((T, H), dt)
+    ld_gx = _rows_of(grad_x, "grad_x", dt, H, dev)
+    if grad_x.shape[0] != T:
+        raise ValueError(f"grad_x has {grad_x.shape[0]} rows, slot {T}")
+    on.call("ep_permute_backward", lib().ep_permute_backward, grad_rows.data_ptr(), _DTYPES[dt], T,
+            H, ld, R, k, slot.data_ptr(), _ptr(topk_weights), _ptr(x), ld_x, grad_x.data_ptr(),
+            ld_gx, _ptr(grad_weights))
+    return grad_x, grad_weights
+
+
+def ep_unpermute(y: torch.Tensor, slot: torch.Tensor, topk_weights: Optional[torch.Tensor] = None,
+                 *, out=None, stream=None):
+    """Rows back in token order: ``out[t] = sum_j topk_weights[t, j] *
+    y[slot[t, j]]``, in fp32, j ascending.  ``y`` is bf16 / fp16 / fp32
+    [rows, H], of any width, rows may be strided.  Returns out [T, H]."""
+    ld = _rows_of(y, "y")
+    R, H = y.shape
+    dev = y.device
+    T, k = _pairs_of(slot, topk_weights, None, dev)
+    on = _On(dev, stream)
+    if out is None:
+        out = on.empty((T, H), y.dtype)
+    ld_out = _rows_of(out, "out", y.dtype, H, dev)
+    if out.shape[0] != T:
+        raise ValueError(f"out has {out.shape[0]} rows, slot {T}")
+    on.call("ep_unpermute", lib().ep_unpermute, y.data_ptr(), _DTYPES[y.dtype], T, H, ld, R, k,
+            slot.data_ptr(), _ptr(topk_weights), out.data_ptr(), ld_out)
+    return out
+
+
+def ep_unpermute_backward(grad_out: torch.Tensor, slot: torch.Tensor,
+                          topk_weights: Optional[torch.Tensor] = None,
+                          y: Optional[torch.Tensor] = None, *, rows: Optional[int] = None,
+                          grad_y=None, grad_weights=None, clear=None, stream=None):
+    """Backward of ep_unpermute: (grad_y [rows, H], grad_weights fp32 [T, k]);
+    the latter None unless ``topk_weights`` and ``y`` are given.  ``rows`` and
+    ``clear`` as in ep_permute (``rows`` is y's with ``y``)."""
+    ld = _rows_of(grad_out, "grad_out")
+    T, H = grad_out.shape
+    dev, dt = grad_out.device, grad_out.dtype
+    _, k = _pairs_of(slot, topk_weights, T, dev)
+    on = _On(dev, stream)
+    ld_y = 0
+    if y is not None and rows is None:
+        rows = y.shape[0]
+    if topk_weights is None or y is None:
+        y = grad_weights = None
+    else:
+        ld_y = _rows_of(y, "y", dt, H, dev)
+        if grad_weights is None:
+            grad_weights = on.empty((T, k), torch.float32)
+        else:
+            _need_on(grad_weights, "grad_weights", torch.float32, dev, T * k)
+    if grad_y is None:
+        grad_y = on.empty((T * k if rows is None else int(rows), H), dt)
+    ld_gy = _rows_of(grad_y, "grad_y", dt, H, dev)
+    R = grad_y.shape[0]
+    if rows is not None and R < rows:
+        raise ValueError(f"grad_y has {R} rows, needs {rows}")
+    if y is not None and y.shape[0] < R:
+        raise ValueError(f"y has {y.shape[0]} rows, grad_y {R}")
+    c, o, E = _clear_of(clear, dev)
+    on.call("ep_unpermute_backward", lib().ep_unpermute_backward, grad_out.data_ptr(), _DTYPES[dt],
+            T, H, ld, k, slot.data_ptr(), _ptr(topk_weights), _ptr(y), ld_y, grad_y.data_ptr(),
+            ld_gy, R, _ptr(grad_weights), c, o, E)
+    return grad_y, grad_weights
+
+
+class W4Weights(NamedTuple):
+    """4-bit expert weights as ep_w4_pack lays them out."""
+    packed: torch.Tensor
+    num_experts: int
+    out_features: int
+    in_features: int
+    group_size: int
+    dtype: torch.dtype
+    has_zeros: bool
+    gated: bool
+
+
+def ep_w4_packed_size(num_experts: int, out_features: int, in_features: int, group_size: int = 128,
+                      has_zeros: bool = False, gated: bool = False) -> int:
+    """Bytes of the packed weights (0 if the shape is invalid)."""
+    return int(lib().ep_w4_packed_size(int(num_experts), int(out_features), int(in_features),
+                                       int(group_size), int(bool(has_zeros)), int(bool(gated))))
+
+
+def ep_w4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Tensor] = None, *,
+               group_size: int = 128, gated: bool = False, packed=None, stream=None) -> W4Weights:
+    """Lay out 4-bit weights, once, for ep_expert_matmul_w4.
+
+    ``codes`` uint8 [E, N, K/2] (the even input's code in the low four bits),
+    ``scales`` bf16 or fp16 [E, N, ceil(K / group_size)], ``zeros`` uint8 of
+    the scales' shape, or None: 8 everywhere.  ``gated``: the N rows are two
+    halves, gate then up."""
+    _need(codes, "codes", torch.uint8)
+    if codes.dim() != 3:
+        raise ValueError("codes must be 3-D [num_experts, out_features, in_features / 2]")
+    E, N, K = codes.shape[0], codes.shape[1], codes.shape[2] * 2
+    dev = codes.device
+    if scales.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"scales must be bfloat16 or float16, got {scales.dtype}")
+    need = ep_w4_packed_size(E, N, K, group_size, zeros is not None, gated)
+    if need == 0:
+        raise ValueError(f"invalid 4-bit weights: {E} x {N} x {K}, groups of {group_size}, "
+                         f"gated={gated}")
+    shape = (E, N, (K + group_size - 1) // group_size)
+    for t, name, dt in ((scales, "scales", scales.dtype), (zeros, "zeros", torch.uint8)):
+        if t is not None:
+            _need_on(t, name, dt, dev)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be {shape}, is {tuple(t.shape)}")
+    on = _On(dev, stream)
+    if packed is None:
+        packed = on.empty(need, torch.uint8)
+    else:
+        _need_on(packed, "packed", torch.uint8, dev, need)
+    on.call("ep_w4_pack", lib().ep_w4_pack, codes.data_ptr(), scales.data_ptr(), _ptr(zeros),
+            _DTYPES[scales.dtype], E, N, K, int(group_size), int(bool(gated)), packed.data_ptr(),
+            packed.numel())
+    return W4Weights(packed, E, N, K, int(group_size), scales.dtype, zeros is not None, bool(gated))
+
+
+def ep_expert_matmul_w4(x: torch.Tensor, weights: W4Weights, offsets: Optional[torch.Tensor] = None,
+                        *, src: Optional[torch.Tensor] = None, counts=None,
+                        rows: Optional[int] = None, out=None, stream=None):
+    """The experts' products with 4-bit weights: row r of expert e (rows
+    ``offsets[e]`` to ``offsets[e+1]``, or ``counts[e]`` of them) gives
+    ``out[r] = W[e] @ x[r]``, or ``W[e] @ x[src[r]]`` with ``src`` (the
+    layout's), or silu(gate) * up of its two halves for gated weights.
+
+    ``x`` has the scales' type and may have strided rows; ``offsets`` may be
+    left out with one expert.  ``rows`` is the layout's row bound (src's
+    length, or x's rows).  Returns out [rows, N] (N/2 if gated); rows of no
+    expert are not written."""
+    w = weights
+    ld = _rows_of(x, "x", w.dtype, w.in_features)
+    dev = x.device
+    _need_on(w.packed, "weights.packed", torch.uint8, dev)
+    if src is not None:
+        _need_on(src, "src", torch.int32, dev, rows)
+    R = int(rows) if rows is not None else (src.numel() if src is not None else x.shape[0])
+    if offsets is not None:
+        _need_on(offsets, "offsets", torch.int32, dev, w.num_experts + 1)
+    if counts is not None:
+        _need_on(counts, "counts", torch.int32, dev, w.num_experts)
+    on = _On(dev, stream)
+    n = w.out_features // 2 if w.gated else w.out_features
+    if out is None:
+        out = on.empty((R, n), w.dtype)
+    ld_out = _rows_of(out, "out", w.dtype, n, dev)
+    if out.shape[0] < R:
+        raise ValueError(f"out has {out.shape[0]} rows, needs {R}")
+    on.call("ep_expert_matmul_w4", lib().ep_expert_matmul_w4, x.data_ptr(), _DTYPES[w.dtype], ld,
+            x.shape[0], _ptr(src), w.packed.data_ptr(), w.packed.numel(), w.num_experts,
+            w.out_features, w.in_features, w.group_size, int(w.has_zeros), int(w.gated),
+            _ptr(offsets), _ptr(counts), R, out.data_ptr(), ld_out)
+    return out
 
 
 # ------------------------------------------------------ C-ABI names, 1:1 --

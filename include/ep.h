@@ -21,6 +21,11 @@
  * permutes, ep_combine_ranked, ep_dispatch_ranked_backward), each declared
  * below with the passage it follows.
  *
+ * Next to them, the layer that they serve: ep_router (the choice of experts)
+ * and its gradient; ep_permute / ep_unpermute (rows of any type, width and
+ * stride, weights on either way) and theirs; ep_expert_matmul_w4 (the
+ * experts' products with 4-bit weights, for few rows per expert).
+ *
  * The operations follow the pages' problem statement:
  *   - NCCL EP (nccl_ep.cc): ncclEpCreateHandle (topk_idx is a 2-D int64
  *     tensor; "Step 3" metadata preprocessing gives per-expert counts),
@@ -738,6 +743,169 @@ ep_status_t ep_dispatch_ranked_backward(const void *const *grad_recv_x,
                                         int64_t num_tokens, int hidden, int num_topk,
                                         int num_experts, int num_ranks, void *grad_x,
                                         float *grad_topk_weights, void *stream);
+
+/* ---- router, general row movement and 4-bit expert products ------------ */
+
+typedef enum {
+    EP_BF16 = 0,
+    EP_FP16 = 1,
+    EP_FP32 = 2
+} ep_dtype_t;
+
+typedef enum {
+    EP_SCORE_SOFTMAX = 0, /* softmax of a token's logits over all experts */
+    EP_SCORE_SIGMOID = 1  /* 1 / (1 + exp(-logit)) of each logit          */
+} ep_score_t;
+
+#define EP_MAX_GROUPS 64        /* expert groups of ep_router              */
+#define EP_MAX_W4_ROWS (1 << 20) /* out_features of the 4-bit weights      */
+
+/*
+ * ep_router -- the choice of experts that topk_idx and topk_weights of the
+ * calls above come from: scores, the num_topk best experts, their weights.
+ *
+ *   score_e = softmax or sigmoid of the logits;  value_e = score_e + bias_e
+ *   The experts form num_groups groups of num_experts / num_groups
+ *   consecutive ones.  A group is rated by the sum of its group_top (1 or 2)
+ *   best values, and only experts of the topk_groups best groups (ties to
+ *   the lower group) can be chosen.
+ *   The num_topk best values are chosen, best first, ties to the lowest
+ *   expert.  Without a bias experts are compared by logit (the score's
+ *   order).  Values that steer the choice are computed in 64 bits.
+ *   weight_j = scale * score_j, over the sum of the chosen scores if
+ *   renormalize (0 if that sum is 0).
+ *
+ * A logit of -inf or NaN, or a bias making the value -inf or NaN, takes the
+ * expert out: it is not chosen; its score is 0 (masked logits).  Where fewer
+ * than num_topk experts are left, the rest of the row is -1 with weight 0.
+ * A logit of +inf gives NaN softmax scores, as the formula does.
+ *
+ * In:  logits   dtype [num_tokens, num_experts], row stride ld_logits
+ *               elements, aligned to the element.
+ *      bias     fp32 [num_experts] or NULL; it has no part in the weights.
+ * Out: topk_idx     int64 [num_tokens, num_topk].
+ *      topk_weights fp32 [num_tokens, num_topk].
+ *      probs        fp32 [num_tokens, num_experts] or NULL: all scores
+ *                   (without bias and scale), 16-byte aligned.
+ * num_topk <= the experts of topk_groups groups.
+ */
+ep_status_t ep_router(const void *logits, int dtype, int64_t num_tokens, int num_experts,
+                      int64_t ld_logits, int num_topk, int score, const float *bias,
+                      int num_groups, int topk_groups, int group_top, int renormalize, float scale,
+                      int64_t *topk_idx, float *topk_weights, float *probs, void *stream);
+
+/*
+ * ep_router_backward -- gradient of topk_weights and probs back to the
+ * logits, the choice held constant.
+ *
+ * In:  logits, dtype, score, renormalize, scale  as given to ep_router.
+ *      topk_idx      from ep_router (-1 or out of range: no choice).
+ *      grad_weights  fp32 [num_tokens, num_topk].
+ *      grad_probs    fp32 [num_tokens, num_experts] or NULL.
+ * Out: grad_logits   dtype [num_tokens, num_experts], packed; every entry is
+ *                    written, 0 for masked logits.  May not overlap logits.
+ */
+ep_status_t ep_router_backward(const void *logits, int dtype, int64_t num_tokens, int num_experts,
+                               int64_t ld_logits, int num_topk, int score, int renormalize,
+                               float scale, const int64_t *topk_idx, const float *grad_weights,
+                               const float *grad_probs, void *grad_logits, void *stream);
+
+/*
+ * ep_permute / ep_unpermute -- token rows sorted by expert and back, by
+ * ep_layout's slots, with the weights on either way, and their gradients.
+ * They do what ep_dispatch and ep_combine do for packed bf16 rows, for rows
+ * of any type of ep_dtype_t, any width up to EP_MAX_HIDDEN and any row
+ * stride (ld_*, in elements, >= hidden); rows need only be aligned to their
+ * element.  Rows that start on 16 bytes and are whole 16-byte vectors move
+ * fastest.
+ *
+ *   ep_permute             rows[slot[t,j]] = w[t,j] * x[t]
+ *   ep_permute_backward    grad_x[t] = sum_j w[t,j] * grad_rows[slot[t,j]];
+ *                          grad_weights[t,j] = <x[t], grad_rows[slot[t,j]]>
+ *   ep_unpermute           out[t] = sum_j w[t,j] * rows[slot[t,j]]
+ *   ep_unpermute_backward  grad_rows[slot[t,j]] = w[t,j] * grad_out[t];
+ *                          grad_weights[t,j] = <grad_out[t], rows[slot[t,j]]>
+ *
+ * topk_weights is fp32 [num_tokens, num_topk], or NULL for unit weights.
+ * Products and sums are fp32, sums in increasing j, rounded once to dtype.
+ * grad_weights (fp32 [num_tokens, num_topk]) may be NULL, and then x or rows
+ * of the backward may be too.  A slot outside [0, num_rows) names no row: it
+ * is not read or written, and its weight gradient is 0.
+ *
+ * counts and offsets (of the layout with num_experts experts; both or
+ * neither): rows of the output that lie past their expert's count, or past
+ * the last segment, are cleared.  Without them rows that no slot names are
+ * not written.
+ */
+ep_status_t ep_permute(const void *x, int dtype, int64_t num_tokens, int hidden, int64_t ld_x,
+                       int num_topk, const int32_t *slot, const float *topk_weights, void *rows,
+                       int64_t ld_rows, int64_t num_rows, const int32_t *counts,
+                       const int32_t *offsets, int num_experts, void *stream);
+ep_status_t ep_permute_backward(const void *grad_rows, int dtype, int64_t num_tokens, int hidden,
+                                int64_t ld_grad_rows, int64_t num_rows, int num_topk,
+                                const int32_t *slot, const float *topk_weights, const void *x,
+                                int64_t ld_x, void *grad_x, int64_t ld_grad_x, float *grad_weights,
+                                void *stream);
+ep_status_t ep_unpermute(const void *rows, int dtype, int64_t num_tokens, int hidden,
+                         int64_t ld_rows, int64_t num_rows, int num_topk, const int32_t *slot,
+                         const float *topk_weights, void *out, int64_t ld_out, void *stream);
+ep_status_t ep_unpermute_backward(const void *grad_out, int dtype, int64_t num_tokens, int hidden,
+                                  int64_t ld_grad_out, int num_topk, const int32_t *slot,
+                                  const float *topk_weights, const void *rows, int64_t ld_rows,
+                                  void *grad_rows, int64_t ld_grad_rows, int64_t num_rows,
+                                  float *grad_weights, const int32_t *counts,
+                                  const int32_t *offsets, int num_experts, void *stream);
+
+/*
+ * ep_w4_pack -- lay the experts' 4-bit weights out for ep_expert_matmul_w4,
+ * once, when they are loaded.
+ *
+ * In:  codes   bytes [num_experts, out_features, in_features / 2], the even
+ *              input's code in the low four bits.
+ *      scales  dtype (EP_BF16 or EP_FP16) [num_experts, out_features,
+ *              ceil(in_features / group_size)].
+ *      zeros   bytes (0..15) of the scales' shape, or NULL: 8 everywhere.
+ *      weight[e, n, k] = scale[e, n, k / G] * (code[e, n, k] - zero[e, n, k / G])
+ *      gated   1: the rows are two halves, gate then up, and the product
+ *              gives silu(gate) * up (out_features even).
+ * Out: packed  ep_w4_packed_size(...) bytes, 256-byte aligned.
+ * in_features: a multiple of 32, at most EP_MAX_HIDDEN; group_size: 32, 64
+ * or a multiple of 128 (the last group may be shorter).
+ * ep_w4_packed_size is host arithmetic; 0 for an invalid shape.
+ */
+size_t ep_w4_packed_size(int num_experts, int out_features, int in_features, int group_size,
+                         int has_zeros, int gated);
+ep_status_t ep_w4_pack(const void *codes, const void *scales, const void *zeros, int dtype,
+                       int num_experts, int out_features, int in_features, int group_size,
+                       int gated, void *packed, size_t packed_bytes, void *stream);
+
+/*
+ * ep_expert_matmul_w4 -- out[r] = weight[e] x[r] for the rows r of each
+ * expert e, for few rows per expert (decoding, short prompts); one expert is
+ * a plain matrix-vector product.
+ *
+ * In:  x        dtype (the scales') rows of in_features, row stride ld_x,
+ *               num_x_rows of them, aligned to the element.
+ *      src      int32 [num_rows] or NULL: row r of the product is x[src[r]]
+ *               (ep_layout's src: the tokens need not be dispatched first),
+ *               else x[r].
+ *      offsets  int32 [num_experts + 1] of the layout, or NULL with one
+ *               expert (all rows).
+ *      counts   int32 [num_experts] or NULL: rows of each expert (for aligned
+ *               or fixed-stride layouts), else offsets[e + 1] - offsets[e].
+ * Out: out      dtype [num_rows, out_features], or out_features / 2 columns
+ *               if gated, row stride ld_out.  Rows that belong to no expert
+ *               are not written.
+ * Sums are fp32, in a fixed order; the result (after the gated activation,
+ * in fp32) is rounded once.  num_rows bounds every row: rows past it are
+ * neither read nor written; src outside [0, num_x_rows) reads row 0.
+ */
+ep_status_t ep_expert_matmul_w4(const void *x, int dtype, int64_t ld_x, int64_t num_x_rows,
+                                const int32_t *src, const void *packed, size_t packed_bytes,
+                                int num_experts, int out_features, int in_features, int group_size,
+                                int has_zeros, int gated, const int32_t *offsets,
+                                const int32_t *counts, int64_t num_rows, void *out, int64_t ld_out,
+                                void *stream);
 
 #ifdef __cplusplus
 }
