@@ -1,0 +1,239 @@
+"""ep_permute, ep_unpermute and their backwards against the 64-bit form."""
+
+import numpy as np
+import pytest
+import torch
+
+from combine_ep_layout_04_amd import ep
+from oracle import moe
+
+from moe_util import DEV, TINY, TYPES, U, check, f64, half_step, rounded, routing, wide
+
+pytestmark = pytest.mark.gpu
+
+CASES = [
+    # T, H, E, k, dtype, pad, shift, masked
+    (1, 1, 1, 1, "bf16", 0, 0, 0.0),
+    (3, 2, 4, 2, "fp32", 1, 1, 0.0),
+    (5, 7, 4, 3, "fp16", 0, 0, 0.2),
+    (9, 8, 8, 8, "bf16", 0, 0, 0.1),
+    (33, 63, 16, 2, "fp16", 2, 1, 0.0),
+    (20, 64, 16, 9, "bf16", 0, 0, 0.1),
+    (11, 65, 8, 5, "fp32", 0, 3, 0.3),
+    (17, 511, 32, 4, "bf16", 1, 1, 0.05),
+    (16, 512, 32, 4, "fp16", 8, 0, 0.05),
+    (12, 513, 8, 1, "fp32", 0, 0, 0.0),
+    (7, 1024, 8, 16, "bf16", 0, 0, 0.1),
+    (6, 1152, 8, 2, "fp16", 0, 0, 0.0),
+    (6, 1153, 8, 8, "fp16", 0, 0, 0.0),
+    (5, 2055, 64, 6, "fp32", 1, 0, 0.05),
+    (4, 2056, 64, 8, "bf16", 0, 8, 0.0),
+    (3, 7168, 256, 8, "bf16", 0, 0, 0.0),
+    (2, 9001, 4, 64, "fp16", 0, 5, 0.2),
+    (300, 40, 8, 4, "fp32", 0, 0, 0.05),
+]
+
+
+def setup(case, seed=1):
+    T, H, E, k, dtype, pad, shift, masked = case
+    rng = np.random.default_rng(seed)
+    idx = routing(rng, T, E, k, masked)
+    counts, offsets, slot, _, _ = ep.ep_layout(torch.from_numpy(idx).to(DEV), E)
+    x = torch.from_numpy(rng.normal(size=(T, H))).to(TYPES[dtype]).double().numpy()
+    y = torch.from_numpy(rng.normal(size=(T * k, H))).to(TYPES[dtype]).double().numpy()
+    w = rng.random((T, k)).astype(np.float32)
+    w[rng.random((T, k)) < 0.3] *= -1.0
+    return counts, offsets, slot, slot.cpu().numpy(), x, y, w
+
+
+@pytest.mark.parametrize("weighted", [True, False])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)))
+def test_forward(case, weighted):
+    T, H, E, k, dtype, pad, shift, masked = case
+    counts, offsets, slot, sl, x, y, w = setup(case)
+    tw = torch.from_numpy(w).to(DEV) if weighted else None
+    nw = w.astype(np.float64) if weighted else None
+    n = int(offsets[E])
+    # rows no slot names stay as they were, or are cleared
+    out = torch.full((T * k, H + pad), 7.0, dtype=TYPES[dtype], device=DEV)
+    got = ep.ep_permute(wide(x, dtype, pad, shift), slot, tw, out=out[:, :H])
+    assert got.data_ptr() == out.data_ptr()
+    ref = moe.permute(x, sl, nw, T * k)
+    if weighted:
+        check(got[:n], ref[:n], rounded(ref, np.abs(ref) * U, dtype)[:n], "permute")
+    else:
+        assert np.array_equal(f64(got[:n]), ref[:n])
+    assert bool((out[n:] == 7.0).all()) and bool((out[:, H:] == 7.0).all())
+    again = ep.ep_permute(wide(x, dtype, pad, shift), slot, tw, out=out[:, :H], clear=(counts, offsets))
+    assert bool((again[n:] == 0.0).all()) and bool((out[:, H:] == 7.0).all())
+    check(again[:n], ref[:n], rounded(ref, np.abs(ref) * U, dtype)[:n], "permute, cleared")
+
+    # rows that no slot names may hold anything
+    ty = wide(y, dtype, pad, shift)
+    ty[n:] = float("nan")
+    got = ep.ep_unpermute(ty, slot, tw)
+    ref = moe.unpermute(y, sl, nw)
+    size = moe.unpermute(np.abs(y), sl, None if nw is None else np.abs(nw))
+    check(got, ref, rounded(ref, size * (k + 1) * U, dtype), "unpermute")
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)))
+def test_backward(case):
+    T, H, E, k, dtype, pad, shift, masked = case
+    counts, offsets, slot, sl, x, y, w = setup(case, 2)
+    tw, nw = torch.from_numpy(w).to(DEV), w.astype(np.float64)
+    n = int(offsets[E])
+    tx, ty = wide(x, dtype, pad, shift), wide(y, dtype, pad, shift)
+    ty[n:] = float("nan")
+    dots, size = moe.pair_dots(x, y, sl)
+    # permute: grad_x is the weighted sum, grad_w the dot products
+    gx, gw = ep.ep_permute_backward(ty, slot, tw, tx)
+    ref = moe.unpermute(y, sl, nw)
+    sums = moe.unpermute(np.abs(y), sl, np.abs(nw))
+    check(gx, ref, rounded(ref, sums * (k + 1) * U, dtype), "grad_x")
+    check(gw, dots, size * (H + 8) * U + 2.0 ** -149, "grad_w of permute")
+    gx, none = ep.ep_permute_backward(ty, slot, tw)
+    assert none is None
+    check(gx, ref, rounded(ref, sums * (k + 1) * U, dtype), "grad_x alone")
+    # unpermute: grad_y is the weighted rows
+    gy, gw = ep.ep_unpermute_backward(tx, slot, tw, ty, clear=(counts, offsets))
+    ref = moe.permute(x, sl, nw, T * k)
+    check(gy, ref, rounded(ref, np.abs(ref) * U, dtype), "grad_y")
+    check(gw, dots, size * (H + 8) * U + 2.0 ** -149, "grad_w of unpermute")
+    gy, none = ep.ep_unpermute_backward(tx, slot, None, clear=(counts, offsets))
+    assert none is None
+    assert np.array_equal(f64(gy), moe.permute(x, sl, None, T * k))
+
+
+def test_same_result_every_time():
+    case = (64, 1000, 8, 6, "fp32", 0, 0, 0.1)
+    counts, offsets, slot, sl, x, y, w = setup(case)
+    tw, tx, ty = torch.from_numpy(w).to(DEV), wide(x, "fp32"), wide(y, "fp32")
+    first = ep.ep_permute_backward(ty, slot, tw, tx)
+    for _ in range(5):
+        again = ep.ep_permute_backward(ty, slot, tw, tx)
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+@pytest.mark.parametrize("alignment,capacity", [(1, 0), (16, 0), (128, 0), (1, 3), (8, 16)])
+def test_clear_in_padded_layouts(alignment, capacity):
+    T, H, E, k = 60, 24, 12, 4
+    rng = np.random.default_rng(4)
+    idx = torch.from_numpy(routing(rng, T, E, k, 0.1, skew=True)).to(DEV)
+    rows = ep.layout_max_rows(T, k, E, alignment, capacity)
+    counts, offsets, slot, _, _ = ep.ep_layout(idx, E, alignment=alignment, capacity=capacity)
+    x = torch.randn(T, H, device=DEV)
+    w = torch.rand(T, k, device=DEV)
+    out = torch.full((rows, H), float("nan"), device=DEV)
+    got = ep.ep_permute(x, slot, w, rows=rows, out=out, clear=(counts, offsets))
+    ref = moe.permute(f64(x), slot.cpu().numpy(), f64(w), rows)
+    check(got, ref, rounded(ref, np.abs(ref) * U, "fp32"), "aligned")
+    gy, _ = ep.ep_unpermute_backward(x, slot, w, rows=rows, clear=(counts, offsets))
+    check(gy, ref, rounded(ref, np.abs(ref) * U, "fp32"), "gradient, aligned")
+    back = ep.ep_unpermute(got, slot, w)
+    ref = moe.unpermute(f64(got), slot.cpu().numpy(), f64(w))
+    check(back, ref, rounded(ref, np.abs(ref) * (k + 1) * U * 4, "fp32"), "back")
+
+
+def test_slots_past_the_rows_name_no_row():
+    T, H, k = 6, 40, 3
+    x = torch.randn(T, H, device=DEV)
+    w = torch.rand(T, k, device=DEV)
+    slot = torch.arange(T * k, dtype=torch.int32, device=DEV).reshape(T, k)
+    out = torch.full((T * k, H), 5.0, device=DEV)
+    ep.ep_permute(x, slot, w, out=out[:10])
+    assert bool((out[10:] == 5.0).all())
+    y = torch.randn(10, H, device=DEV)
+    sl = slot.cpu().numpy()
+    ref = moe.unpermute(f64(y), sl, f64(w))
+    check(ep.ep_unpermute(y, slot, w), ref, rounded(ref, moe.unpermute(np.abs(f64(y)), sl, f64(w)) * 4 * U,
+                                                    "fp32"), "short rows")
+    _, gw = ep.ep_permute_backward(y, slot, w, x)
+    d, s = moe.pair_dots(f64(x), f64(y), sl)
+    check(gw, d, s * (H + 8) * U, "short rows, grad_w")
+
+
+def test_empty():
+    x = torch.randn(4, 16, device=DEV)
+    slot = torch.full((4, 2), -1, dtype=torch.int32, device=DEV)
+    w = torch.rand(4, 2, device=DEV)
+    none = torch.empty(0, 16, device=DEV)
+    assert ep.ep_permute(x, slot, w, rows=0).shape == (0, 16)
+    assert bool((ep.ep_unpermute(none, slot, w) == 0).all())
+    gx, gw = ep.ep_permute_backward(none, slot, w, x)
+    assert bool((gx == 0).all()) and bool((gw == 0).all())
+    gy, gw = ep.ep_unpermute_backward(x, slot, w, none)
+    assert gy.shape == (0, 16) and bool((gw == 0).all())
+    assert ep.ep_permute(x[:0], slot[:0], w[:0]).shape == (0, 16)
+    counts = torch.zeros(3, dtype=torch.int32, device=DEV)
+    offsets = torch.zeros(4, dtype=torch.int32, device=DEV)
+    out = ep.ep_permute(x[:0], slot[:0], rows=5, clear=(counts, offsets))
+    assert out.shape == (5, 16) and bool((out == 0).all())
+
+
+def test_infinities_and_overflow():
+    # an infinity or NaN in a row is that row's alone; fp16 overflows to inf
+    x = torch.ones(3, 20, device=DEV, dtype=torch.float16)
+    x[1, 4], x[1, 5] = float("inf"), float("nan")
+    x[2] = 60000.0
+    slot = torch.tensor([[0, -1], [2, -1], [1, 3]], dtype=torch.int32, device=DEV)
+    w = torch.tensor([[1.0, float("nan")], [2.0, float("inf")], [2.0, 0.5]], device=DEV)
+    rows = ep.ep_permute(x, slot, w)
+    assert bool((rows[0] == 1).all()) and rows[2, 4] == float("inf") and bool(torch.isnan(rows[2, 5]))
+    assert bool((rows[1] == float("inf")).all()) and bool((rows[3] == 30000).all())
+    back = ep.ep_unpermute(rows[:4], slot, w)
+    assert bool((back[0] == 1).all()) and bool((back[1, :4] == 4).all())
+    assert back[1, 4] == float("inf") and bool(torch.isnan(back[1, 5]))
+
+
+def test_rows_past_32_bits():
+    # 36000 rows of 65536 bf16: offsets past 2^31 elements
+    R, H, k = 36000, 65536, 2
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GiB free")
+    T = 4
+    x = torch.randn(T, H, device=DEV).bfloat16()
+    w = torch.rand(T, k, device=DEV)
+    slot = torch.tensor([[0, R - 1], [33000, -1], [R - 2, 5], [32768, 32767]], dtype=torch.int32,
+                        device=DEV)
+    rows = torch.zeros(R, H, dtype=torch.bfloat16, device=DEV)
+    ep.ep_permute(x, slot, w, out=rows)
+    sl = slot.cpu().numpy()
+    for t in range(T):
+        for j in range(k):
+            if sl[t, j] >= 0:
+                ref = f64(x[t]) * float(w[t, j])
+                check(rows[int(sl[t, j])], ref, rounded(ref, np.abs(ref) * U, "bf16"), f"row {sl[t, j]}")
+    assert int((rows.view(torch.int16) != 0).any(1).sum()) == 7
+    got = ep.ep_unpermute(rows, slot, w)
+    gx, gw = ep.ep_permute_backward(rows, slot, w, x)
+    assert torch.equal(got, gx)
+    for t in range(T):
+        r = [(f64(rows[int(s)]), float(w[t, j])) for j, s in enumerate(sl[t]) if s >= 0]
+        ref = sum(a * b for a, b in r)
+        check(got[t], ref, rounded(ref, sum(np.abs(a * b) for a, b in r) * 3 * U, "bf16"), "sum")
+
+
+def test_refuses():
+    x = torch.randn(4, 16, device=DEV)
+    slot = torch.zeros(4, 2, dtype=torch.int32, device=DEV)
+    with pytest.raises(TypeError, match="bfloat16"):
+        ep.ep_permute(x.double(), slot)
+    with pytest.raises(TypeError):
+        ep.ep_permute(x, slot.long())
+    with pytest.raises(ValueError, match="contiguous rows"):
+        ep.ep_permute(x.t(), slot)
+    with pytest.raises(ValueError, match="overlap"):
+        ep.ep_unpermute_backward(x[:1].expand(4, 16), slot)
+    with pytest.raises(ValueError, match="slot"):
+        ep.ep_permute(x[:3], slot)
+    with pytest.raises(TypeError):
+        ep.ep_permute(x, slot, torch.rand(4, 2, dtype=torch.float64, device=DEV))
+    with pytest.raises(ValueError, match="rows"):
+        ep.ep_permute(x, slot, rows=8, out=torch.empty(7, 16, device=DEV))
+    with pytest.raises(ValueError, match="columns"):
+        ep.ep_permute(x, slot, out=torch.empty(8, 15, device=DEV))
+    with pytest.raises(TypeError):
+        ep.ep_permute_backward(x, slot, torch.rand(4, 2, device=DEV), x.half())
+    with pytest.raises(ValueError, match="device tensor"):
+        ep.ep_unpermute(x, slot.cpu())
