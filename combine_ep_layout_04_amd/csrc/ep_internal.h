@@ -223,7 +223,7 @@ hipError_t launch_clear_rows(int dtype, const int32_t* counts, const int32_t* of
 
 // The packed 4-bit weights: sections and sizes.
 struct W4Shape {
-    int halves, half_n, row_blocks, k_tiles, groups;
+    int halves, half_n, row_blocks, k_tiles, tile_groups;
     int64_t scales_at, zeros_at, bytes;
 };
 W4Shape w4_shape(int num_experts, int n, int k, int group, bool zeros, bool glu);

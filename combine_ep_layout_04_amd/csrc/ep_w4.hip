@@ -29,8 +29,9 @@
 // instructions.  Tiles of one row block follow one another along k, so a
 // workgroup streams consecutive memory.  With the gated activation the row
 // blocks of the two halves alternate.  Scales and zero points are held per
-// row block as [group][16 rows].  Rows are padded to 16 (scale 0), k to 128
-// (the kernel takes x as 0 there).
+// tile, as the 4 rows of a lane's results for each group inside the tile (a
+// group of more than 128 repeats its scale: 32 bytes a tile).  Rows are
+// padded to 16 (scale 0), k to 128 (the kernels take x as 0 there).
 //
 // Split: a workgroup makes RT row blocks (16 RT outputs) for up to 16 CT
 // rows of one expert, its wavefronts take turns at the k tiles and are
@@ -74,17 +75,31 @@ __device__ __forceinline__ f32x4_t mma(const uint4& a, const uint4& b, f32x4_t c
                                                   __builtin_bit_cast(fp16x8_t, b), c, 0, 0, 0);
 }
 
-// Eight codes of a packed word as eight 16-bit floats 16 + n.
+// The two constants of the unpacking, in a scalar and a vector register: as
+// literals they would take an and and an or each, since the one instruction
+// that does both has no room for a literal.
 template <typename T>
-__device__ __forceinline__ uint4 decode(uint32_t w)
+struct Unpacker {
+    uint32_t mask, base;
+    __device__ __forceinline__ Unpacker()
+    {
+        asm("s_mov_b32 %0, %1" : "=s"(mask) : "i"(Code<T>::kMask));
+        asm("v_mov_b32 %0, %1" : "=v"(base) : "i"(Code<T>::kBase));
+    }
+    // Eight codes of a packed word as eight 16-bit floats 16 + n.
+    __device__ __forceinline__ uint4 operator()(uint32_t w) const
+    {
+        return make_uint4((w & mask) | base, (__builtin_amdgcn_alignbit(w, w, 4) & mask) | base,
+                          (__builtin_amdgcn_alignbit(w, w, 8) & mask) | base,
+                          (__builtin_amdgcn_alignbit(w, w, 12) & mask) | base);
+    }
+};
+
+// v / (1 + exp(-v)) by the hardware's exponential and reciprocal (one unit in
+// the last place each; rounding the exponent's argument adds |v| * 2^-24).
+__device__ __forceinline__ float silu(float v)
 {
-    using C = Code<T>;
-    uint4 d;
-    d.x = (w & C::kMask) | C::kBase;
-    d.y = (__builtin_amdgcn_alignbit(w, w, 4) & C::kMask) | C::kBase;
-    d.z = (__builtin_amdgcn_alignbit(w, w, 8) & C::kMask) | C::kBase;
-    d.w = (__builtin_amdgcn_alignbit(w, w, 12) & C::kMask) | C::kBase;
-    return d;
+    return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896f * v));
 }
 
 template <typename T>
@@ -98,8 +113,21 @@ __device__ __forceinline__ f32x4_t four(const uint2& s)
     return f;
 }
 
+// Inclusive sum over a wavefront's lanes, by lane moves in registers.
+__device__ __forceinline__ int wave_scan(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);      // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);     // lane 15 to the next row
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);     // lane 31 to the upper half
+    return v;
+}
+
 // The item-th (expert, block of TM rows) pair in expert order, found by a
-// whole wavefront: each lane counts the blocks of `per` consecutive experts.
+// whole wavefront, 256 experts at a time: a lane counts the blocks of four
+// experts (their loads go out together: what follows waits for them once).
 struct Item {
     int expert, first, rows;
 };
@@ -107,62 +135,79 @@ __device__ __forceinline__ Item find_item(const int32_t* offsets, const int32_t*
                                           int num_rows, int TM, int item)
 {
     const int lane = threadIdx.x & 63;
+    Item it = {0, 0, 0};
     if (offsets == nullptr) {         // one expert, all rows
-        const int left = num_rows - item * TM;
-        return Item{0, item * TM, left < TM ? left : TM};
+        it.first = item * TM;
+        it.rows = num_rows - it.first < TM ? num_rows - it.first : TM;
+        return it;
     }
-    const int per = (E + 63) >> 6;
-    const int e0 = lane * per;
-    int blocks = 0;
-    for (int i = 0; i < per; ++i) {
-        const int e = e0 + i;
-        const int n = e >= E ? 0 : counts != nullptr ? counts[e] : offsets[e + 1] - offsets[e];
-        blocks += (n + TM - 1) / TM;
-    }
-    int upto = blocks;
+    int done = 0;
+    for (int base = 0; base < E; base += 256) {
+        const int e0 = base + lane * 4;
+        int start[5], n[4], blocks[4];
 #pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-        const int o = __shfl_up(upto, s, 64);
-        upto += lane >= s ? o : 0;
-    }
-    const uint64_t past = __ballot(upto > item);
-    if (past == 0) return Item{0, 0, 0};
-    int expert = 0, first = 0, rows = 0;
-    int before = upto - blocks;
-    for (int i = 0; i < per; ++i) {
-        const int e = e0 + i;
-        if (e < E) {
-            const int n = counts != nullptr ? counts[e] : offsets[e + 1] - offsets[e];
-            const int b = (n + TM - 1) / TM;
-            if (item >= before && item < before + b) {
-                const int skip = (item - before) * TM;
-                expert = e;
-                first = offsets[e] + skip;
-                rows = n - skip < TM ? n - skip : TM;
-            }
-            before += b;
+        for (int i = 0; i < 5; ++i) start[i] = offsets[e0 + i < E ? e0 + i : E];
+        if (counts != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) n[i] = e0 + i < E ? counts[e0 + i] : 0;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) n[i] = start[i + 1] - start[i];
         }
+        int mine = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            blocks[i] = (n[i] + TM - 1) / TM;
+            mine += blocks[i];
+        }
+        const int upto = done + wave_scan(mine);
+        const uint64_t past = __ballot(upto > item);
+        if (past != 0) {
+            int before = upto - mine;
+            int expert = 0, first = 0, rows = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (item >= before && item < before + blocks[i]) {
+                    const int skip = (item - before) * TM;
+                    expert = e0 + i;
+                    first = start[i] + skip;
+                    rows = n[i] - skip < TM ? n[i] - skip : TM;
+                }
+                before += blocks[i];
+            }
+            const int at = __ffsll((unsigned long long)past) - 1;
+            it.expert = __builtin_amdgcn_readlane(expert, at);
+            it.first = __builtin_amdgcn_readlane(first, at);
+            it.rows = __builtin_amdgcn_readlane(rows, at);
+            break;
+        }
+        done = __builtin_amdgcn_readlane(upto, 63);
     }
-    const int at = __ffsll((unsigned long long)past) - 1;
-    Item it;
-    it.expert = __builtin_amdgcn_readlane(expert, at);
-    it.first = __builtin_amdgcn_readlane(first, at);
-    it.rows = __builtin_amdgcn_readlane(rows, at);
     // never past the rows the caller gave, whatever the offsets say
     if (it.first < 0 || it.first >= num_rows) it.rows = 0;
     else if (it.rows > num_rows - it.first) it.rows = num_rows - it.first;
     return it;
 }
 
+// What one k tile needs, in registers: weights, x, scales, zero points.
+template <int GS, int RT, int CT>
+struct Stage {
+    uint4 a[RT];
+    uint4 x[CT][4];
+    uint2 s[RT][GS];
+    uint32_t z[RT][GS];
+};
+
 // GS: groups that end inside a 128-wide k tile (1 for groups of 128 and
-// more); RT row blocks and CT blocks of 16 rows per workgroup.
-template <typename T, int GS, bool ZEROS, bool GLU, int RT, int CT, int MAXT>
-__global__ __launch_bounds__(MAXT)
+// more); RT row blocks and CT blocks of 16 rows per workgroup of at most
+// WAVES wavefronts.
+template <typename T, int GS, bool ZEROS, bool GLU, int RT, int CT, int WAVES>
+__global__ __launch_bounds__(WAVES * 64)
 void w4_kernel(const T* __restrict__ x, int64_t ldx, int64_t x_rows, const int32_t* __restrict__ src,
                const uint4* __restrict__ weights, const uint2* __restrict__ scales,
                const uint32_t* __restrict__ zeros, const int32_t* __restrict__ offsets,
                const int32_t* __restrict__ counts, int E, int num_rows, int K, int half_n,
-               int row_blocks, int k_tiles, int groups, int tiles_per_group, int units,
+               int row_blocks, int k_tiles, int units,
                T* __restrict__ out, int64_t ldo)
 {
     extern __shared__ f32x4_t part[];       // [wave][2][CT][64]
@@ -170,23 +215,10 @@ void w4_kernel(const T* __restrict__ x, int64_t ldx, int64_t x_rows, const int32
     const Item it = find_item(offsets, counts, E, num_rows, CT * 16, (int)(blockIdx.x / units));
     if (it.rows <= 0) return;
     const int lane = threadIdx.x & 63;
-    const int wave = threadIdx.x >> 6;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int waves = blockDim.x >> 6;
     const int col = lane & 15;              // row of x within a block of 16, row of a weight tile
     const int quad = lane >> 4;
-
-    // rows past the item's repeat its first row; their results are dropped
-    const T* xr[CT];
-#pragma unroll
-    for (int c = 0; c < CT; ++c) {
-        const int in = c * 16 + col;
-        int64_t r = it.first + (in < it.rows ? in : 0);
-        if (src != nullptr) {
-            r = src[r];
-            if (r < 0 || r >= x_rows) r = 0;
-        }
-        xr[c] = x + r * ldx + quad * 8;
-    }
 
     const int64_t block0 = (int64_t)it.expert * row_blocks + (int64_t)unit * RT;
     int last = row_blocks - unit * RT - 1;  // the last unit may hold fewer row blocks
@@ -197,11 +229,36 @@ void w4_kernel(const T* __restrict__ x, int64_t ldx, int64_t x_rows, const int32
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
         const int64_t b = block0 + (r < last ? r : last);
-        wp[r] = weights + b * k_tiles * 64 + lane;
-        sp[r] = scales + b * groups * 4 + quad;
-        zp[r] = zeros + b * groups * 4 + quad;
+        wp[r] = weights + b * k_tiles * 64;
+        sp[r] = scales + b * k_tiles * GS * 4;
+        zp[r] = zeros + b * k_tiles * GS * 4;
     }
 
+    using St = Stage<GS, RT, CT>;
+    const T* xr[CT];
+    auto load_weights = [&](St& st, int kt) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) st.a[r] = wp[r][kt * 64 + lane];
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int g = 0; g < GS; ++g) {
+                st.s[r][g] = sp[r][(kt * 4 + quad) * GS + g];
+                if constexpr (ZEROS) st.z[r][g] = zp[r][(kt * 4 + quad) * GS + g];
+            }
+    };
+    auto load_x = [&](St& st, int kt) {
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = kt * 128 + i * 32;    // k past K: read at 0, taken as 0 below
+                st.x[c][i] = __builtin_bit_cast(uint4, (u32x4)*reinterpret_cast<
+                                 const typename Unaligned16<T>::type*>(xr[c] + (k < K ? k : 0)));
+            }
+    };
+
+    const Unpacker<T> decode;
     f32x4_t acc[RT][CT];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
@@ -209,31 +266,15 @@ void w4_kernel(const T* __restrict__ x, int64_t ldx, int64_t x_rows, const int32
         for (int c = 0; c < CT; ++c) acc[r][c] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     const uint4 ones = make_uint4(Code<T>::kOnes, Code<T>::kOnes, Code<T>::kOnes, Code<T>::kOnes);
 
-    uint4 next[RT];
-    if (wave < k_tiles) {
+    auto compute = [&](St& st, int kt) {
+        if (kt * 128 + 128 > K) {                   // the last tile, K not a multiple of 128
 #pragma unroll
-        for (int r = 0; r < RT; ++r) next[r] = wp[r][(int64_t)wave * 64];
-    }
-    for (int kt = wave; kt < k_tiles; kt += waves) {
-        uint4 cur[RT];
+            for (int i = 1; i < 4; ++i)
+                if (kt * 128 + i * 32 >= K) {
 #pragma unroll
-        for (int r = 0; r < RT; ++r) cur[r] = next[r];
-        const int kn = kt + waves < k_tiles ? kt + waves : kt;
-#pragma unroll
-        for (int r = 0; r < RT; ++r) next[r] = wp[r][(int64_t)kn * 64];
-
-        uint4 xv[CT][4];
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k = kt * 128 + i * 32;
-                // K is a multiple of 32: a step is inside or outside as a whole
-                xv[c][i] = k < K ? __builtin_bit_cast(uint4, (u32x4)*reinterpret_cast<
-                                       const typename Unaligned16<T>::type*>(xr[c] + k))
-                                 : make_uint4(0u, 0u, 0u, 0u);
-            }
-        const int g0 = GS > 1 ? kt * GS : kt / tiles_per_group;
+                    for (int c = 0; c < CT; ++c) st.x[c][i] = make_uint4(0u, 0u, 0u, 0u);
+                }
+        }
 #pragma unroll
         for (int g = 0; g < GS; ++g) {
             f32x4_t sum[CT];
@@ -242,14 +283,14 @@ void w4_kernel(const T* __restrict__ x, int64_t ldx, int64_t x_rows, const int32
                 sum[c] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int i = 0; i < 4 / GS; ++i)
-                    sum[c] = mma(ones, xv[c][g * (4 / GS) + i], sum[c], static_cast<const T*>(nullptr));
+                    sum[c] = mma(ones, st.x[c][g * (4 / GS) + i], sum[c], static_cast<const T*>(nullptr));
             }
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-                const f32x4_t s = four<T>(sp[r][(int64_t)(g0 + g) * 4]);
+                const f32x4_t s = four<T>(st.s[r][g]);
                 f32x4_t off;
                 if constexpr (ZEROS) {
-                    const uint32_t z = zp[r][(int64_t)(g0 + g) * 4];
+                    const uint32_t z = st.z[r][g];
                     off.x = 16.0f + (float)(z & 255u);
                     off.y = 16.0f + (float)((z >> 8) & 255u);
                     off.z = 16.0f + (float)((z >> 16) & 255u);
@@ -257,16 +298,16 @@ void w4_kernel(const T* __restrict__ x, int64_t ldx, int64_t x_rows, const int32
                 } else {
                     off = f32x4_t{24.0f, 24.0f, 24.0f, 24.0f};
                 }
-                const uint32_t words[4] = {cur[r].x, cur[r].y, cur[r].z, cur[r].w};
+                const uint32_t words[4] = {st.a[r].x, st.a[r].y, st.a[r].z, st.a[r].w};
                 f32x4_t d[CT];
 #pragma unroll
                 for (int c = 0; c < CT; ++c) d[c] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int i = 0; i < 4 / GS; ++i) {
-                    const uint4 a = decode<T>(words[g * (4 / GS) + i]);
+                    const uint4 a = decode(words[g * (4 / GS) + i]);
 #pragma unroll
                     for (int c = 0; c < CT; ++c)
-                        d[c] = mma(a, xv[c][g * (4 / GS) + i], d[c], static_cast<const T*>(nullptr));
+                        d[c] = mma(a, st.x[c][g * (4 / GS) + i], d[c], static_cast<const T*>(nullptr));
                 }
 #pragma unroll
                 for (int c = 0; c < CT; ++c) {
@@ -277,6 +318,31 @@ void w4_kernel(const T* __restrict__ x, int64_t ldx, int64_t x_rows, const int32
                     acc[r][c].w = __builtin_fmaf(s.w, __builtin_fmaf(-off.w, sx, d[c].w), acc[r][c].w);
                 }
             }
+        }
+    };
+
+    // The weights' first loads go out before the rows of x are known.
+    // Rows past the item's repeat its first row; their results are dropped.
+    St st;
+    int kt = wave;
+    if (kt < k_tiles) load_weights(st, kt);
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+        const int in = c * 16 + col;
+        int64_t r = it.first + (in < it.rows ? in : 0);
+        if (src != nullptr) {
+            r = src[r];
+            if (r < 0 || r >= x_rows) r = 0;
+        }
+        xr[c] = x + r * ldx + quad * 8;
+    }
+    if (kt < k_tiles) load_x(st, kt);
+    while (kt < k_tiles) {
+        compute(st, kt);
+        kt += waves;
+        if (kt < k_tiles) {
+            load_weights(st, kt);
+            load_x(st, kt);
         }
     }
 
@@ -304,7 +370,7 @@ void w4_kernel(const T* __restrict__ x, int64_t ldx, int64_t x_rows, const int32
             if constexpr (GLU) {
                 const float up[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = f[i] / (1.0f + expf(-f[i])) * up[i];
+                for (int i = 0; i < 4; ++i) f[i] = silu(f[i]) * up[i];
             }
             const int blk = GLU ? (unit * RT + r0) / 2 : unit * RT + r0 + j;
             const int n = blk * 16 + (ol >> 4) * 4;
@@ -367,19 +433,27 @@ void w4_pack_codes_kernel(const uint8_t* __restrict__ codes, int N, int K, int h
 
 __global__ __launch_bounds__(256)
 void w4_pack_scales_kernel(const uint16_t* __restrict__ scales, const uint8_t* __restrict__ zeros,
-                           int N, int in_groups, int groups, int halves, int half_n, int row_blocks,
-                           int64_t total, uint16_t* __restrict__ out_s, uint8_t* __restrict__ out_z)
+                           int N, int K, int group, int in_groups, int gs, int halves, int half_n,
+                           int row_blocks, int k_tiles, int64_t total, uint16_t* __restrict__ out_s,
+                           uint8_t* __restrict__ out_z)
 {
+    // [expert][row block][k tile][4 quads][gs groups][4 rows]
     const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (at >= total) return;
-    const int64_t bg = at >> 4;
-    const int g = (int)(bg % groups);
-    const int64_t eb = bg / groups;
-    const int n = row_of_block((int)(eb % row_blocks), (int)(at & 15), halves, half_n);
-    const bool in = n >= 0 && g < in_groups;
-    const int64_t from = (eb / row_blocks * N + n) * (int64_t)in_groups + g;
+    const int i = (int)(at & 3);
+    int64_t rest = at >> 2;
+    const int g = (int)(rest % gs);
+    rest /= gs;
+    const int quad = (int)(rest & 3);
+    rest >>= 2;
+    const int kt = (int)(rest % k_tiles);
+    const int64_t eb = rest / k_tiles;
+    const int n = row_of_block((int)(eb % row_blocks), quad * 4 + i, halves, half_n);
+    const int k = kt * 128 + g * (128 / gs);
+    const bool in = n >= 0 && k < K;
+    const int64_t from = in ? (eb / row_blocks * N + n) * (int64_t)in_groups + k / group : 0;
     out_s[at] = in ? scales[from] : (uint16_t)0;
-    if (out_z != nullptr) out_z[at] = in && zeros != nullptr ? zeros[from] : (uint8_t)0;
+    if (out_z != nullptr) out_z[at] = in ? zeros[from] : (uint8_t)0;
 }
 
 }  // namespace
@@ -391,11 +465,11 @@ W4Shape w4_shape(int num_experts, int n, int k, int group, bool zeros, bool glu)
     s.half_n = n / s.halves;
     s.row_blocks = (s.half_n + 15) / 16 * s.halves;
     s.k_tiles = (k + 127) / 128;
-    s.groups = group >= 128 ? (k + group - 1) / group : s.k_tiles * (128 / group);
-    const int64_t blocks = (int64_t)num_experts * s.row_blocks;
-    s.scales_at = blocks * s.k_tiles * 1024;
-    s.zeros_at = (s.scales_at + blocks * s.groups * 32 + 255) / 256 * 256;
-    s.bytes = zeros ? (s.zeros_at + blocks * s.groups * 16 + 255) / 256 * 256 : s.zeros_at;
+    s.tile_groups = group >= 128 ? 1 : 128 / group;
+    const int64_t tiles = (int64_t)num_experts * s.row_blocks * s.k_tiles;
+    s.scales_at = tiles * 1024;
+    s.zeros_at = (s.scales_at + tiles * s.tile_groups * 32 + 255) / 256 * 256;
+    s.bytes = zeros ? (s.zeros_at + tiles * s.tile_groups * 16 + 255) / 256 * 256 : s.zeros_at;
     return s;
 }
 
@@ -412,10 +486,10 @@ hipError_t launch_w4_pack(int dtype, const uint8_t* codes, const void* scales, c
                        reinterpret_cast<uint32_t*>(base));
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    const int64_t total = (int64_t)num_experts * s.row_blocks * s.groups * 16;
+    const int64_t total = (int64_t)num_experts * s.row_blocks * s.k_tiles * s.tile_groups * 16;
     hipLaunchKernelGGL(w4_pack_scales_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, stream,
-                       static_cast<const uint16_t*>(scales), zeros, n, (k + group - 1) / group, s.groups,
-                       s.halves, s.half_n, s.row_blocks, total,
+                       static_cast<const uint16_t*>(scales), zeros, n, k, group, (k + group - 1) / group,
+                       s.tile_groups, s.halves, s.half_n, s.row_blocks, s.k_tiles, total,
                        reinterpret_cast<uint16_t*>(base + s.scales_at),
                        zeros != nullptr ? reinterpret_cast<uint8_t*>(base + s.zeros_at) : nullptr);
     return hipGetLastError();
@@ -423,32 +497,70 @@ hipError_t launch_w4_pack(int dtype, const uint8_t* codes, const void* scales, c
 
 namespace {
 
-template <typename T, int GS, bool ZEROS, bool GLU, int RT, int CT, int MAXT>
+template <typename T, int GS, bool ZEROS, bool GLU, int RT, int CT, int WAVES>
 hipError_t w4_launch(const W4Args& a, const W4Shape& s, int64_t items, int waves, hipStream_t stream)
 {
     const int units = (s.row_blocks + RT - 1) / RT;
     const char* base = static_cast<const char*>(a.packed);
     const size_t lds = (size_t)waves * (RT < 2 ? 1 : 2) * CT * 1024;
-    hipLaunchKernelGGL((w4_kernel<T, GS, ZEROS, GLU, RT, CT, MAXT>), dim3((unsigned)(items * units)),
+    hipLaunchKernelGGL((w4_kernel<T, GS, ZEROS, GLU, RT, CT, WAVES>), dim3((unsigned)(items * units)),
                        dim3(waves * 64), lds, stream, static_cast<const T*>(a.x), a.ld_x, a.x_rows,
                        a.src, reinterpret_cast<const uint4*>(base),
                        reinterpret_cast<const uint2*>(base + s.scales_at),
                        reinterpret_cast<const uint32_t*>(base + s.zeros_at), a.offsets, a.counts,
-                       a.num_experts, (int)a.num_rows, a.k, s.half_n, s.row_blocks, s.k_tiles, s.groups,
-                       a.group >= 128 ? a.group / 128 : 1, units, static_cast<T*>(a.out), a.ld_out);
+                       a.num_experts, (int)a.num_rows, a.k, s.half_n, s.row_blocks, s.k_tiles,
+                       units, static_cast<T*>(a.out), a.ld_out);
     return hipGetLastError();
 }
 
+// The split, by the rows an expert holds on average and by the 16-row output
+// blocks the grid has to make (row blocks of the weights times items).  More
+// row blocks a workgroup read x less often and join less; more wavefronts
+// and smaller workgroups give a small grid enough loads in flight.  Measured
+// on MI355X, weights not in the caches, us (bf16, groups of 128, RT x CT x
+// wavefronts):
+//   129024 blocks (64 tokens x 8 of 256, 2048 -> 7168)     8x1x2 290   4x1x2 298   4x1x4 331   2x1x4 398
+//     2048 blocks (1 token x 8 of 256, 7168 -> 2 x 2048)   8x1x4  31   4x1x4  27   2x1x4  31
+//     1068 blocks (3 x 4 of 64, 2048 -> 1411, groups 32)   4x1x4  12   2x1x4  10   2x1x8  13
+//      256 blocks (1 row, 1 expert, 8192 -> 4096)          2x1x4  13   2x1x8   9   2x1x16  9
+//    33792 blocks (64 rows an expert, 2048 -> 2 x 1408)    8x2x1 110   4x2x1 135   8x1x1 128   4x4x1 157
+//     7040 blocks (128 rows an expert, 8 experts)          8x2x1  33   8x2x2  31   8x2x4  36   4x2x1  37
+//     4352 blocks (512 rows, 1 expert, 4096 -> 4096)       8x2x2  45   8x2x4  32   4x2x4  42
+//     2816 blocks (32 rows an expert, 8 experts)           8x2x4  17   4x2x4  17   2x2x4  20
+//      768 blocks (64 rows, 1 expert, 4096 -> 4096)        4x2x8  14   2x2x8  12   2x2x16 13
+// Groups of 32 and 64 hold 2 to 4 times the scales of a row block: eight
+// row blocks do not fit the registers, four took 532 us against 603 (64
+// tokens) and 233 against 808 with two blocks of rows (512 tokens).
 template <typename T, int GS, bool ZEROS, bool GLU>
 hipError_t w4_sized(const W4Args& a, const W4Shape& s, hipStream_t stream)
 {
-    // blocks of rows: at most one per expert holding rows, and one more for
-    // every full block
+    // items: at most one per expert holding rows, and one more for every
+    // full block of rows
     const int64_t hold = a.num_rows < a.num_experts ? a.num_rows : a.num_experts;
-    const int64_t mean = a.num_rows / hold;
-    auto items = [&](int tm) { return hold + a.num_rows / tm; };
-    if (mean <= 16) return w4_launch<T, GS, ZEROS, GLU, 2, 1, 256>(a, s, items(16), 4, stream);
-    return w4_launch<T, GS, ZEROS, GLU, 4, 4, 256>(a, s, items(64), 4, stream);
+    const bool few = a.num_rows / hold <= 16;
+    const int64_t items = hold + a.num_rows / (few ? 16 : 32);
+    const int64_t blocks = items * s.row_blocks;
+    auto cap = [&](int waves) { return waves < s.k_tiles ? waves : s.k_tiles; };
+    if (few) {
+        if (blocks >= 32768) {
+            if constexpr (GS == 1) return w4_launch<T, GS, ZEROS, GLU, 8, 1, 4>(a, s, items, cap(2), stream);
+            else return w4_launch<T, GS, ZEROS, GLU, 4, 1, 4>(a, s, items, cap(2), stream);
+        }
+        if (blocks >= (GS == 1 ? 1536 : 4096))
+            return w4_launch<T, GS, ZEROS, GLU, 4, 1, 4>(a, s, items, cap(4), stream);
+        if (blocks >= 512) return w4_launch<T, GS, ZEROS, GLU, 2, 1, 4>(a, s, items, cap(4), stream);
+        constexpr int kMost = GS == 1 ? 16 : 8;
+        return w4_launch<T, GS, ZEROS, GLU, 2, 1, kMost>(a, s, items, cap(kMost), stream);
+    }
+    if (blocks >= 4096) {
+        if constexpr (GS == 1)
+            return w4_launch<T, GS, ZEROS, GLU, 8, 2, 4>(
+                a, s, items, cap(blocks >= 16384 ? 1 : blocks >= 6144 ? 2 : 4), stream);
+        else
+            return w4_launch<T, GS, ZEROS, GLU, 4, 2, 4>(a, s, items, 1, stream);
+    }
+    if (blocks >= 1536) return w4_launch<T, GS, ZEROS, GLU, 4, 2, 4>(a, s, items, cap(4), stream);
+    return w4_launch<T, GS, ZEROS, GLU, 2, 2, 8>(a, s, items, cap(8), stream);
 }
 
 template <typename T, int GS>
