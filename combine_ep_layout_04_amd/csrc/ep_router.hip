@@ -40,9 +40,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kNegInf = -__builtin_inff();
 
-// lane ^ STEP inside aligned groups of 16 or 64 lanes.  Up to 8 a DPP move
-// (the mirror forms pair lane i with 7 - i and 15 - i, which meets lane ^ 4
-// and ^ 8's half: what is moved is the same in all lanes of a half).
+// lane ^ STEP.  Up to 8 a DPP move (the mirror forms pair lane i with 7 - i
+// and 15 - i, which meets lane ^ 4's and ^ 8's half: what is moved is the
+// same in all lanes of a half); 16 and 32 swap rows of two registers, here
+// copies of one, and take the half that is not the lane's own.
 template <int STEP>
 __device__ __forceinline__ uint32_t exchange(uint32_t v)
 {
@@ -50,7 +51,13 @@ __device__ __forceinline__ uint32_t exchange(uint32_t v)
     else if constexpr (STEP == 2) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true);
     else if constexpr (STEP == 4) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true);
     else if constexpr (STEP == 8) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, true);
-    else return (uint32_t)__shfl_xor((int)v, STEP, 64);
+    else if constexpr (STEP == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return (threadIdx.x & 16) ? r[0] : r[1];
+    } else {
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return (threadIdx.x & 32) ? r[0] : r[1];
+    }
 }
 template <int STEP>
 __device__ __forceinline__ float exchange(float v)
@@ -94,17 +101,23 @@ __device__ __forceinline__ void row_best(S& key, uint32_t& idx)
         row_best<LPR, STEP * 2>(key, idx);
     }
 }
-// the two largest keys (a >= b)
+// the two largest of a >= b and c >= d
+template <typename S>
+__device__ __forceinline__ void two_best(S& a, S& b, S c, S d)
+{
+    const S lo = c > a ? a : c;
+    a = c > a ? c : a;
+    b = d > b ? d : b;
+    b = lo > b ? lo : b;
+}
+// the two largest keys of `width` lanes (a power of two)
 template <int LPR, int STEP = 1, typename S>
-__device__ __forceinline__ void row_top2(S& a, S& b)
+__device__ __forceinline__ void group_top2(S& a, S& b, int width)
 {
     if constexpr (STEP < LPR) {
-        const S oa = exchange<STEP>(a), ob = exchange<STEP>(b);
-        const S lo = oa > a ? a : oa;
-        a = oa > a ? oa : a;
-        b = ob > b ? ob : b;
-        b = lo > b ? lo : b;
-        row_top2<LPR, STEP * 2>(a, b);
+        if (STEP >= width) return;
+        two_best(a, b, exchange<STEP>(a), exchange<STEP>(b));
+        group_top2<LPR, STEP * 2>(a, b, width);
     }
 }
 
@@ -226,21 +239,35 @@ void router_kernel(const T* __restrict__ logits, int64_t num_tokens, int E, int6
         // rate each group, then keep those with fewer than topk_groups better
         // ones (ties to the lower group)
         const int per = E / num_groups;
-        for (int g = 0; g < num_groups; ++g) {
-            Key a = (Key)kNegInf, b = (Key)kNegInf;
+        const int seg = per / 4;            // lanes of a group, if it is whole vectors
+        if (per % 4 == 0 && seg <= LPR && (seg & (seg - 1)) == 0) {
+            // each vector's lanes hold whole groups side by side: the two best
+            // of the vector, then of the group's lanes
 #pragma unroll
-            for (int i = 0; i < VV; ++i)
+            for (int i = 0; i < VV; ++i) {
+                Key a = (Key)kNegInf, b = (Key)kNegInf;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int e = (i * LPR + lr) * 4 + c;
-                    const Key v = e >= g * per && e < (g + 1) * per ? val[i][c] : (Key)kNegInf;
-                    const Key lo = v > a ? a : v;
-                    a = v > a ? v : a;
-                    b = lo > b ? lo : b;
-                }
-            row_top2<LPR>(a, b);
-            if (group_top > 1 && b > (Key)kNegInf) a += b;
-            if (lr == 0) rating[r][g] = a;
+                for (int c = 0; c < 4; ++c) two_best(a, b, val[i][c], (Key)kNegInf);
+                group_top2<LPR>(a, b, seg);
+                if (group_top > 1 && b > (Key)kNegInf) a += b;
+                const int g = (i * LPR + lr) / seg;
+                if (lr % seg == 0 && g < num_groups) rating[r][g] = a;
+            }
+        } else {
+            for (int g = 0; g < num_groups; ++g) {
+                Key a = (Key)kNegInf, b = (Key)kNegInf;
+#pragma unroll
+                for (int i = 0; i < VV; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int e = (i * LPR + lr) * 4 + c;
+                        const Key v = e >= g * per && e < (g + 1) * per ? val[i][c] : (Key)kNegInf;
+                        two_best(a, b, v, (Key)kNegInf);
+                    }
+                group_top2<LPR>(a, b, LPR);
+                if (group_top > 1 && b > (Key)kNegInf) a += b;
+                if (lr == 0) rating[r][g] = a;
+            }
         }
         __syncthreads();
         uint64_t keep = 0;
@@ -506,12 +533,20 @@ void router_backward_kernel(const T* __restrict__ logits, int64_t num_tokens, in
 }
 
 // f(lanes per row, vectors per lane) for a row of E experts: 4 lanes up to
-// 16 experts, 16 up to 256, 64 beyond.
+// 16 experts, 16 up to 256, 64 beyond.  Few rows leave the chip idle and only
+// the length of the chain counts: then 65 to 256 experts take 64 lanes too.
+// Measured on MI355X, us in a graph, 16 against 64 lanes: 256 experts, 1
+// token 6.5 / 5.7 (sigmoid, bias, 8 groups: 14.8 / 8.3), 2048 tokens 7.2 /
+// 6.9 (17.4 / 10.3), 8192 tokens 7.8 / 13.6; 96 experts, 1 token 5.4 / 5.9
+// (12.4 / 11.1), 2048 tokens 6.1 / 7.0 (14.2 / 15.1); the backward at 256
+// experts, 1 token 4.3 / 3.0, 8192 tokens 5.4 / 6.3.
 template <typename F>
-hipError_t with_row_shape(int E, F&& f)
+hipError_t with_row_shape(int E, int64_t num_tokens, F&& f)
 {
     if (E <= 16) return f(std::integral_constant<int, 4>(), std::integral_constant<int, 1>());
     if (E <= 64) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 1>());
+    if (E <= 256 && num_tokens <= (E <= 128 ? 1024 : 2048))
+        return f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
     if (E <= 128) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 2>());
     if (E <= 256) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 4>());
     return f(std::integral_constant<int, 64>(), std::integral_constant<int, 4>());
@@ -521,7 +556,7 @@ template <typename T>
 hipError_t router_of(const RouterArgs& a, hipStream_t stream)
 {
     const bool wide = a.bias != nullptr || (a.num_groups > 1 && a.group_top > 1);
-    return with_row_shape(a.num_experts, [&](auto lpr, auto vv) {
+    return with_row_shape(a.num_experts, a.num_tokens, [&](auto lpr, auto vv) {
         constexpr int kRows = kThreads / decltype(lpr)::value;
         const dim3 grid((unsigned)((a.num_tokens + kRows - 1) / kRows));
         auto go = [&](auto w) {
@@ -540,7 +575,7 @@ hipError_t router_of(const RouterArgs& a, hipStream_t stream)
 template <typename T>
 hipError_t router_backward_of(const RouterBackwardArgs& a, hipStream_t stream)
 {
-    return with_row_shape(a.num_experts, [&](auto lpr, auto vv) {
+    return with_row_shape(a.num_experts, a.num_tokens, [&](auto lpr, auto vv) {
         constexpr int kRows = kThreads / decltype(lpr)::value;
         const dim3 grid((unsigned)((a.num_tokens + kRows - 1) / kRows));
         hipLaunchKernelGGL((router_backward_kernel<T, decltype(lpr)::value, decltype(vv)::value>),

@@ -1082,6 +1082,11 @@ def _need_on(t, name, dtype, device, numel=None):
         raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
+# the current stream's handle without a Stream object: 0.1 us against 1.8 of
+# the 10 that a call takes on the host
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 class _On:
     """The device and stream of a call: ``empty`` allocates for that stream,
     ``call`` launches on it."""
@@ -1092,7 +1097,7 @@ class _On:
         self.device = device
         self.ctx = None
         if stream is None:
-            self.stream = torch.cuda.current_stream(device).cuda_stream
+            self.stream = _raw_stream(device.index)
         else:
             if not isinstance(stream, torch.cuda.Stream):
                 stream = torch.cuda.ExternalStream(int(stream), device=device)
