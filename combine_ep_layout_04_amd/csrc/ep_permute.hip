@@ -29,8 +29,8 @@
 // FAST: every row starts on 16 bytes and is a whole number of vectors, and
 // accesses go through buffer resources (past the row's end, and in a masked
 // row, a load gives zeros, without a branch).  Otherwise vectors are loaded
-// and stored at whatever element the row starts on, and the partial last
-// vector element by element.
+// and stored at whatever element the row starts on, and the last vector is
+// moved back to end with the row.
 
 #include "ep_device.h"
 #include "ep_internal.h"
@@ -42,6 +42,16 @@ namespace {
 template <typename T>
 using UVec = typename Unaligned16<T>::type;
 
+// Where vector v of a row of H elements starts: the last one is moved back to
+// end with the row (its first elements are another vector's too, with the
+// same values).  Rows shorter than a vector have one, taken by elements.
+template <typename T, bool FAST>
+__device__ __forceinline__ int vec_start(int H, int v)
+{
+    const int e = v * kVec<T>;
+    return FAST || e + kVec<T> <= H ? e : H - kVec<T>;
+}
+
 // Vector v of a row of H elements; `here` false reads nothing.
 template <typename T, bool FAST, int cpol>
 __device__ __forceinline__ uint4 load_vec(const T* row, bool here, int H, int v)
@@ -51,15 +61,15 @@ __device__ __forceinline__ uint4 load_vec(const T* row, bool here, int H, int v)
         return load_row16<cpol>(buffer_rsrc(row, here ? H * (int)sizeof(T) : 0), v * 16);
     } else {
         uint4 d = make_uint4(0u, 0u, 0u, 0u);
-        const int e = v * EV;
-        if (here && e + EV <= H) {
-            const UVec<T>* p = reinterpret_cast<const UVec<T>*>(row + e);
+        if (!here || v * EV >= H) return d;
+        if (H >= EV) {
+            const UVec<T>* p = reinterpret_cast<const UVec<T>*>(row + vec_start<T, FAST>(H, v));
             d = __builtin_bit_cast(uint4, (u32x4)(cpol == kCpolNT ? __builtin_nontemporal_load(p) : *p));
-        } else if (here && e < H) {
+        } else {
             T raw[EV] = {};
 #pragma unroll
             for (int c = 0; c < EV; ++c)
-                if (e + c < H) raw[c] = row[e + c];
+                if (c < H) raw[c] = row[c];
             __builtin_memcpy(&d, raw, 16);
         }
         return d;
@@ -70,21 +80,42 @@ template <typename T, bool FAST>
 __device__ __forceinline__ void store_vec(T* row, int H, int v, const uint4& d)
 {
     constexpr int EV = kVec<T>;
-    const int e = v * EV;
+    if (v * EV >= H) return;
     if constexpr (FAST) {
-        if (e < H) store_row16(buffer_rsrc(row, H * (int)sizeof(T)), v * 16, d);
+        store_row16(buffer_rsrc(row, H * (int)sizeof(T)), v * 16, d);
+    } else if (H >= EV) {
+        // not streaming: the lines that two vectors share are put together
+        // in the L2
+        *reinterpret_cast<UVec<T>*>(row + vec_start<T, FAST>(H, v)) =
+            (UVec<T>)__builtin_bit_cast(u32x4, d);
     } else {
-        if (e + EV <= H) {
-            __builtin_nontemporal_store((UVec<T>)__builtin_bit_cast(u32x4, d),
-                                        reinterpret_cast<UVec<T>*>(row + e));
-        } else if (e < H) {
-            T raw[EV];
-            __builtin_memcpy(raw, &d, 16);
+        T raw[EV];
+        __builtin_memcpy(raw, &d, 16);
 #pragma unroll
-            for (int c = 0; c < EV; ++c)
-                if (e + c < H) row[e + c] = raw[c];
+        for (int c = 0; c < EV; ++c)
+            if (c < H) row[c] = raw[c];
+    }
+}
+
+// The bits of vector v that no vector before it holds (a dot product counts
+// an element once).
+template <typename T, bool FAST>
+__device__ __forceinline__ uint4 own_bits(int H, int v)
+{
+    uint32_t m[4] = {~0u, ~0u, ~0u, ~0u};
+    if constexpr (!FAST) {
+        const int skip = H >= kVec<T> ? (v * kVec<T> - vec_start<T, FAST>(H, v)) * (int)sizeof(T) * 8 : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int s = skip - 32 * i;
+            m[i] = s <= 0 ? ~0u : s >= 32 ? 0u : ~0u << s;
         }
     }
+    return make_uint4(m[0], m[1], m[2], m[3]);
+}
+__device__ __forceinline__ uint4 operator&(const uint4& a, const uint4& b)
+{
+    return make_uint4(a.x & b.x, a.y & b.y, a.z & b.z, a.w & b.w);
 }
 
 template <typename T>
@@ -226,10 +257,12 @@ void dot_kernel(const T* __restrict__ a, int64_t lda, const T* __restrict__ b, i
             float acc[kVec<T>];
 #pragma unroll
             for (int i = 0; i < kVec<T>; ++i) acc[i] = 0.0f;
+            const uint4 own = own_bits<T, FAST>(H, v);
+            const uint4 ao = av & own;
 #pragma unroll
             for (int q = 0; q < KB; ++q) {
                 const int32_t r = c.row(q);
-                if (r >= 0) dots[q] = dot_vec<T>(av, bv[q], dots[q]);
+                if (r >= 0) dots[q] = dot_vec<T>(ao, bv[q] & own, dots[q]);
                 if constexpr (MODE == kDotSum) add_scaled<T>(acc, bv[q], r >= 0 ? c.w(q) : 0.0f);
                 if constexpr (MODE == kDotScatter)
                     if (r >= 0) store_vec<T, FAST>(out + r * ldo, H, v, scaled<T>(av, c.w(q)));
