@@ -148,24 +148,23 @@ __device__ __forceinline__ float dot_vec(const uint4& a, const uint4& b, float a
     return acc;
 }
 
-// slot and weight of choice j of a token, held by lane j of each wavefront
-// (k <= 64) and read back as wavefront-uniform values.
+// Rows and weights of choices j0 .. j0 + N - 1 of token t, -1 for no row.
+// t and j0 are the same in the whole workgroup, so these are scalar loads
+// into scalar registers: whichever lanes are active where they are used.
+template <int N>
 struct Choices {
-    int32_t slot;
-    float weight;
-    __device__ __forceinline__ Choices(const int32_t* s, const float* w, int64_t t, int j0, int n,
-                                       int k, int64_t rows)
+    int32_t row[N];
+    float w[N];
+    __device__ __forceinline__ Choices(const int32_t* __restrict__ slot,
+                                       const float* __restrict__ weights, int64_t t, int j0, int k,
+                                       int64_t rows)
     {
-        const int j = j0 + ((int)threadIdx.x & 63);
-        const bool mine = ((int)threadIdx.x & 63) < n && j < k;
-        slot = mine ? s[t * k + j] : -1;
-        if (slot >= rows) slot = -1;
-        weight = mine && w != nullptr ? w[t * k + j] : 1.0f;
-    }
-    __device__ __forceinline__ int32_t row(int q) const { return __builtin_amdgcn_readlane(slot, q); }
-    __device__ __forceinline__ float w(int q) const
-    {
-        return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(weight), q));
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+            const int32_t r = j0 + q < k ? slot[t * k + j0 + q] : -1;
+            row[q] = r < rows ? r : -1;
+            w[q] = weights == nullptr ? 1.0f : row[q] >= 0 ? weights[t * k + j0 + q] : 0.0f;
+        }
     }
 };
 
@@ -183,13 +182,20 @@ void scatter_kernel(const T* __restrict__ x, int64_t ldx, int H, int k, int tpr,
     int gi;
     if (!xcd_tile(blockIdx.x, groups, num_tiles, tile, gi)) return;
     const int64_t t = tile / tpr;
-    const int v = (int)(tile - t * tpr) * NT + (int)threadIdx.x;
-    const Choices c(slot, w, t, gi * kScatterSlots, kScatterSlots, k, num_rows);
-    const uint4 d = load_vec<T, FAST, 0>(x + t * ldx, true, H, v);
+    const Choices<kScatterSlots> c(slot, w, t, gi * kScatterSlots, k, num_rows);
+    auto one = [&](int v) {
+        const uint4 d = load_vec<T, FAST, 0>(x + t * ldx, true, H, v);
 #pragma unroll
-    for (int q = 0; q < kScatterSlots; ++q) {
-        const int32_t r = c.row(q);
-        if (r >= 0) store_vec<T, FAST>(rows + r * ldr, H, v, w != nullptr ? scaled<T>(d, c.w(q)) : d);
+        for (int q = 0; q < kScatterSlots; ++q) {
+            const int32_t r = c.row[q];
+            if (r >= 0) store_vec<T, FAST>(rows + r * ldr, H, v, w != nullptr ? scaled<T>(d, c.w[q]) : d);
+        }
+    };
+    if constexpr (FAST) {
+        one((int)(tile - t * tpr) * NT + (int)threadIdx.x);
+    } else {
+        const int nvec = (H + kVec<T> - 1) / kVec<T>;
+        for (int v = (int)threadIdx.x; v < nvec; v += NT) one(v);
     }
 }
 
@@ -203,22 +209,20 @@ void gather_kernel(const T* __restrict__ y, int64_t ldy, int H, int k, int tpr,
 {
     const int64_t t = blockIdx.x / tpr;
     const int v = (int)(blockIdx.x - t * tpr) * NT + (int)threadIdx.x;
-    const Choices c(slot, w, t, 0, 64, k, num_rows);
     float acc[kVec<T>];
 #pragma unroll
     for (int i = 0; i < kVec<T>; ++i) acc[i] = 0.0f;
     for (int j0 = 0; j0 < k; j0 += KB) {
+        const Choices<KB> c(slot, w, t, j0, k, num_rows);
         uint4 d[KB];
-        float wj[KB];
 #pragma unroll
         for (int q = 0; q < KB; ++q) {
-            // past k: the lane holds -1, and lane 63 at most is asked
-            const int32_t r = j0 + q < k ? c.row((j0 + q) & 63) : -1;
-            wj[q] = r >= 0 ? c.w((j0 + q) & 63) : 0.0f;
+            const int32_t r = c.row[q];
             d[q] = load_vec<T, FAST, kCpolNT>(y + (r >= 0 ? r * ldy : 0), r >= 0, H, v);
         }
+        // no row: zeros times its weight, 0 or 1
 #pragma unroll
-        for (int q = 0; q < KB; ++q) add_scaled<T>(acc, d[q], wj[q]);
+        for (int q = 0; q < KB; ++q) add_scaled<T>(acc, d[q], c.w[q]);
     }
     store_vec<T, FAST>(out + t * ldo, H, v, pack<T>(acc));
 }
@@ -242,7 +246,7 @@ void dot_kernel(const T* __restrict__ a, int64_t lda, const T* __restrict__ b, i
     const int tid = threadIdx.x;
     const int nvec = (H + kVec<T> - 1) / kVec<T>;
     for (int j0 = 0; j0 < k; j0 += KB) {
-        const Choices c(slot, w, t, j0, KB, k, num_rows);
+        const Choices<KB> c(slot, w, t, j0, k, num_rows);
         float dots[KB];
 #pragma unroll
         for (int q = 0; q < KB; ++q) dots[q] = 0.0f;
@@ -251,7 +255,7 @@ void dot_kernel(const T* __restrict__ a, int64_t lda, const T* __restrict__ b, i
             uint4 bv[KB];
 #pragma unroll
             for (int q = 0; q < KB; ++q) {
-                const int32_t r = c.row(q);
+                const int32_t r = c.row[q];
                 bv[q] = load_vec<T, FAST, kCpolNT>(b + (r >= 0 ? r * ldb : 0), r >= 0, H, v);
             }
             float acc[kVec<T>];
@@ -261,11 +265,11 @@ void dot_kernel(const T* __restrict__ a, int64_t lda, const T* __restrict__ b, i
             const uint4 ao = av & own;
 #pragma unroll
             for (int q = 0; q < KB; ++q) {
-                const int32_t r = c.row(q);
+                const int32_t r = c.row[q];
                 if (r >= 0) dots[q] = dot_vec<T>(ao, bv[q] & own, dots[q]);
-                if constexpr (MODE == kDotSum) add_scaled<T>(acc, bv[q], r >= 0 ? c.w(q) : 0.0f);
+                if constexpr (MODE == kDotSum) add_scaled<T>(acc, bv[q], c.w[q]);
                 if constexpr (MODE == kDotScatter)
-                    if (r >= 0) store_vec<T, FAST>(out + r * ldo, H, v, scaled<T>(av, c.w(q)));
+                    if (r >= 0) store_vec<T, FAST>(out + r * ldo, H, v, scaled<T>(av, c.w[q]));
             }
             if constexpr (MODE == kDotSum) store_vec<T, FAST>(out + t * ldo, H, v, pack<T>(acc));
         }
@@ -280,7 +284,8 @@ void dot_kernel(const T* __restrict__ a, int64_t lda, const T* __restrict__ b, i
             float s = 0.0f;
 #pragma unroll
             for (int i = 0; i < NT / 64; ++i) s += part[i][tid];
-            grad_w[t * k + j0 + tid] = c.slot >= 0 ? s : 0.0f;
+            const int32_t r = slot[t * k + j0 + tid];
+            grad_w[t * k + j0 + tid] = r >= 0 && r < num_rows ? s : 0.0f;
         }
         __syncthreads();
     }
@@ -324,8 +329,13 @@ template <typename T, bool FAST>
 hipError_t scatter_of(const MoveArgs& a, hipStream_t stream)
 {
     const int nvec = (a.hidden + kVec<T> - 1) / kVec<T>;
-    const int nt = use64(nvec) ? 64 : 128;
-    const int tpr = (nvec + nt - 1) / nt;
+    // A long row that is not whole vectors goes to one workgroup: its parts
+    // share lines, which only meet in one XCD's L2 (bf16, 8192 tokens: 4097
+    // wide, k 8: 157 us against 176 in tiles; 2047 wide, k 4: 39 against 43;
+    // 1001 wide, k 2, 126 vectors: 14 us in a workgroup of 256, 10 in one of
+    // 128).
+    const int nt = !FAST ? (nvec <= 64 ? 64 : nvec <= 128 ? 128 : 256) : use64(nvec) ? 64 : 128;
+    const int tpr = FAST ? (nvec + nt - 1) / nt : 1;
     const int groups = (a.num_topk + kScatterSlots - 1) / kScatterSlots;
     const int64_t tiles = a.num_tokens * tpr;
     const dim3 grid((unsigned)((tiles + 7) / 8 * 8 * groups));
@@ -337,7 +347,10 @@ hipError_t scatter_of(const MoveArgs& a, hipStream_t stream)
                            a.num_rows);
         return hipGetLastError();
     };
-    return nt == 64 ? go(std::integral_constant<int, 64>()) : go(std::integral_constant<int, 128>());
+    if (nt == 64) return go(std::integral_constant<int, 64>());
+    if constexpr (!FAST)
+        if (nt == 256) return go(std::integral_constant<int, 256>());
+    return go(std::integral_constant<int, 128>());
 }
 
 template <typename T, bool FAST>

@@ -31,6 +31,9 @@ CASES = [
     (3, 7168, 256, 8, "bf16", 0, 0, 0.0),
     (2, 9001, 4, 64, "fp16", 0, 5, 0.2),
     (300, 40, 8, 4, "fp32", 0, 0, 0.05),
+    # rows of fewer vectors than a token has choices
+    (40, 3, 64, 8, "bf16", 0, 0, 0.1),
+    (40, 9, 64, 64, "fp32", 1, 0, 0.1),
 ]
 
 
