@@ -1154,7 +1154,7 @@ ep_status_t ep_w4_pack(const void* codes, const void* scales, const void* zeros,
                                           zeros != nullptr, gated);
     if (packed_bytes < need)
         return fail(EP_INVALID_ARGUMENT, "packed holds %zu bytes, needs %zu", packed_bytes, need);
-    if (need / 4 / 256 > (size_t)INT32_MAX)
+    if (need / 16 / 256 > (size_t)INT32_MAX)
         return fail(EP_UNSUPPORTED, "the weights need more than 2^31 workgroups");
     return from_hip(ep::launch_w4_pack(dtype, static_cast<const uint8_t*>(codes), scales,
                                        static_cast<const uint8_t*>(zeros), num_experts, out_features,

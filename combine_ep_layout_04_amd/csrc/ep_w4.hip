@@ -392,7 +392,7 @@ void w4_kernel(const T* __restrict__ x, int64_t ldx, int64_t x_rows, const int32
     }
 }
 
-// ---- packing, one thread per word of the tiles, then per scale
+// ---- packing: the tiles of codes, then one thread per scale
 
 __device__ __forceinline__ int row_of_block(int b, int i, int halves, int half_n)
 {
@@ -401,34 +401,46 @@ __device__ __forceinline__ int row_of_block(int b, int i, int halves, int half_n
     return n < half_n ? (b % halves) * half_n + n : -1;
 }
 
+// A wavefront a tile: lane l reads the 32 codes of chunk l % 4 of row l / 4
+// (64 bytes a row), the words change places through LDS, and the tile goes
+// out as it lies in memory.
 __global__ __launch_bounds__(256)
 void w4_pack_codes_kernel(const uint8_t* __restrict__ codes, int N, int K, int halves, int half_n,
-                          int row_blocks, int k_tiles, int shift, int64_t words,
-                          uint32_t* __restrict__ out)
+                          int row_blocks, int k_tiles, int shift, int64_t tiles,
+                          uint4* __restrict__ out)
 {
-    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (at >= words) return;
-    const int i = (int)(at & 3), lane = (int)(at >> 2) & 63;
-    const int64_t tile = at >> 8;
-    const int kt = (int)(tile % k_tiles);
-    const int64_t eb = tile / k_tiles;
-    const int n = row_of_block((int)(eb % row_blocks), lane & 15, halves, half_n);
-    const int k = kt * 128 + i * 32 + (lane >> 4) * 8;
-    uint32_t w = 0;
-    if (n >= 0 && k < K) {
-        const uint8_t* p = codes + ((eb / row_blocks * N + n) * (int64_t)K + k) / 2;
-        uint32_t c;
-        __builtin_memcpy(&c, p, 4);
-        // even codes to the low half, odd ones to the high half, then turned
-        // so that the first pair lies in the mantissas
+    typedef uint32_t bytes16 __attribute__((ext_vector_type(4), aligned(1)));
+    __shared__ uint32_t turn[4][256];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t tile = (int64_t)blockIdx.x * 4 + wave;
+    if (tile < tiles) {
+        const int kt = (int)(tile % k_tiles);
+        const int64_t eb = tile / k_tiles;
+        const int row = lane >> 2, chunk = lane & 3;
+        const int n = row_of_block((int)(eb % row_blocks), row, halves, half_n);
+        const int k = kt * 128 + chunk * 32;
+        u32x4 c = {0, 0, 0, 0};
+        if (n >= 0 && k < K)
+            c = (u32x4)*reinterpret_cast<const bytes16*>(
+                codes + ((eb / row_blocks * N + n) * (int64_t)K + k) / 2);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            w |= ((c >> (8 * q)) & 15u) << (4 * q);
-            w |= ((c >> (8 * q + 4)) & 15u) << (16 + 4 * q);
+            // even codes to the low half, odd ones to the high half, then
+            // turned so that the first pair lies in the mantissas
+            uint32_t w = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                w |= ((c[q] >> (8 * j)) & 15u) << (4 * j);
+                w |= ((c[q] >> (8 * j + 4)) & 15u) << (16 + 4 * j);
+            }
+            turn[wave][(row + 16 * q) * 4 + chunk] = (w << shift) | (w >> (32 - shift));
         }
-        w = (w << shift) | (w >> (32 - shift));
     }
-    out[at] = w;
+    __syncthreads();
+    if (tile < tiles) {
+        const uint32_t* t = &turn[wave][lane * 4];
+        out[tile * 64 + lane] = make_uint4(t[0], t[1], t[2], t[3]);
+    }
 }
 
 __global__ __launch_bounds__(256)
@@ -479,11 +491,11 @@ hipError_t launch_w4_pack(int dtype, const uint8_t* codes, const void* scales, c
 {
     const W4Shape s = w4_shape(num_experts, n, k, group, zeros != nullptr, glu);
     char* base = static_cast<char*>(packed);
-    const int64_t words = s.scales_at / 4;
-    hipLaunchKernelGGL(w4_pack_codes_kernel, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, stream,
+    const int64_t tiles = s.scales_at / 1024;
+    hipLaunchKernelGGL(w4_pack_codes_kernel, dim3((unsigned)((tiles + 3) / 4)), dim3(256), 0, stream,
                        codes, n, k, s.halves, s.half_n, s.row_blocks, s.k_tiles,
-                       dtype == 0 ? Code<Bf16>::kShift : Code<Fp16>::kShift, words,
-                       reinterpret_cast<uint32_t*>(base));
+                       dtype == 0 ? Code<Bf16>::kShift : Code<Fp16>::kShift, tiles,
+                       reinterpret_cast<uint4*>(base));
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     const int64_t total = (int64_t)num_experts * s.row_blocks * s.k_tiles * s.tile_groups * 16;
