@@ -3,6 +3,10 @@
 // zero[e, n, k / G]) * x[r, k], for few rows per expert, optionally with the
 // gated activation out = silu(gate) * up over the two halves of n.
 //
+// Measured on MI355X: 64 tokens through 8 of 256 experts, 2048 -> 7168, 286 us
+// (5.9 TB/s of weights, scales and rows); one token, 7168 -> 2 x 2048 gated,
+// 25 us (4.8 TB/s).
+//
 // What bounds it: with few rows per expert every weight is used for a few
 // products only, so the time is that of streaming the chosen experts'
 // weights.  At half a byte per weight the vector unit has about 2.4

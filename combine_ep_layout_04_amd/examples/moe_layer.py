@@ -50,21 +50,23 @@ def train_step(x, gate_weight, w13, w2, num_topk: int, grad_out, *, score: str =
     idx, w, probs = ep.ep_router(logits, num_topk, score=score, want_probs=grad_probs_of is not None)
     counts, offsets, slot, _, _ = ep.ep_layout(idx, E)
     rows = ep.ep_permute(x, slot)
-    # the experts, by torch, with a graph of their own
-    rows = rows.requires_grad_()
-    w13, w2 = w13.detach().requires_grad_(), w2.detach().requires_grad_()
+    # the experts, by torch, with a graph of their own whose leaves are each
+    # expert's rows and weights
     bounds = offsets.tolist()
+    leaves = [[t.detach().requires_grad_() for t in (rows[bounds[e]:bounds[e + 1]], w13[e], w2[e])]
+              for e in range(E)]
     with torch.enable_grad():
         parts = []
-        for e in range(E):
-            a = rows[bounds[e]:bounds[e + 1]] @ w13[e].t()
-            gate, up = a.chunk(2, 1)
-            parts.append((torch.nn.functional.silu(gate) * up) @ w2[e].t())
+        for r, a, b in leaves:
+            gate, up = (r @ a.t()).chunk(2, 1)
+            parts.append((torch.nn.functional.silu(gate) * up) @ b.t())
         y = torch.cat(parts)
     out = ep.ep_unpermute(y.detach(), slot, w)
 
     grad_y, grad_w = ep.ep_unpermute_backward(grad_out, slot, w, y.detach())
-    grad_rows, grad_w13, grad_w2 = torch.autograd.grad(y, (rows, w13, w2), grad_y[:bounds[E]])
+    grads = torch.autograd.grad(y, [t for leaf in leaves for t in leaf], grad_y[:bounds[E]])
+    grad_rows = torch.cat(grads[0::3])
+    grad_w13, grad_w2 = torch.stack(grads[1::3]), torch.stack(grads[2::3])
     grad_x, _ = ep.ep_permute_backward(grad_rows, slot)
     grad_probs = None if grad_probs_of is None else grad_probs_of(probs, counts)
     grad_logits = ep.ep_router_backward(logits, idx, grad_w, grad_probs, score=score)
