@@ -93,6 +93,38 @@ def test_product(case):
     assert torch.equal(again[:n].view(torch.int16), got[:n].contiguous().view(torch.int16))
 
 
+@pytest.mark.parametrize("group,dtype,zeros,gated", [
+    (128, "bf16", False, False), (128, "fp16", True, True), (64, "bf16", True, False),
+    (32, "fp16", False, True), (32, "bf16", True, False)])
+@pytest.mark.parametrize("T,E,k,N", [
+    # few rows an expert: over 32768 blocks of 16 outputs, over 4096, over
+    # 1536, over 512, below
+    (64, 16, 4, 16400), (16, 16, 4, 4008), (16, 16, 4, 1400), (16, 16, 4, 500), (2, 2, 1, 72),
+    # over 16 rows an expert: over 16384, 6144, 4096, 1536, below
+    (200, 4, 2, 16408), (200, 4, 2, 8008), (200, 4, 2, 5000), (200, 4, 2, 1800), (200, 4, 2, 200),
+])
+def test_every_split(T, E, k, N, group, dtype, zeros, gated):
+    K = 96 if N > 2000 else 416
+    rng = np.random.default_rng(N)
+    codes, s, z = make(rng, E, N, K, group, dtype, zeros)
+    idx = routing(rng, T, E, k)
+    _, offsets, _, src, _ = ep.ep_layout(torch.from_numpy(idx).to(DEV), E)
+    x = torch.from_numpy(rng.normal(size=(T, K))).to(TYPES[dtype])
+    W = ep.ep_w4_pack(torch.from_numpy(codes).to(DEV), s.to(DEV),
+                      None if z is None else torch.from_numpy(z).to(DEV), group_size=group, gated=gated)
+    got = ep.ep_expert_matmul_w4(x.to(DEV), W, offsets, src=src)
+    xs, off, rows = f64(x), offsets.cpu().numpy(), src.cpu().numpy()
+    deq = moe.w4_dequantize(codes, f64(s), z, group)
+    for e in range(E):
+        a, b = off[e], off[e + 1]
+        if a == b:
+            continue
+        xe = xs[rows[a:b]]
+        ref, err = product(xe, deq[e], gated,
+                           np.abs(xe) @ (f64(s)[e][:, np.arange(K) // group] * 62.0).T)
+        check(got[a:b], ref, rounded(ref, err, dtype), f"expert {e}")
+
+
 def test_one_expert_needs_no_offsets():
     rng = np.random.default_rng(8)
     codes, s, z = make(rng, 1, 70, 256, 128, "bf16", False)
