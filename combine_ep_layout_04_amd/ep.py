@@ -1231,11 +1231,12 @@ def ep_permute(x: torch.Tensor, slot: torch.Tensor, topk_weights: Optional[torch
     _, k = _pairs_of(slot, topk_weights, T, dev)
     on = _On(dev, stream)
     if out is None:
-        out = on.empty((T * k if rows is None else int(rows), H), x.dtype)
-    ld_out = _rows_of(out, "out", x.dtype, H, dev)
-    if rows is not None and out.shape[0] < rows:
-        raise ValueError(f"out has {out.shape[0]} rows, needs {rows}")
-    R = out.shape[0]
+        R, ld_out = T * k if rows is None else int(rows), H
+        out = on.empty((R, H), x.dtype)
+    else:
+        R, ld_out = out.shape[0], _rows_of(out, "out", x.dtype, H, dev)
+        if rows is not None and R < rows:
+            raise ValueError(f"out has {R} rows, needs {rows}")
     c, o, E = _clear_of(clear, dev)
     on.call("ep_permute", lib().ep_permute, x.data_ptr(), _DTYPES[x.dtype], T, H, ld, k,
             slot.data_ptr(), _ptr(topk_weights), out.data_ptr(), ld_out, R, c, o, E)
@@ -1265,10 +1266,11 @@ def ep_permute_backward(grad_rows: torch.Tensor, slot: torch.Tensor,
         else:
             _need_on(grad_weights, "grad_weights", torch.float32, dev, T * k)
     if grad_x is None:
-        grad_x = on.empty((T, H), dt)
-    ld_gx = _rows_of(grad_x, "grad_x", dt, H, dev)
-    if grad_x.shape[0] != T:
-        raise ValueError(f"grad_x has {grad_x.shape[0]} rows, slot {T}")
+        grad_x, ld_gx = on.empty((T, H), dt), H
+    else:
+        ld_gx = _rows_of(grad_x, "grad_x", dt, H, dev)
+        if grad_x.shape[0] != T:
+            raise ValueError(f"grad_x has {grad_x.shape[0]} rows, slot {T}")
     on.call("ep_permute_backward", lib().ep_permute_backward, grad_rows.data_ptr(), _DTYPES[dt], T,
             H, ld, R, k, slot.data_ptr(), _ptr(topk_weights), _ptr(x), ld_x, grad_x.data_ptr(),
             ld_gx, _ptr(grad_weights))
@@ -1286,10 +1288,11 @@ def ep_unpermute(y: torch.Tensor, slot: torch.Tensor, topk_weights: Optional[tor
     T, k = _pairs_of(slot, topk_weights, None, dev)
     on = _On(dev, stream)
     if out is None:
-        out = on.empty((T, H), y.dtype)
-    ld_out = _rows_of(out, "out", y.dtype, H, dev)
-    if out.shape[0] != T:
-        raise ValueError(f"out has {out.shape[0]} rows, slot {T}")
+        out, ld_out = on.empty((T, H), y.dtype), H
+    else:
+        ld_out = _rows_of(out, "out", y.dtype, H, dev)
+        if out.shape[0] != T:
+            raise ValueError(f"out has {out.shape[0]} rows, slot {T}")
     on.call("ep_unpermute", lib().ep_unpermute, y.data_ptr(), _DTYPES[y.dtype], T, H, ld, R, k,
             slot.data_ptr(), _ptr(topk_weights), out.data_ptr(), ld_out)
     return out
@@ -1319,11 +1322,12 @@ def ep_unpermute_backward(grad_out: torch.Tensor, slot: torch.Tensor,
         else:
             _need_on(grad_weights, "grad_weights", torch.float32, dev, T * k)
     if grad_y is None:
-        grad_y = on.empty((T * k if rows is None else int(rows), H), dt)
-    ld_gy = _rows_of(grad_y, "grad_y", dt, H, dev)
-    R = grad_y.shape[0]
-    if rows is not None and R < rows:
-        raise ValueError(f"grad_y has {R} rows, needs {rows}")
+        R, ld_gy = T * k if rows is None else int(rows), H
+        grad_y = on.empty((R, H), dt)
+    else:
+        R, ld_gy = grad_y.shape[0], _rows_of(grad_y, "grad_y", dt, H, dev)
+        if rows is not None and R < rows:
+            raise ValueError(f"grad_y has {R} rows, needs {rows}")
     if y is not None and y.shape[0] < R:
         raise ValueError(f"y has {y.shape[0]} rows, grad_y {R}")
     c, o, E = _clear_of(clear, dev)
@@ -1414,10 +1418,11 @@ def ep_expert_matmul_w4(x: torch.Tensor, weights: W4Weights, offsets: Optional[t
     on = _On(dev, stream)
     n = w.out_features // 2 if w.gated else w.out_features
     if out is None:
-        out = on.empty((R, n), w.dtype)
-    ld_out = _rows_of(out, "out", w.dtype, n, dev)
-    if out.shape[0] < R:
-        raise ValueError(f"out has {out.shape[0]} rows, needs {R}")
+        out, ld_out = on.empty((R, n), w.dtype), n
+    else:
+        ld_out = _rows_of(out, "out", w.dtype, n, dev)
+        if out.shape[0] < R:
+            raise ValueError(f"out has {out.shape[0]} rows, needs {R}")
     on.call("ep_expert_matmul_w4", lib().ep_expert_matmul_w4, x.data_ptr(), _DTYPES[w.dtype], ld,
             x.shape[0], _ptr(src), w.packed.data_ptr(), w.packed.numel(), w.num_experts,
             w.out_features, w.in_features, w.group_size, int(w.has_zeros), int(w.gated),
