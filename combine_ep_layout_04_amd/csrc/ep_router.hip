@@ -29,9 +29,10 @@
 // lanes and a wavefront works on four rows.  Every reduction is a butterfly
 // inside the LPR lanes, in registers (lane moves of the DPP kind up to 16
 // lanes), and the k best are taken one at a time, each round a scan of the
-// lane's own values and one butterfly.  Those rounds bound it: 8192 tokens of
-// 256 fp32 logits take 7.8 us, 10.4 with all scores written (17 MB, 3.5 us of
-// copying), the backward 8.2.
+// lane's own values and one butterfly for the largest value, another for the
+// lowest expert that has it.  Those rounds bound it: 8192 tokens of 256 fp32
+// logits take 6.3 us, 9.0 with all scores written (17 MB, 3.5 us of copying),
+// the backward 8.1.
 
 #include "ep_internal.h"
 #include "ep_types.h"
@@ -80,27 +81,22 @@ __device__ __forceinline__ S row_sum(S v)
     if constexpr (STEP < LPR) return row_sum<LPR, STEP * 2>(v + exchange<STEP>(v));
     else return v;
 }
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return __builtin_fmax(a, b); }
 template <int LPR, int STEP = 1, typename S>
 __device__ __forceinline__ S row_max(S v)
 {
-    if constexpr (STEP < LPR) {
-        const S o = exchange<STEP>(v);
-        return row_max<LPR, STEP * 2>(o > v ? o : v);
-    } else {
-        return v;
-    }
+    if constexpr (STEP < LPR) return row_max<LPR, STEP * 2>(larger(v, exchange<STEP>(v)));
+    else return v;
 }
-// the larger key, ties to the lower index
-template <int LPR, int STEP = 1, typename S>
-__device__ __forceinline__ void row_best(S& key, uint32_t& idx)
+template <int LPR, int STEP = 1>
+__device__ __forceinline__ uint32_t row_min(uint32_t v)
 {
     if constexpr (STEP < LPR) {
-        const S ok = exchange<STEP>(key);
-        const uint32_t oi = exchange<STEP>(idx);
-        const bool take = ok > key || (ok == key && oi < idx);
-        key = take ? ok : key;
-        idx = take ? oi : idx;
-        row_best<LPR, STEP * 2>(key, idx);
+        const uint32_t o = exchange<STEP>(v);
+        return row_min<LPR, STEP * 2>(o < v ? o : v);
+    } else {
+        return v;
     }
 }
 // the two largest of a >= b and c >= d
@@ -304,17 +300,20 @@ void router_kernel(const T* __restrict__ logits, int64_t num_tokens, int E, int6
 #pragma unroll
     for (int q = 0; q < kSel; ++q) sel[q] = -1;
     for (int j = 0; j < k; ++j) {
+        // the largest value of the row, then the lowest expert that has it
         Key best = (Key)kNegInf;
-        uint32_t at = 0xFFFFFFFFu;
 #pragma unroll
         for (int i = 0; i < VV; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const bool take = val[i][c] > best;
-                best = take ? val[i][c] : best;
-                at = take ? (uint32_t)((i * LPR + lr) * 4 + c) : at;
-            }
-        row_best<LPR>(best, at);
+            for (int c = 0; c < 4; ++c) best = larger(best, val[i][c]);
+        best = row_max<LPR>(best);
+        uint32_t at = 0xFFFFFFFFu;
+#pragma unroll
+        for (int i = VV - 1; i >= 0; --i)
+#pragma unroll
+            for (int c = 3; c >= 0; --c)
+                at = val[i][c] == best ? (uint32_t)((i * LPR + lr) * 4 + c) : at;
+        at = row_min<LPR>(at);
 #pragma unroll
         for (int i = 0; i < VV; ++i)
 #pragma unroll
@@ -538,10 +537,11 @@ void router_backward_kernel(const T* __restrict__ logits, int64_t num_tokens, in
 // 16 experts, 16 up to 256, 64 beyond.  Few rows leave the chip idle and only
 // the length of the chain counts: then 65 to 256 experts take 64 lanes too.
 // Measured on MI355X, us in a graph, 16 against 64 lanes: 256 experts, 1
-// token 6.5 / 5.7 (sigmoid, bias, 8 groups: 14.8 / 8.3), 2048 tokens 7.2 /
-// 6.9 (17.4 / 10.3), 8192 tokens 7.8 / 13.6; 96 experts, 1 token 5.4 / 5.9
-// (12.4 / 11.1), 2048 tokens 6.1 / 7.0 (14.2 / 15.1); the backward at 256
-// experts, 1 token 4.3 / 3.0, 8192 tokens 5.4 / 6.3.
+// token 4.9 / 3.6 (sigmoid, bias, 8 groups: 12.9 / 6.3), 2048 tokens 5.4 /
+// 4.9 (13.9 / 8.3), 8192 tokens 6.3 / 11.1 (17.5 / 19.2); 96 experts, 1 token
+// 4.0 / 3.8 (11.2 / 9.1), 1024 tokens 4.4 / 4.2 (11.6 / 9.6), 2048 tokens 4.5
+// / 4.9 (11.6 / 12.7); the backward at 256 experts, 1 token 4.3 / 2.9, 8192
+// tokens 5.4 / 6.3.
 template <typename F>
 hipError_t with_row_shape(int E, int64_t num_tokens, F&& f)
 {
