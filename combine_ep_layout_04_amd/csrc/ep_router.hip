@@ -424,10 +424,21 @@ void router_backward_kernel(const T* __restrict__ logits, int64_t num_tokens, in
     if (renormalize) {
         ms = row_max<LPR>(ms);
         ms = ms == kNegInf ? 0.0f : ms;
+        // Scores relative to the largest chosen one, so that they do not
+        // vanish in fp32 where the forward's 64 bits hold them.  Sigmoid with
+        // all chosen logits below 0: exp(l - ms) / (1 + exp(l)), the score
+        // over exp(ms).  Where the forward's scores are 0 (exp(-ms) is past
+        // the largest double) so are its weights, and these.
+        const bool below = !softmax && ms < 0.0f;
+        const bool zero = below && (double)ms < -709.782712893384;
         float s[kSel], sum = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int q = 0; q < kSel; ++q) {
-            s[q] = sel[q] < 0 ? 0.0f : softmax ? expf(ls[q] - ms) : 1.0f / (1.0f + expf(-ls[q]));
+            s[q] = 0.0f;
+            if (q * LPR >= k) continue;         // no choice here in any row
+            s[q] = softmax || below ? expf(ls[q] - ms) : 1.0f;
+            if (!softmax) s[q] /= 1.0f + expf(below ? ls[q] : -ls[q]);
+            if (sel[q] < 0 || zero) s[q] = 0.0f;
             sum += s[q];
             dot = __builtin_fmaf(s[q], gw[q], dot);
         }
@@ -436,6 +447,8 @@ void router_backward_kernel(const T* __restrict__ logits, int64_t num_tokens, in
         const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
         for (int q = 0; q < kSel; ++q) {
+            direct[q] = 0.0f;
+            if (q * LPR >= k) continue;
             direct[q] = s[q] * inv * (gw[q] - dot * inv);
             if (!softmax) direct[q] *= 1.0f / (1.0f + expf(ls[q]));    // 1 - score
             if (sel[q] < 0) direct[q] = 0.0f;
