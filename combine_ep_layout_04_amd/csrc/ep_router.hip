@@ -9,8 +9,11 @@
 //            without a bias by logit, which orders like the score
 //   weight_j = scale * score_ij [ / sum_j score_ij ]
 //
-// A logit of -inf or NaN, or a bias that makes the value -inf or NaN, takes
-// the expert out: it is never chosen and its score is 0.
+// A logit of -inf or NaN takes the expert out: it is never chosen and its
+// score is 0.  A value of -inf or NaN keeps it from being chosen, wherever
+// values steer the choice (a bias, or groups rated by two).  With a logit of
+// +inf all softmax scores of its row are NaN, and so are the weights of what
+// is chosen by logit; by value nothing is left to choose.
 //
 // Backward, with r_j the renormalised weights and the choice held constant:
 //   renormalised:  d logit_ij += scale * r_j (g_j - sum r g) * (softmax: 1,
@@ -137,6 +140,16 @@ __device__ __forceinline__ void load4(const T* row, int e, int E, float (&f)[4])
     for (int c = 0; c < 4; ++c) f[c] = f[c] == f[c] ? f[c] : kNegInf;
 }
 
+// A row of logits for a second reading by few: hidden from the compiler that
+// it is the same, which would hold the first reading's values for all (8192 x
+// 512 with a bias: 48.3 us against 44.8).
+template <typename T>
+__device__ __forceinline__ const T* read_again(const T* row)
+{
+    asm("" : "+v"(row));
+    return row;
+}
+
 // WIDE: 64-bit values (score + bias) rate the groups and, with a bias, make the
 // choice; else both are by the logits.
 template <typename T, int LPR, int VV, bool WIDE>
@@ -161,7 +174,7 @@ void router_kernel(const T* __restrict__ logits, int64_t num_tokens, int E, int6
     for (int i = 0; i < VV; ++i) load4(x, (i * LPR + lr) * 4, E, l[i]);
 
     // softmax statistics: m the largest logit (0 for a row with none left),
-    // z the sum of exp(l - m)
+    // z the sum of exp(l - m), NaN where m is +inf
     float m = 0.0f;
     if (softmax) {
         m = kNegInf;
@@ -185,14 +198,15 @@ void router_kernel(const T* __restrict__ logits, int64_t num_tokens, int E, int6
                 z += d;
             }
         if (softmax) z = row_sum<LPR>(z);
-        const double inv = softmax ? 1.0 / (z > 0 ? z : 1.0) : 1.0;
+        const double inv = softmax ? 1.0 / (z == 0 ? 1.0 : z) : 1.0;
 #pragma unroll
         for (int i = 0; i < VV; ++i) {
             const int e = (i * LPR + lr) * 4;
             if (probs != nullptr && live) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    if (e + c < E) probs[row * E + e + c] = (float)(val[i][c] * inv);
+                    if (e + c < E)
+                        probs[row * E + e + c] = l[i][c] > kNegInf ? (float)(val[i][c] * inv) : 0.0f;
             }
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -217,17 +231,19 @@ void router_kernel(const T* __restrict__ logits, int64_t num_tokens, int E, int6
                 }
             if (softmax) z = row_sum<LPR>(z);
             if (probs != nullptr && live) {
-                const float inv = softmax ? 1.0f / (z > 0.0f ? z : 1.0f) : 1.0f;
+                const float inv = softmax ? 1.0f / (z == 0 ? 1.0f : z) : 1.0f;
 #pragma unroll
                 for (int i = 0; i < VV; ++i) {
                     const int e = (i * LPR + lr) * 4;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) p[i][c] = l[i][c] > kNegInf ? p[i][c] * inv : 0.0f;
                     if (e + 4 <= E && (E & 3) == 0) {
                         *reinterpret_cast<float4*>(probs + row * E + e) =
-                            make_float4(p[i][0] * inv, p[i][1] * inv, p[i][2] * inv, p[i][3] * inv);
+                            make_float4(p[i][0], p[i][1], p[i][2], p[i][3]);
                     } else {
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
-                            if (e + c < E) probs[row * E + e + c] = p[i][c] * inv;
+                            if (e + c < E) probs[row * E + e + c] = p[i][c];
                     }
                 }
             }
@@ -297,12 +313,8 @@ void router_kernel(const T* __restrict__ logits, int64_t num_tokens, int E, int6
         if constexpr (WIDE) {
             if (bias == nullptr) {
                 // the scores have rated the groups; the choice is by logit,
-                // also among scores that are the same number.  The logits are
-                // read again (the pointer hides that they are the same): held
-                // since the start they slow the rows with a bias (8192 x 512:
-                // 48.3 us against 44.8).
-                const T* again = x;
-                asm("" : "+v"(again));
+                // also among scores that are the same number
+                const T* again = read_again(x);
 #pragma unroll
                 for (int i = 0; i < VV; ++i) {
                     float f[4];
@@ -456,6 +468,7 @@ void router_backward_kernel(const T* __restrict__ logits, int64_t num_tokens, in
     }
 
     float out[VV][4];
+    float whole = 0.0f;             // the softmax's sum: NaN in a row with a logit of +inf
     const bool dense = grad_probs != nullptr || !renormalize;
     if (dense) {
         float l[VV][4], b[VV][4];
@@ -515,6 +528,7 @@ void router_backward_kernel(const T* __restrict__ logits, int64_t num_tokens, in
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     out[i][c] = l[i][c] != 0.0f ? l[i][c] * inv * (b[i][c] - dot * inv) : 0.0f;
+            whole = z;
         } else {
 #pragma unroll
             for (int i = 0; i < VV; ++i)
@@ -550,6 +564,16 @@ void router_backward_kernel(const T* __restrict__ logits, int64_t num_tokens, in
     }
     if (!live) return;
     T* o = grad_logits + row * E;
+    if (whole != whole) {           // every gradient of the row, its masked experts apart
+        for (int i = 0; i < VV; ++i) {
+            const int e = (i * LPR + lr) * 4;
+            float f[4];
+            load4(x, e, E, f);
+            for (int c = 0; c < 4; ++c)
+                if (e + c < E) o[e + c] = from_float<T>(f[c] > kNegInf ? whole : 0.0f);
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < VV; ++i) {
         const int e = (i * LPR + lr) * 4;

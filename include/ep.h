@@ -775,10 +775,13 @@ typedef enum {
  *   weight_j = scale * score_j, over the sum of the chosen scores if
  *   renormalize (0 if that sum is 0).
  *
- * A logit of -inf or NaN, or a bias making the value -inf or NaN, takes the
- * expert out: it is not chosen; its score is 0 (masked logits).  Where fewer
+ * A logit of -inf or NaN takes the expert out: it is not chosen and its score
+ * is 0 (masked logits).  Where values steer the choice (a bias, or group_top
+ * 2), an expert whose value is -inf or NaN is not chosen either.  Where fewer
  * than num_topk experts are left, the rest of the row is -1 with weight 0.
- * A logit of +inf gives NaN softmax scores, as the formula does.
+ * A logit of +inf makes all softmax scores of its row NaN, as the formula
+ * does: where the choice is by logit its expert comes first and the chosen
+ * weights are NaN; where values steer it, none is left (-1, weight 0).
  *
  * In:  logits   dtype [num_tokens, num_experts], row stride ld_logits
  *               elements, aligned to the element.

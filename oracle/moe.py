@@ -35,7 +35,8 @@ def router(logits: np.ndarray, k: int, score: str = "softmax", bias=None, num_gr
         on = logits[t] > NEG
         value = probs[t] + (0.0 if bias is None else np.asarray(bias, dtype=np.float64))
         by_value = bias is not None
-        on = on & (value > NEG)
+        if by_value or (num_groups > 1 and group_top > 1):   # values steer: False for NaN
+            on = on & (value > NEG)
         rank = value if by_value else logits[t]
         allowed = on.copy()
         if num_groups > 1:
@@ -60,7 +61,8 @@ def router(logits: np.ndarray, k: int, score: str = "softmax", bias=None, num_gr
                 l = logits[t, order]
                 w[t, :len(order)] = np.exp(l - l.max()) if len(order) else 0.0
             s = w[t].sum()
-            w[t] = w[t] / s if s > 0 else 0.0
+            if s != 0:                                       # NaN with a logit of +inf
+                w[t, :len(order)] /= s
     return idx, w * scale, probs
 
 
@@ -87,7 +89,8 @@ def router_backward(logits, topk_idx, grad_weights, grad_probs=None, score: str 
             for j, gj in zip(at, g):
                 gp[t, topk_idx[t, j]] += gj
     if score == "softmax":
-        return direct + p * (gp - (p * gp).sum(1, keepdims=True))
+        # NaN throughout a row with a logit of +inf, its masked experts apart
+        return direct + np.where(logits > NEG, p * (gp - (p * gp).sum(1, keepdims=True)), 0.0)
     return direct + p * (1.0 - p) * gp
 
 
