@@ -21,8 +21,14 @@
 //   * the 16 and the zero point leave again per group, by
 //     sum (16 + n) x - (16 + z) sum x, with sum x from the same matrix
 //     instruction on a row of ones.  Codes, 16 + n and ones are exact in 16
-//     bits and all sums are fp32; the subtraction costs at most 5 of fp32's
-//     24 bits, against 8 or 11 in the result;
+//     bits and all sums are fp32: what the subtraction leaves is off by fp32
+//     roundings of sum (32 + n + z) |x|, at most 62 scale sum |x| for the
+//     result, however near to each other codes and zero points are;
+//   * in bf16 both rows are taken 2^-12 times, and the result 2^12 times at
+//     the end: 128 terms of at most 31 / 4096 x then stay below the largest
+//     float for every finite x, where 31 x passed it from 1e37 on.  Nothing is
+//     lost at the other end: the matrix instruction keeps subnormal numbers,
+//     and a 2^-149 is 2^-137 in the result, under bf16's smallest step;
 //   * the scale is applied once per group, to the fp32 sum.
 //
 // Layout of the packed weights (made once by ep_w4_pack): tiles of 16 rows
@@ -54,18 +60,21 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 fp16x8_t __attribute__((ext_vector_type(8)));
 
 // 16 + n as a 16-bit float: the code's place in the mantissa, the exponent
-// of 16, and the float 1.0 (twice each: two weights a word).
+// of 16, and the float 1.0 (twice each: two weights a word), all in units of
+// 1 / kUnit.
 template <typename T>
 struct Code;
 template <>
 struct Code<Bf16> {
     static constexpr int kShift = 3;
-    static constexpr uint32_t kMask = 0x00780078u, kBase = 0x41804180u, kOnes = 0x3F803F80u;
+    static constexpr uint32_t kMask = 0x00780078u, kBase = 0x3B803B80u, kOnes = 0x39803980u;
+    static constexpr float kUnit = 4096.0f;
 };
 template <>
 struct Code<Fp16> {
     static constexpr int kShift = 6;
     static constexpr uint32_t kMask = 0x03C003C0u, kBase = 0x4C004C00u, kOnes = 0x3C003C00u;
+    static constexpr float kUnit = 1.0f;
 };
 
 __device__ __forceinline__ f32x4_t mma(const uint4& a, const uint4& b, f32x4_t c, const Bf16*)
@@ -101,6 +110,8 @@ struct Unpacker {
 
 // v / (1 + exp(-v)) by the hardware's exponential and reciprocal (one unit in
 // the last place each; rounding the exponent's argument adds |v| * 2^-24).
+// Below about -87, where 1 / (1 + exp(-v)) has no normal float, 0 for a value
+// under 1e-35.
 __device__ __forceinline__ float silu(float v)
 {
     return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896f * v));
@@ -370,9 +381,10 @@ void w4_kernel(const T* __restrict__ x, int64_t ldx, int64_t x_rows, const int32
                 v += part[((w * kJoin + j) * CT + c) * 64 + ol];
                 if constexpr (GLU) u += part[((w * kJoin + 1) * CT + c) * 64 + ol];
             }
-            float f[4] = {v.x, v.y, v.z, v.w};
+            constexpr float kUnit = Code<T>::kUnit;
+            float f[4] = {v.x * kUnit, v.y * kUnit, v.z * kUnit, v.w * kUnit};
             if constexpr (GLU) {
-                const float up[4] = {u.x, u.y, u.z, u.w};
+                const float up[4] = {u.x * kUnit, u.y * kUnit, u.z * kUnit, u.w * kUnit};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) f[i] = silu(f[i]) * up[i];
             }

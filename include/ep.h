@@ -900,8 +900,9 @@ ep_status_t ep_w4_pack(const void *codes, const void *scales, const void *zeros,
  *               if gated, row stride ld_out.  Rows that belong to no expert
  *               are not written.
  * Sums are fp32, in a fixed order; the result (after the gated activation,
- * in fp32) is rounded once.  num_rows bounds every row: rows past it are
- * neither read nor written; src outside [0, num_x_rows) reads row 0.
+ * in fp32) is rounded once.  A row of x that holds an infinity or a NaN gives
+ * NaN in its own row of the result.  num_rows bounds every row: rows past it
+ * are neither read nor written; src outside [0, num_x_rows) reads row 0.
  */
 ep_status_t ep_expert_matmul_w4(const void *x, int dtype, int64_t ld_x, int64_t num_x_rows,
                                 const int32_t *src, const void *packed, size_t packed_bytes,
