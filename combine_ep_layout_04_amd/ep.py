@@ -1082,9 +1082,14 @@ def _need_on(t, name, dtype, device, numel=None):
         raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
+def _stream_handle(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
 # the current stream's handle without a Stream object: 0.1 us against 1.8 of
-# the 10 that a call takes on the host
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# the 10 that a call takes on the host.  The name is torch's own and may be
+# missing from a build: then through the Stream.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_handle)
 
 
 class _On:
