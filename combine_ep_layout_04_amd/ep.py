@@ -1253,7 +1253,10 @@ def ep_permute_backward(grad_rows: torch.Tensor, slot: torch.Tensor,
                         x: Optional[torch.Tensor] = None, *, grad_x=None, grad_weights=None,
                         stream=None):
     """Backward of ep_permute: (grad_x [T, H], grad_weights fp32 [T, k]); the
-    latter None unless ``topk_weights`` and ``x`` are given."""
+    latter None unless ``topk_weights`` and ``x`` are given, which a
+    ``grad_weights`` buffer needs."""
+    if grad_weights is not None and (topk_weights is None or x is None):
+        raise ValueError("grad_weights needs topk_weights and x")
     ld = _rows_of(grad_rows, "grad_rows")
     R, H = grad_rows.shape
     dev, dt = grad_rows.device, grad_rows.dtype
@@ -1261,7 +1264,7 @@ def ep_permute_backward(grad_rows: torch.Tensor, slot: torch.Tensor,
     on = _On(dev, stream)
     ld_x = 0
     if topk_weights is None or x is None:
-        x = grad_weights = None
+        x = None
     else:
         ld_x = _rows_of(x, "x", dt, H, dev)
         if x.shape[0] != T:
@@ -1308,8 +1311,11 @@ def ep_unpermute_backward(grad_out: torch.Tensor, slot: torch.Tensor,
                           y: Optional[torch.Tensor] = None, *, rows: Optional[int] = None,
                           grad_y=None, grad_weights=None, clear=None, stream=None):
     """Backward of ep_unpermute: (grad_y [rows, H], grad_weights fp32 [T, k]);
-    the latter None unless ``topk_weights`` and ``y`` are given.  ``rows`` and
-    ``clear`` as in ep_permute (``rows`` is y's with ``y``)."""
+    the latter None unless ``topk_weights`` and ``y`` are given, which a
+    ``grad_weights`` buffer needs.  ``rows`` and ``clear`` as in ep_permute
+    (``rows`` is y's with ``y``)."""
+    if grad_weights is not None and (topk_weights is None or y is None):
+        raise ValueError("grad_weights needs topk_weights and y")
     ld = _rows_of(grad_out, "grad_out")
     T, H = grad_out.shape
     dev, dt = grad_out.device, grad_out.dtype
@@ -1319,7 +1325,7 @@ def ep_unpermute_backward(grad_out: torch.Tensor, slot: torch.Tensor,
     if y is not None and rows is None:
         rows = y.shape[0]
     if topk_weights is None or y is None:
-        y = grad_weights = None
+        y = None
     else:
         ld_y = _rows_of(y, "y", dt, H, dev)
         if grad_weights is None:

@@ -27,3 +27,21 @@ def test_stream_handles():
     for stream in (torch.cuda.current_stream(), torch.cuda.Stream()):
         with torch.cuda.stream(stream):
             assert ep._raw_stream(0) == ep._stream_handle(0) == stream.cuda_stream
+
+
+def test_a_weights_gradient_needs_weights_and_rows():
+    # refused before anything is looked at on a device
+    rows, w = torch.zeros(4, 8), torch.zeros(4, 2)
+    slot = torch.zeros(4, 2, dtype=torch.int32)
+    grad = torch.zeros(4, 2)
+    for kw in (dict(), dict(topk_weights=w), dict(x=rows)):
+        with pytest.raises(ValueError, match="grad_weights needs topk_weights and x"):
+            ep.ep_permute_backward(rows, slot, grad_weights=grad, **kw)
+    for kw in (dict(), dict(topk_weights=w), dict(y=rows)):
+        with pytest.raises(ValueError, match="grad_weights needs topk_weights and y"):
+            ep.ep_unpermute_backward(rows, slot, grad_weights=grad, **kw)
+    # with both the tensors are looked at
+    with pytest.raises(ValueError, match="device tensor"):
+        ep.ep_permute_backward(rows, slot, w, rows, grad_weights=grad)
+    with pytest.raises(ValueError, match="device tensor"):
+        ep.ep_unpermute_backward(rows, slot, w, rows, grad_weights=grad)
