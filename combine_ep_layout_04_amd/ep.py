@@ -1050,7 +1050,9 @@ def ep_dispatch_ranked_backward(sparse_to_dense: torch.Tensor, num_experts: int,
 # -------------------------------------- router, row movement, 4-bit products --
 # Outputs that are not given are allocated with torch on the stream of the
 # call; every tensor of a call lives on one device, which need not be the
-# current one.
+# current one.  No call takes part in torch's autograd: outputs carry no
+# gradient function whatever their inputs require, and each backward is a call
+# of its own.
 
 def _rows_of(t: torch.Tensor, name: str, dtype: Optional[torch.dtype] = None,
              cols: Optional[int] = None, device=None) -> int:
@@ -1145,7 +1147,8 @@ def ep_router(logits: torch.Tensor, num_topk: int, *, score: str = "softmax",
     ``renormalize``, times ``scale``.
 
     Returns (topk_idx int64 [T, k], -1 where no expert is left, topk_weights
-    fp32 [T, k], probs fp32 [T, E] or None).
+    fp32 [T, k], probs fp32 [T, E] or None), all outside autograd: their
+    gradient is ep_router_backward.
     """
     ld = _rows_of(logits, "logits")
     T, E = logits.shape
@@ -1229,7 +1232,8 @@ def ep_permute(x: torch.Tensor, slot: torch.Tensor, topk_weights: Optional[torch
 
     ``rows`` (T*k by default) is the layout's row bound.  ``clear`` =
     (counts, offsets) of the layout clears the rows that no slot names; else
-    they are not written.  Returns out [rows, H]."""
+    they are not written.  Returns out [rows, H], outside autograd: its
+    gradient is ep_permute_backward."""
     ld = _rows_of(x, "x")
     T, H = x.shape
     dev = x.device
@@ -1289,7 +1293,8 @@ def ep_unpermute(y: torch.Tensor, slot: torch.Tensor, topk_weights: Optional[tor
                  *, out=None, stream=None):
     """Rows back in token order: ``out[t] = sum_j topk_weights[t, j] *
     y[slot[t, j]]``, in fp32, j ascending.  ``y`` is bf16 / fp16 / fp32
-    [rows, H], of any width, rows may be strided.  Returns out [T, H]."""
+    [rows, H], of any width, rows may be strided.  Returns out [T, H], outside
+    autograd: its gradient is ep_unpermute_backward."""
     ld = _rows_of(y, "y")
     R, H = y.shape
     dev = y.device
@@ -1413,8 +1418,8 @@ def ep_expert_matmul_w4(x: torch.Tensor, weights: W4Weights, offsets: Optional[t
 
     ``x`` has the scales' type and may have strided rows; ``offsets`` may be
     left out with one expert.  ``rows`` is the layout's row bound (src's
-    length, or x's rows).  Returns out [rows, N] (N/2 if gated); rows of no
-    expert are not written."""
+    length, or x's rows).  Returns out [rows, N] (N/2 if gated), outside
+    autograd and without a backward call; rows of no expert are not written."""
     w = weights
     ld = _rows_of(x, "x", w.dtype, w.in_features)
     dev = x.device
