@@ -9,6 +9,7 @@
 
 #include "ep.h"
 #include "ep_internal.h"
+#include "ep_layer.h"
 
 static_assert(EP_LAYOUT_NOALLOC_SCRATCH_BYTES == ep::kLayoutScratchBytes,
               "the header states the layout scratch size");

@@ -36,6 +36,7 @@
 
 #include "ep_device.h"
 #include "ep_internal.h"
+#include "ep_layer.h"
 #include "ep_types.h"
 
 namespace ep {

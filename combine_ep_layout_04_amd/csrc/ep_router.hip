@@ -38,6 +38,7 @@
 // the backward 8.1.
 
 #include "ep_internal.h"
+#include "ep_layer.h"
 #include "ep_types.h"
 
 namespace ep {

@@ -51,6 +51,7 @@
 
 #include "ep_device.h"
 #include "ep_internal.h"
+#include "ep_layer.h"
 #include "ep_types.h"
 
 namespace ep {
