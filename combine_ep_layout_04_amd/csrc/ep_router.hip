@@ -34,8 +34,10 @@
 // lanes), and the k best are taken one at a time, each round a scan of the
 // lane's own values and one butterfly for the largest value, another for the
 // lowest expert that has it.  Those rounds bound it: 8192 tokens of 256 fp32
-// logits take 6.3 us, 9.0 with all scores written (17 MB, 3.5 us of copying),
-// the backward 8.1.
+// logits, k 8, take 6.3 us, 8.8 with all scores written (17 MB, 2.6 us of
+// copying), and 16.8 with sigmoid, a bias and 8 groups, where the rounds scan
+// 64-bit values and every score is a 64-bit exponential; the backward of the
+// softmax with all scores 8.1.
 
 #include "ep_internal.h"
 #include "ep_layer.h"
@@ -594,12 +596,13 @@ void router_backward_kernel(const T* __restrict__ logits, int64_t num_tokens, in
 // f(lanes per row, vectors per lane) for a row of E experts: 4 lanes up to
 // 16 experts, 16 up to 256, 64 beyond.  Few rows leave the chip idle and only
 // the length of the chain counts: then 65 to 256 experts take 64 lanes too.
-// Measured on MI355X, us in a graph, 16 against 64 lanes: 256 experts, 1
-// token 4.9 / 3.6 (sigmoid, bias, 8 groups: 12.9 / 6.3), 2048 tokens 5.4 /
-// 4.9 (13.9 / 8.3), 8192 tokens 6.3 / 11.1 (17.5 / 19.2); 96 experts, 1 token
-// 4.0 / 3.8 (11.2 / 9.1), 1024 tokens 4.4 / 4.2 (11.6 / 9.6), 2048 tokens 4.5
-// / 4.9 (11.6 / 12.7); the backward at 256 experts, 1 token 4.3 / 2.9, 8192
-// tokens 5.4 / 6.3.
+// Measured on MI355X, us in a graph, 16 against 64 lanes, in brackets with
+// sigmoid, a bias and 8 groups: 256 experts, 1 token 5.0 / 3.7 (12.9 / 6.1),
+// 2048 tokens 5.4 / 4.9 (13.7 / 8.3), 4096 5.5 / 6.8 (13.9 / 11.1), 8192 6.4 /
+// 11.0 (17.0 / 18.5); 128 experts, 1024 tokens 4.3 / 4.2 (8.6 / 6.6), 2048 4.4
+// / 4.9 (8.7 / 8.1); 96 experts, 1 token 4.0 / 3.8 (11.1 / 9.1), 1024 tokens
+// 4.4 / 4.2 (11.6 / 9.6), 2048 4.4 / 4.9 (11.6 / 12.5); the backward at 256
+// experts, 1 token 4.3 / 3.0, 2048 4.8 / 3.6, 4096 5.1 / 4.5, 8192 5.4 / 6.4.
 template <typename F>
 hipError_t with_row_shape(int E, int64_t num_tokens, F&& f)
 {

@@ -546,20 +546,56 @@ hipError_t w4_launch(const W4Args& a, const W4Shape& s, int64_t items, int waves
 // blocks the grid has to make (row blocks of the weights times items).  More
 // row blocks a workgroup read x less often and join less; more wavefronts
 // and smaller workgroups give a small grid enough loads in flight.  Measured
-// on MI355X, weights not in the caches, us (bf16, groups of 128, RT x CT x
-// wavefronts):
-//   129024 blocks (64 tokens x 8 of 256, 2048 -> 7168)     8x1x2 290   4x1x2 298   4x1x4 331   2x1x4 398
-//     2048 blocks (1 token x 8 of 256, 7168 -> 2 x 2048)   8x1x4  31   4x1x4  27   2x1x4  31
-//     1068 blocks (3 x 4 of 64, 2048 -> 1411, groups 32)   4x1x4  12   2x1x4  10   2x1x8  13
-//      256 blocks (1 row, 1 expert, 8192 -> 4096)          2x1x4  13   2x1x8   9   2x1x16  9
-//    33792 blocks (64 rows an expert, 2048 -> 2 x 1408)    8x2x1 110   4x2x1 135   8x1x1 128   4x4x1 157
-//     7040 blocks (128 rows an expert, 8 experts)          8x2x1  33   8x2x2  31   8x2x4  36   4x2x1  37
-//     4352 blocks (512 rows, 1 expert, 4096 -> 4096)       8x2x2  45   8x2x4  32   4x2x4  42
-//     2816 blocks (32 rows an expert, 8 experts)           8x2x4  17   4x2x4  17   2x2x4  20
-//      768 blocks (64 rows, 1 expert, 4096 -> 4096)        4x2x8  14   2x2x8  12   2x2x16 13
-// Groups of 32 and 64 hold 2 to 4 times the scales of a row block: eight
-// row blocks do not fit the registers, four took 532 us against 603 (64
-// tokens) and 233 against 808 with two blocks of rows (512 tokens).
+// on MI355X in a graph, us, RT x CT x wavefronts, bf16, the weights in copies
+// that hold 0.8 GB or more together, so not in the caches; groups of 128, in
+// brackets with zero points.  The rule's choice stands first.
+//   at most 16 rows an expert:
+//      256 blocks (1 row, 8192 -> 4096)          2x1x16 10 [11]   2x1x4 16 [16]   4x1x4 20 [20]
+//      448        (1 row, 8192 -> 7168)          2x1x16 11 [12]   2x1x4 16 [17]
+//      576        (1 row, 8192 -> 9216)          2x1x4 18 [18]   2x1x16 19 [20]   2x1x8 17 [17]
+//     1496        (2 x 8 of 64, 2048 -> 1408)    2x1x4 10 [11]   4x1x4 11 [11]
+//     2176        (2 x 8 of 64, 2048 -> 2048)    4x1x4 12 [12]   2x1x4 13 [13]
+//    30720        (64 x 8 of 64, 2048 -> 5120)   4x1x4 76 [80]   8x1x2 79 [83]
+//    35328        (64 x 8 of 64, 2048 -> 5888)   8x1x2 83 [92]   4x1x4 86 [90]
+//   129024        (64 x 8 of 256, 2048 -> 7168)  8x1x2 296 [336]   4x1x4 329 [347]   4x1x1 299 [313]
+//   more than 16:
+//      768        (64 rows, 4096 -> 4096)        2x2x8 13 [13]   4x2x4 15 [16]
+//     1344        (64 rows, 4096 -> 7168)        2x2x8 21 [21]   4x2x4 16 [16]
+//     1728        (64 rows, 4096 -> 9216)        4x2x4 24 [25]   2x2x8 29 [30]   8x2x4 22 [22]
+//     3584        (64 x 2 of 4, 2048 -> 7168)    4x2x4 22 [22]   8x2x4 21 [28]
+//     4352        (512 rows, 4096 -> 4096)       8x2x4 33 [42]   4x2x4 42 [44]   8x2x2 46 [37]
+//     5760        (512 x 2 of 8, 2048 -> 2304)   8x2x4 34 [42]   8x2x2 31 [42]   4x2x4 33 [34]
+//     7040        (512 x 2 of 8, 2048 -> 2816)   8x2x2 34 [43]   8x2x4 38 [53]   4x2x4 39 [40]
+//    14080        (512 x 2 of 8, 2048 -> 5632)   8x2x2 61 [79]   8x2x1 55 [71]
+//    16896        (512 x 8 of 64, 2048 -> 1408)  8x2x1 61 [75]   8x2x2 67 [83]   4x2x4 78 [79]
+//    33792        (512 x 8 of 64, 2048 -> 2816)  8x2x1 119 [144]   8x2x2 120 [144]
+// So the borders are good to a few per cent but for grids just below 1536,
+// between 4096 and 6144 and between 10000 and 16384, where a neighbour is up
+// to a quarter faster; with zero points, which take the 8 x 2 tile from two
+// wavefronts a SIMD to one, 4 x 2 would be up to a quarter faster between
+// 4608 and 14080 blocks.
+//
+// Groups of 32 and 64 hold 2 to 4 times the scales of a row block: eight row
+// blocks do not fit the registers.  Groups of 64, of 32 and of 32 with zero
+// points:
+//     3808 blocks (2 x 8 of 64, 2048 -> 3584)    2x1x4 19, 22, 25   4x1x4 19, 23, 28
+//     4352        (2 x 8 of 64, 2048 -> 4096)    4x1x4 21, 24, 29   2x1x4 21, 24, 29
+//    24576        (64 x 8 of 64, 2048 -> 4096)   4x1x4 68, 87, 100   2x1x4 77, 89, 107
+//    30720        (64 x 8 of 64, 2048 -> 5120)   4x1x4 84, 111, 127   4x1x2 81, 100, 124
+//    35328        (64 x 8 of 64, 2048 -> 5888)   4x1x2 91, 112, 143   4x1x4 96, 126, 148
+//   129024        (64 x 8 of 256, 2048 -> 7168)  4x1x2 336, 423, 525   4x1x4 374, 486, 578   4x1x1 319, 401, 523
+//   more than 16 rows an expert:
+//     1344        (64 rows, 4096 -> 7168)        2x2x8 23, 25, 26   4x2x4 16, 19, 22
+//     1728        (64 rows, 4096 -> 9216)        4x2x4 25, 34, 40   2x2x8 33, 35, 37
+//     3584        (64 x 2 of 4, 2048 -> 7168)    4x2x4 25, 34, 37   4x2x1 25, 31, 36
+//     4608        (64 x 2 of 4, 2048 -> 9216)    4x2x1 26, 32, 37   4x2x4 27, 40, 48
+//    33792        (512 x 8 of 64, 2048 -> 2816)  4x2x1 154, 205, 241   2x2x2 213, 230, 247
+//
+// num_rows stands for the rows there are: in a padded layout it is their bound
+// only, and the split is that of a larger grid, most of whose workgroups find
+// no row and leave (8 of 256 experts, packed, aligned to 128 rows, 16 rows an
+// expert: 64 tokens 2048 -> 7168 300, 374, 305; 1 token 7168 -> 4096 28, 46,
+// 47; 512 tokens of 8 of 64, 2048 -> 2816, 96 rows an expert: 120, 121, 122).
 template <typename T, int GS, bool ZEROS, bool GLU>
 hipError_t w4_sized(const W4Args& a, const W4Shape& s, hipStream_t stream)
 {

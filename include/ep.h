@@ -896,6 +896,9 @@ ep_status_t ep_w4_pack(const void *codes, const void *scales, const void *zeros,
  *               expert (all rows).
  *      counts   int32 [num_experts] or NULL: rows of each expert (for aligned
  *               or fixed-stride layouts), else offsets[e + 1] - offsets[e].
+ *      num_rows  rows of the layout.  The launch is fitted to it, so a packed
+ *               layout, where it is the rows there are, is fastest; a padded
+ *               one of few rows takes up to 2.2 times as long.
  * Out: out      dtype [num_rows, out_features], or out_features / 2 columns
  *               if gated, row stride ld_out.  Rows that belong to no expert
  *               are not written.
