@@ -412,7 +412,9 @@ hipError_t move_of(const MoveArgs& a, hipStream_t stream)
 {
     if (a.gather) {
         // the fused pass holds a vector of all choices at once; more than 8
-        // take the sum and the dot products in two passes
+        // take the sum and the dot products in two passes, which read the
+        // rows twice (8192 x 4096 bf16, caches emptied: k 8 121 us, 103
+        // without dot products; k 9 226, 118; k 16 372, 196; k 64 1374, 714)
         if (a.grad_weights != nullptr && a.num_topk <= 8) return dot_of<T, FAST, kDotSum>(a, stream);
         hipError_t err = gather_of<T, FAST>(a, stream);
         if (err != hipSuccess || a.grad_weights == nullptr) return err;
