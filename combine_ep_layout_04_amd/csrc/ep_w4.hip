@@ -555,7 +555,7 @@ hipError_t w4_launch(const W4Args& a, const W4Shape& s, int64_t items, int waves
 //      576        (1 row, 8192 -> 9216)          2x1x4 18 [18]   2x1x16 19 [20]   2x1x8 17 [17]
 //     1496        (2 x 8 of 64, 2048 -> 1408)    2x1x4 10 [11]   4x1x4 11 [11]
 //     2176        (2 x 8 of 64, 2048 -> 2048)    4x1x4 12 [12]   2x1x4 13 [13]
-//    30720        (64 x 8 of 64, 2048 -> 5120)   4x1x4 76 [80]   8x1x2 79 [83]
+//    30.7 k       (64 x 8 of 64, 2048 -> 5120)   4x1x4 76 [80]   8x1x2 79 [83]
 //    35328        (64 x 8 of 64, 2048 -> 5888)   8x1x2 83 [92]   4x1x4 86 [90]
 //   129024        (64 x 8 of 256, 2048 -> 7168)  8x1x2 296 [336]   4x1x4 329 [347]   4x1x1 299 [313]
 //   more than 16:
@@ -581,7 +581,7 @@ hipError_t w4_launch(const W4Args& a, const W4Shape& s, int64_t items, int waves
 //     3808 blocks (2 x 8 of 64, 2048 -> 3584)    2x1x4 19, 22, 25   4x1x4 19, 23, 28
 //     4352        (2 x 8 of 64, 2048 -> 4096)    4x1x4 21, 24, 29   2x1x4 21, 24, 29
 //    24576        (64 x 8 of 64, 2048 -> 4096)   4x1x4 68, 87, 100   2x1x4 77, 89, 107
-//    30720        (64 x 8 of 64, 2048 -> 5120)   4x1x4 84, 111, 127   4x1x2 81, 100, 124
+//    30.7 k       (64 x 8 of 64, 2048 -> 5120)   4x1x4 84, 111, 127   4x1x2 81, 100, 124
 //    35328        (64 x 8 of 64, 2048 -> 5888)   4x1x2 91, 112, 143   4x1x4 96, 126, 148
 //   129024        (64 x 8 of 256, 2048 -> 7168)  4x1x2 336, 423, 525   4x1x4 374, 486, 578   4x1x1 319, 401, 523
 //   more than 16 rows an expert:
