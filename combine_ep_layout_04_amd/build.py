@@ -9,11 +9,13 @@ kept; packed-fp32 instruction selection disabled.
 
 from __future__ import annotations
 
+import concurrent.futures
 import glob
 import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -54,18 +56,32 @@ def sources():
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source into combine_ep_layout_04_amd/libep.so."""
+    """Compile every HIP source into combine_ep_layout_04_amd/libep.so, the
+    sources side by side."""
     tmp = LIB + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, f"-I{INCLUDE}", f"-I{CSRC}", "-o", tmp, *sources()]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
     noise = ("packed-fp32-ops", "--hip-link")
-    msgs = [ln for ln in (res.stdout + res.stderr).splitlines() if not any(n in ln for n in noise)]
-    if res.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
-    if verbose and msgs:
-        print("\n".join(msgs))
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        msgs = [ln for ln in (res.stdout + res.stderr).splitlines() if not any(n in ln for n in noise)]
+        if res.returncode != 0:
+            raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
+        if verbose and msgs:
+            print("\n".join(msgs))
+
+    flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory() as objs, \
+            concurrent.futures.ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+        def compile_one(src):
+            obj = os.path.join(objs, os.path.basename(src) + ".o")
+            run([hipcc(), *flags, f"-I{INCLUDE}", f"-I{CSRC}", "-c", src, "-o", obj])
+            return obj
+        # the largest first: they take longest
+        files = sorted(sources(), key=os.path.getsize, reverse=True)
+        run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp,
+             *sorted(pool.map(compile_one, files))])
     os.replace(tmp, LIB)
     return LIB
 

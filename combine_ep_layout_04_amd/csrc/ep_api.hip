@@ -8,6 +8,7 @@
 #include <stdio.h>
 
 #include "ep.h"
+#include "ep_expert.h"
 #include "ep_internal.h"
 #include "ep_layer.h"
 
@@ -1203,6 +1204,241 @@ ep_status_t ep_expert_matmul_w4(const void* x, int dtype, int64_t ld_x, int64_t 
         return fail(EP_UNSUPPORTED, "the product needs more than 2^31 workgroups");
     return from_hip(ep::launch_w4(dtype, a, static_cast<hipStream_t>(stream)),
                     "ep_expert_matmul_w4 launch");
+}
+
+// What the experts' products share: the shape and the rows.
+static ep_status_t check_expert(int num_experts, int out_features, int in_features, bool gated,
+                                const int32_t* offsets, const int32_t* counts, int64_t num_rows)
+{
+    if (num_experts < 1 || num_experts > EP_MAX_EXPERTS)
+        return fail(EP_INVALID_ARGUMENT, "num_experts %d outside [1, %d]", num_experts, EP_MAX_EXPERTS);
+    if (out_features < 1 || out_features > EP_MAX_OUT_FEATURES || (gated && out_features % 2 != 0))
+        return fail(EP_INVALID_ARGUMENT, "out_features %d outside [1, %d], or odd and gated",
+                    out_features, EP_MAX_OUT_FEATURES);
+    if (in_features < 1 || in_features > EP_MAX_HIDDEN)
+        return fail(EP_INVALID_ARGUMENT, "in_features %d outside [1, %d]", in_features, EP_MAX_HIDDEN);
+    if (num_rows < 0 || num_rows >= ((int64_t)1 << 31))
+        return fail(EP_INVALID_ARGUMENT, "num_rows %lld outside [0, 2^31)", (long long)num_rows);
+    if (!offsets && (num_experts != 1 || counts))
+        return fail(EP_INVALID_ARGUMENT, "offsets is required with more than one expert or counts");
+    if (off_by(offsets, 4) || off_by(counts, 4))
+        return fail(EP_INVALID_ARGUMENT, "offsets and counts must be 4-byte aligned");
+    return EP_SUCCESS;
+}
+
+static ep_status_t check_rows_of(const void* x, int64_t ld_x, int64_t num_x_rows, const int32_t* src,
+                                 int in_features, int dtype, int64_t num_rows)
+{
+    const ep_status_t st = check_matrix(x, ld_x, in_features, dtype, "x");
+    if (st) return st;
+    if (num_x_rows < 1 || (!src && num_x_rows < num_rows))
+        return fail(EP_INVALID_ARGUMENT, "x has %lld rows for %lld rows of the product",
+                    (long long)num_x_rows, (long long)num_rows);
+    if (off_by(src, 4)) return fail(EP_INVALID_ARGUMENT, "src must be 4-byte aligned");
+    return EP_SUCCESS;
+}
+
+static ep_status_t expert_forward(const void* x, int dtype, int64_t ld_x, int64_t num_x_rows,
+                                  const int32_t* src, const void* weights, int num_experts,
+                                  int out_features, int in_features, bool gated,
+                                  const int32_t* offsets, const int32_t* counts, int64_t num_rows,
+                                  void* out, int64_t ld_out, void* pre, int64_t ld_pre, void* stream,
+                                  const char* what)
+{
+    g_last_error[0] = '\0';
+    ep_status_t st = check_dtype(dtype, false);
+    if (st) return st;
+    st = check_expert(num_experts, out_features, in_features, gated, offsets, counts, num_rows);
+    if (st) return st;
+    if (num_rows == 0) return EP_SUCCESS;
+    st = check_rows_of(x, ld_x, num_x_rows, src, in_features, dtype, num_rows);
+    if (st) return st;
+    st = check_matrix(weights, in_features, in_features, dtype, "weights");
+    if (st) return st;
+    st = check_matrix(out, ld_out, gated ? out_features / 2 : out_features, dtype, "out");
+    if (st) return st;
+    if (pre) {
+        st = check_matrix(pre, ld_pre, out_features, dtype, "pre");
+        if (st) return st;
+    }
+    const ep::ExpertArgs a = {x, ld_x, num_x_rows, src, weights, num_experts, out_features, in_features,
+                              offsets, counts, num_rows, gated, out, ld_out, pre, ld_pre};
+    if (ep::expert_max_blocks(a) > INT32_MAX)
+        return fail(EP_UNSUPPORTED, "the product needs more than 2^31 workgroups");
+    return from_hip(ep::launch_expert(dtype, a, static_cast<hipStream_t>(stream)), what);
+}
+
+ep_status_t ep_expert_matmul(const void* x, int dtype, int64_t ld_x, int64_t num_x_rows,
+                             const int32_t* src, const void* weights, int num_experts,
+                             int out_features, int in_features, const int32_t* offsets,
+                             const int32_t* counts, int64_t num_rows, void* out, int64_t ld_out,
+                             void* stream)
+{
+    return expert_forward(x, dtype, ld_x, num_x_rows, src, weights, num_experts, out_features,
+                          in_features, false, offsets, counts, num_rows, out, ld_out, nullptr, 0,
+                          stream, "ep_expert_matmul launch");
+}
+
+ep_status_t ep_expert_glu(const void* x, int dtype, int64_t ld_x, int64_t num_x_rows,
+                          const int32_t* src, const void* weights, int num_experts,
+                          int out_features, int in_features, const int32_t* offsets,
+                          const int32_t* counts, int64_t num_rows, void* out, int64_t ld_out,
+                          void* pre, int64_t ld_pre, void* stream)
+{
+    return expert_forward(x, dtype, ld_x, num_x_rows, src, weights, num_experts, out_features,
+                          in_features, true, offsets, counts, num_rows, out, ld_out, pre, ld_pre,
+                          stream, "ep_expert_glu launch");
+}
+
+// Row stride of the gated backward's workspace: whole 16-byte vectors.
+static int64_t glu_workspace_ld(int out_features) { return ((int64_t)out_features + 7) / 8 * 8; }
+
+size_t ep_expert_glu_backward_workspace_size(int64_t num_rows, int out_features)
+{
+    if (num_rows < 0 || num_rows >= ((int64_t)1 << 31) || out_features < 2 ||
+        out_features > EP_MAX_OUT_FEATURES || out_features % 2 != 0)
+        return 0;
+    return (size_t)num_rows * (size_t)glu_workspace_ld(out_features) * 2;
+}
+
+static ep_status_t expert_backward(const void* grad_out, int dtype, int64_t ld_grad_out,
+                                   const void* pre, int64_t ld_pre, const void* x, int64_t ld_x,
+                                   int64_t num_x_rows, const int32_t* src, const void* weights,
+                                   int num_experts, int out_features, int in_features, bool gated,
+                                   const int32_t* offsets, const int32_t* counts, int64_t num_rows,
+                                   void* grad_rows, int64_t ld_grad_rows, void* grad_weights,
+                                   int grad_weights_dtype, void* workspace, size_t workspace_bytes,
+                                   void* stream, const char* what)
+{
+    g_last_error[0] = '\0';
+    ep_status_t st = check_dtype(dtype, false);
+    if (st) return st;
+    st = check_expert(num_experts, out_features, in_features, gated, offsets, counts, num_rows);
+    if (st) return st;
+    if (!grad_rows && !grad_weights)
+        return fail(EP_INVALID_ARGUMENT, "one of grad_rows and grad_weights is required");
+    if (grad_weights) {
+        if (grad_weights_dtype != dtype && grad_weights_dtype != EP_FP32)
+            return fail(EP_INVALID_ARGUMENT, "grad_weights_dtype %d must be dtype %d or EP_FP32",
+                        grad_weights_dtype, dtype);
+        if (off_by(grad_weights, dtype_bytes(grad_weights_dtype)))
+            return fail(EP_INVALID_ARGUMENT, "grad_weights must be aligned to its element");
+    }
+    if (num_rows == 0 && !grad_weights) return EP_SUCCESS;
+    if (num_rows > 0) {
+        st = check_matrix(grad_out, ld_grad_out, gated ? out_features / 2 : out_features, dtype, "grad_out");
+        if (st) return st;
+        if (grad_weights) {
+            st = check_rows_of(x, ld_x, num_x_rows, src, in_features, dtype, num_rows);
+            if (st) return st;
+        }
+        if (grad_rows) {
+            st = check_matrix(weights, in_features, in_features, dtype, "weights");
+            if (st) return st;
+            st = check_matrix(grad_rows, ld_grad_rows, in_features, dtype, "grad_rows");
+            if (st) return st;
+        }
+        if (gated) {
+            st = check_matrix(pre, ld_pre, out_features, dtype, "pre");
+            if (st) return st;
+            const size_t need = ep_expert_glu_backward_workspace_size(num_rows, out_features);
+            if (!workspace || !aligned16(workspace) || workspace_bytes < need)
+                return fail(EP_INVALID_ARGUMENT,
+                            "workspace must be 16-byte aligned and hold %zu bytes, holds %zu", need,
+                            workspace ? workspace_bytes : (size_t)0);
+        }
+    }
+    ep::ExpertBackwardArgs a = {grad_out, ld_grad_out, false, x, ld_x, num_x_rows, src, weights,
+                                num_experts, out_features, in_features, offsets, counts, num_rows,
+                                grad_rows, ld_grad_rows, grad_weights, grad_weights_dtype == EP_FP32};
+    if (ep::expert_backward_max_blocks(a) > INT32_MAX ||
+        num_rows * ((out_features + 15) / 16) / 256 >= INT32_MAX)
+        return fail(EP_UNSUPPORTED, "the gradients need more than 2^31 workgroups");
+    if (gated) {
+        a.grad = workspace;
+        a.ld_grad = glu_workspace_ld(out_features);
+        a.padded = true;
+        const ep::GluBackwardArgs g = {grad_out, ld_grad_out, pre, ld_pre, num_rows, out_features,
+                                       workspace, a.ld_grad};
+        st = from_hip(ep::launch_glu_backward(dtype, g, static_cast<hipStream_t>(stream)), what);
+        if (st) return st;
+    }
+    return from_hip(ep::launch_expert_backward(dtype, a, static_cast<hipStream_t>(stream)), what);
+}
+
+ep_status_t ep_expert_matmul_backward(const void* grad_out, int dtype, int64_t ld_grad_out,
+                                      const void* x, int64_t ld_x, int64_t num_x_rows,
+                                      const int32_t* src, const void* weights, int num_experts,
+                                      int out_features, int in_features, const int32_t* offsets,
+                                      const int32_t* counts, int64_t num_rows, void* grad_rows,
+                                      int64_t ld_grad_rows, void* grad_weights,
+                                      int grad_weights_dtype, void* stream)
+{
+    return expert_backward(grad_out, dtype, ld_grad_out, nullptr, 0, x, ld_x, num_x_rows, src, weights,
+                           num_experts, out_features, in_features, false, offsets, counts, num_rows,
+                           grad_rows, ld_grad_rows, grad_weights, grad_weights_dtype, nullptr, 0, stream,
+                           "ep_expert_matmul_backward launch");
+}
+
+ep_status_t ep_expert_glu_backward(const void* grad_out, int dtype, int64_t ld_grad_out,
+                                   const void* pre, int64_t ld_pre, const void* x, int64_t ld_x,
+                                   int64_t num_x_rows, const int32_t* src, const void* weights,
+                                   int num_experts, int out_features, int in_features,
+                                   const int32_t* offsets, const int32_t* counts, int64_t num_rows,
+                                   void* grad_rows, int64_t ld_grad_rows, void* grad_weights,
+                                   int grad_weights_dtype, void* workspace, size_t workspace_bytes,
+                                   void* stream)
+{
+    return expert_backward(grad_out, dtype, ld_grad_out, pre, ld_pre, x, ld_x, num_x_rows, src, weights,
+                           num_experts, out_features, in_features, true, offsets, counts, num_rows,
+                           grad_rows, ld_grad_rows, grad_weights, grad_weights_dtype, workspace,
+                           workspace_bytes, stream, "ep_expert_glu_backward launch");
+}
+
+ep_status_t ep_expert_matmul_fp8(const void* x, int x_format, int64_t ld_x, int64_t num_x_rows,
+                                 const void* x_scales, int scale_format, int64_t scale_row_stride,
+                                 int64_t scale_block_stride, const int32_t* src,
+                                 const void* weights, const float* weight_scales, int num_experts,
+                                 int out_features, int in_features, int gated,
+                                 const int32_t* offsets, const int32_t* counts, int64_t num_rows,
+                                 void* out, int out_dtype, int64_t ld_out, void* stream)
+{
+    g_last_error[0] = '\0';
+    ep_status_t st = check_dtype(out_dtype, false);
+    if (st) return st;
+    if (x_format != EP_OUT_FP8_E4M3 && x_format != EP_OUT_FP8_E5M2)
+        return fail(EP_INVALID_ARGUMENT, "x_format %d must be EP_OUT_FP8_E4M3 or EP_OUT_FP8_E5M2", x_format);
+    if (scale_format != EP_SCALE_FP32 && scale_format != EP_SCALE_FP32_POW2 && scale_format != EP_SCALE_UE8M0)
+        return fail(EP_INVALID_ARGUMENT, "unknown scale_format %d", scale_format);
+    st = check_expert(num_experts, out_features, in_features, gated != 0, offsets, counts, num_rows);
+    if (st) return st;
+    if (in_features % 16 != 0)
+        return fail(EP_INVALID_ARGUMENT, "in_features %d must be a multiple of 16", in_features);
+    if (num_rows == 0) return EP_SUCCESS;
+    if (!x || !aligned16(x) || ld_x < in_features || ld_x % 16 != 0)
+        return fail(EP_INVALID_ARGUMENT, "x must be 16-byte aligned, its row stride %lld a multiple of 16 "
+                                         "and at least in_features %d", (long long)ld_x, in_features);
+    if (num_x_rows < 1 || (!src && num_x_rows < num_rows))
+        return fail(EP_INVALID_ARGUMENT, "x has %lld rows for %lld rows of the product",
+                    (long long)num_x_rows, (long long)num_rows);
+    if (!weights || !aligned16(weights))
+        return fail(EP_INVALID_ARGUMENT, "weights must be non-NULL and 16-byte aligned");
+    if (!x_scales || !weight_scales || off_by(weight_scales, 4) || off_by(src, 4) ||
+        (scale_format != EP_SCALE_UE8M0 && off_by(x_scales, 4)))
+        return fail(EP_INVALID_ARGUMENT, "x_scales and weight_scales are required, and they and src must be "
+                                         "aligned to their elements");
+    if (scale_row_stride < 0 || scale_block_stride < 0)
+        return fail(EP_INVALID_ARGUMENT, "the scales' strides must not be negative");
+    st = check_matrix(out, ld_out, gated ? out_features / 2 : out_features, out_dtype, "out");
+    if (st) return st;
+    const ep::ExpertFp8Args a = {x, ld_x, num_x_rows, src, x_format == EP_OUT_FP8_E5M2 ? 1 : 0, x_scales,
+                                 scale_format == EP_SCALE_UE8M0, scale_row_stride, scale_block_stride,
+                                 weights, weight_scales, num_experts, out_features, in_features,
+                                 offsets, counts, num_rows, gated != 0, out, ld_out};
+    if (ep::expert_fp8_max_blocks(a) > INT32_MAX)
+        return fail(EP_UNSUPPORTED, "the product needs more than 2^31 workgroups");
+    return from_hip(ep::launch_expert_fp8(out_dtype, a, static_cast<hipStream_t>(stream)),
+                    "ep_expert_matmul_fp8 launch");
 }
 
 }  // extern "C"

@@ -1,0 +1,189 @@
+// ep_expert.hip -- the experts' products in 16 bits: out[r] = W[e] x[r] for
+// the rows r of each expert e, or silu(gate) * up of the two halves of W[e]
+// x[r], computed in one kernel.
+//
+// A workgroup makes a tile of BP outputs by BQ rows of one expert.  The
+// weights are the matrix instruction's first operand, the rows its second:
+// a lane ends with runs of outputs of one row.  For the gated product a tile
+// takes 32 rows of the gate half, the 32 rows of the up half that belong to
+// them, and so on: both land in the same lane, and the activation and the
+// product happen in registers, in fp32, before the one rounding.
+#include "ep_expert.h"
+#include "ep_product.h"
+
+namespace ep {
+namespace {
+
+template <typename T>
+struct Product {
+    const T* x;
+    int64_t ld_x, x_rows;
+    const int32_t* src;
+    const T* w;
+    int n, k;
+    Segments seg;
+    T* out;
+    int64_t ld_out;
+    T* pre;
+    int64_t ld_pre;
+    int col_tiles, group;
+};
+
+// WP x WQ wavefronts.  DIRECT: rows and weights in whole 16-byte chunks,
+// loaded into LDS directly; else by way of registers.
+template <typename T, bool GLU, bool DIRECT, int BP, int BQ, int WP, int WQ>
+__global__ __launch_bounds__(WP * WQ * 64)
+void expert_kernel(Product<T> a)
+{
+    constexpr int kThreads = WP * WQ * 64;
+    constexpr int PB = BP / WP / 32, QB = BQ / WQ / 32;
+    using P = RowOperand<BP, kThreads>;
+    using Q = RowOperand<BQ, kThreads>;
+    constexpr int kStage = P::kBytes + Q::kBytes;
+    __shared__ __attribute__((aligned(128))) char lds[2 * kStage];
+
+    int item, tile;
+    place_of(a.group, a.col_tiles, item, tile);
+    const RowBlock rb = find_rows(a.seg, BQ, item);
+    if (rb.rows <= 0) return;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int p0 = wave / WQ * (PB * 32), q0 = wave % WQ * (QB * 32);
+    const int half = a.n / 2;
+    const int n0 = tile * (GLU ? BP / 2 : BP);
+
+    P p;
+    Q q;
+    const T* w = a.w + (int64_t)rb.expert * a.n * a.k;
+    p.init([&](int i) {
+        int n;
+        if constexpr (GLU) {
+            n = n0 + i / 64 * 32 + (i & 31);
+            n = (n < half ? n : half - 1) + (i & 32 ? half : 0);
+        } else {
+            n = n0 + i < a.n ? n0 + i : a.n - 1;
+        }
+        return reinterpret_cast<const char*>(w + (int64_t)n * a.k);
+    });
+    q.init([&](int i) {
+        int64_t r = rb.first + (i < rb.rows ? i : 0);
+        if (a.src != nullptr) {
+            r = a.src[r];
+            if (r < 0 || r >= a.x_rows) r = 0;
+        }
+        return reinterpret_cast<const char*>(a.x + r * a.ld_x);
+    });
+
+    f32x16_t acc[PB][QB];
+#pragma unroll
+    for (int i = 0; i < PB; ++i)
+#pragma unroll
+        for (int j = 0; j < QB; ++j) acc[i][j] = f32x16_t{};
+
+    const int bytes = a.k * 2, steps = (bytes + 127) / 128;
+    if constexpr (DIRECT) {
+        const uint32_t at = lds_address(lds) + wave * 1024;
+        p.load(at, 0, bytes);
+        q.load(at + P::kBytes, 0, bytes);
+        for (int s = 0; s < steps; ++s) {
+            wait_barrier();
+            const int now = (s & 1) * kStage, next = kStage - now;
+            if (s + 1 < steps) {
+                p.load(at + next, s + 1, bytes);
+                q.load(at + next + P::kBytes, s + 1, bytes);
+            }
+            multiply<T, P, Q>(lds + now, lds + now + P::kBytes, p0, q0, acc);
+        }
+    } else {
+        uint4 pv[P::kLoads], qv[Q::kLoads];
+        p.template fetch<T>(pv, 0, bytes);
+        q.template fetch<T>(qv, 0, bytes);
+        P::put(lds, pv);
+        Q::put(lds + P::kBytes, qv);
+        for (int s = 0; s < steps; ++s) {
+            __syncthreads();
+            const int now = (s & 1) * kStage, next = kStage - now;
+            if (s + 1 < steps) {
+                p.template fetch<T>(pv, s + 1, bytes);
+                q.template fetch<T>(qv, s + 1, bytes);
+            }
+            multiply<T, P, Q>(lds + now, lds + now + P::kBytes, p0, q0, acc);
+            if (s + 1 < steps) {
+                P::put(lds + next, pv);
+                Q::put(lds + next + P::kBytes, qv);
+            }
+        }
+    }
+
+#pragma unroll
+    for (int j = 0; j < QB; ++j) {
+        const int r = q0 + j * 32 + (lane & 31);
+        const bool live = r < rb.rows;
+        const int64_t row = rb.first + (live ? r : 0);
+        if constexpr (GLU) {
+#pragma unroll
+            for (int i = 0; i < PB; i += 2) {
+                const int64_t c = n0 + (p0 + i * 32) / 2;
+                f32x16_t f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) f[e] = silu_of(acc[i][j][e]) * acc[i + 1][j][e];
+                store_block(f, a.out + row * a.ld_out, c, half, live);
+                if (a.pre != nullptr) {
+                    store_block(acc[i][j], a.pre + row * a.ld_pre, c, half, live);
+                    store_block(acc[i + 1][j], a.pre + row * a.ld_pre + half, c, half, live);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < PB; ++i)
+                store_block(acc[i][j], a.out + row * a.ld_out, n0 + p0 + i * 32, a.n, live);
+        }
+    }
+}
+
+template <typename T, bool GLU, bool DIRECT, int BP, int BQ, int WP, int WQ>
+hipError_t launch(const ExpertArgs& a, hipStream_t stream)
+{
+    Product<T> p = {static_cast<const T*>(a.x), a.ld_x, a.x_rows, a.src, static_cast<const T*>(a.w), a.n, a.k,
+                    {a.offsets, a.counts, a.num_experts, (int)a.num_rows},
+                    static_cast<T*>(a.out), a.ld_out, static_cast<T*>(a.pre), a.ld_pre, 0, 8};
+    constexpr int kCols = GLU ? BP / 2 : BP;
+    const int n = GLU ? a.n / 2 : a.n;
+    p.col_tiles = (n + kCols - 1) / kCols;
+    const int64_t items = max_row_blocks(a.num_rows, a.num_experts, BQ);
+    hipLaunchKernelGGL((expert_kernel<T, GLU, DIRECT, BP, BQ, WP, WQ>),
+                       dim3((unsigned)tile_grid(items, p.group, p.col_tiles)), dim3(WP * WQ * 64), 0, stream, p);
+    return hipGetLastError();
+}
+
+template <typename T, bool GLU>
+hipError_t sized(const ExpertArgs& a, hipStream_t stream)
+{
+    const bool direct = a.k % 8 == 0 && a.ld_x % 8 == 0 &&
+                        ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.w)) & 15) == 0;
+    if (!direct) return launch<T, GLU, false, 128, 128, 2, 2>(a, stream);
+    const int64_t hold = a.num_rows < a.num_experts ? a.num_rows : a.num_experts;
+    if (a.num_rows / hold >= 192) return launch<T, GLU, true, 256, 256, 2, 4>(a, stream);
+    return launch<T, GLU, true, 128, 128, 2, 2>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_expert(int dtype, const ExpertArgs& a, hipStream_t stream)
+{
+    if (a.num_rows == 0) return hipSuccess;
+    const int64_t hold = a.num_rows < a.num_experts ? a.num_rows : a.num_experts;
+    if (a.num_rows / hold <= 32) return launch_expert_few(dtype, a, stream);
+    if (dtype == 0) return a.gated ? sized<Bf16, true>(a, stream) : sized<Bf16, false>(a, stream);
+    return a.gated ? sized<Fp16, true>(a, stream) : sized<Fp16, false>(a, stream);
+}
+
+int64_t expert_max_blocks(const ExpertArgs& a)
+{
+    // the smallest tiles of ep_expert_few.hip, and the tiles above
+    const int64_t few = max_row_blocks(a.num_rows, a.num_experts, 16) * ((a.n + 31) / 32 + 1);
+    const int64_t tiles = tile_grid(max_row_blocks(a.num_rows, a.num_experts, 128), 8, (a.n + 127) / 128 + 1);
+    return few > tiles ? few : tiles;
+}
+
+}  // namespace ep

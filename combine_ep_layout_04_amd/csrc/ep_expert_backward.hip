@@ -1,0 +1,381 @@
+// ep_expert_backward.hip -- the gradients of the experts' products, in 16
+// bits: with d[r] the gradient of out[r] = W[e] x[r],
+//
+//   grad_rows[r, k] = sum_n d[r, n] W[e, n, k]
+//   grad_w[e, n, k] = sum_r d[r, n] x[r, k]     over the rows r of expert e
+//
+// and, for the gated product, d from the gradient of silu(gate) * up:
+//
+//   d_gate = g up s (1 + gate (1 - s)),  d_up = g gate s,  s = 1 / (1 + exp(-gate)).
+//
+// In the first the weights, in the second both operands lie across the
+// reduction; they are transposed on the way from LDS to the registers
+// (ColOperand), so nothing is transposed in memory.  Sums are fp32 in a fixed
+// order, no atomics.
+#include "ep_expert.h"
+#include "ep_product.h"
+
+namespace ep {
+namespace {
+
+template <typename T>
+struct RowsGrad {
+    const T* grad;
+    int64_t ld_grad;
+    const T* w;
+    int n, k;
+    Segments seg;
+    T* out;
+    int64_t ld_out;
+    int col_tiles, group;
+};
+
+// A tile of BP columns (k) by BQ rows; the reduction goes along n.
+template <typename T, bool DIRECT, int BP, int BQ, int WP, int WQ>
+__global__ __launch_bounds__(WP * WQ * 64)
+void rows_grad_kernel(RowsGrad<T> a)
+{
+    constexpr int kThreads = WP * WQ * 64;
+    constexpr int PB = BP / WP / 32, QB = BQ / WQ / 32;
+    using P = ColOperand<BP, kThreads>;
+    using Q = RowOperand<BQ, kThreads>;
+    constexpr int kStage = P::kBytes + Q::kBytes;
+    __shared__ __attribute__((aligned(128))) char lds[2 * kStage];
+
+    int item, tile;
+    place_of(a.group, a.col_tiles, item, tile);
+    const RowBlock rb = find_rows(a.seg, BQ, item);
+    if (rb.rows <= 0) return;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int p0 = wave / WQ * (PB * 32), q0 = wave % WQ * (QB * 32);
+    const int64_t k0 = (int64_t)tile * BP;
+
+    P p;
+    Q q;
+    p.init(k0, a.k);
+    q.init([&](int i) {
+        const int64_t r = rb.first + (i < rb.rows ? i : 0);
+        return reinterpret_cast<const char*>(a.grad + r * a.ld_grad);
+    });
+    // this thread's rows of the weights
+    const char* wr[P::kLoads];
+    const int64_t ld_w = (int64_t)a.k * 2;
+#pragma unroll
+    for (int i = 0; i < P::kLoads; ++i)
+        wr[i] = reinterpret_cast<const char*>(a.w) +
+                ((int64_t)rb.expert * a.n + p.row + i * P::kRowStep) * ld_w;
+    auto w_row = [&](int s) { return [&, s](int i) { return wr[i] + s * 64 * ld_w; }; };
+
+    f32x16_t acc[PB][QB];
+#pragma unroll
+    for (int i = 0; i < PB; ++i)
+#pragma unroll
+        for (int j = 0; j < QB; ++j) acc[i][j] = f32x16_t{};
+
+    const int bytes = a.n * 2, steps = (a.n + 63) / 64;
+    if constexpr (DIRECT) {
+        const uint32_t at = lds_address(lds) + wave * 1024;
+        // a chunk that ends past n reads what lies behind the row: the caller
+        // keeps zeros there
+        const int chunks = (bytes + 15) / 16 * 16;
+        p.load(at, a.n, w_row(0));
+        q.load(at + P::kBytes, 0, chunks);
+        for (int s = 0; s < steps; ++s) {
+            wait_barrier();
+            const int now = (s & 1) * kStage, next = kStage - now;
+            if (s + 1 < steps) {
+                p.load(at + next, a.n - (s + 1) * 64, w_row(s + 1));
+                q.load(at + next + P::kBytes, s + 1, chunks);
+            }
+            multiply<T, P, Q>(lds + now, lds + now + P::kBytes, p0, q0, acc);
+        }
+    } else {
+        uint4 pv[P::kLoads], qv[Q::kLoads];
+        p.template fetch<T>(pv, a.n, w_row(0));
+        q.template fetch<T>(qv, 0, bytes);
+        P::put(lds, pv);
+        Q::put(lds + P::kBytes, qv);
+        for (int s = 0; s < steps; ++s) {
+            __syncthreads();
+            const int now = (s & 1) * kStage, next = kStage - now;
+            if (s + 1 < steps) {
+                p.template fetch<T>(pv, a.n - (s + 1) * 64, w_row(s + 1));
+                q.template fetch<T>(qv, s + 1, bytes);
+            }
+            multiply<T, P, Q>(lds + now, lds + now + P::kBytes, p0, q0, acc);
+            if (s + 1 < steps) {
+                P::put(lds + next, pv);
+                Q::put(lds + next + P::kBytes, qv);
+            }
+        }
+    }
+
+#pragma unroll
+    for (int j = 0; j < QB; ++j) {
+        const int r = q0 + j * 32 + (lane & 31);
+        const bool live = r < rb.rows;
+        const int64_t row = rb.first + (live ? r : 0);
+#pragma unroll
+        for (int i = 0; i < PB; ++i)
+            store_block(acc[i][j], a.out + row * a.ld_out, k0 + p0 + i * 32, a.k, live);
+    }
+}
+
+template <typename T>
+struct WeightGrad {
+    const T* grad;
+    int64_t ld_grad;
+    const T* x;
+    int64_t ld_x, x_rows;
+    const int32_t* src;
+    int n, k;
+    Segments seg;
+    void* out;
+    int k_tiles, n_tiles;
+};
+
+// A tile of BP columns (k) by BQ outputs (n) of one expert; the reduction
+// goes over its rows.  Experts without rows get zeros.
+template <typename T, typename O, bool DIRECT, int BP, int BQ, int WP, int WQ>
+__global__ __launch_bounds__(WP * WQ * 64)
+void weight_grad_kernel(WeightGrad<T> a)
+{
+    constexpr int kThreads = WP * WQ * 64;
+    constexpr int PB = BP / WP / 32, QB = BQ / WQ / 32;
+    using P = ColOperand<BP, kThreads>;
+    using Q = ColOperand<BQ, kThreads>;
+    constexpr int kStage = P::kBytes + Q::kBytes;
+    __shared__ __attribute__((aligned(128))) char lds[2 * kStage];
+
+    const unsigned place = run_place(), tiles = (unsigned)a.k_tiles * (unsigned)a.n_tiles;
+    const int expert = (int)(place / tiles);
+    if (expert >= a.seg.num_experts) return;
+    const int tile_n = (int)(place % tiles / (unsigned)a.k_tiles), tile_k = (int)(place % tiles % (unsigned)a.k_tiles);
+    RowBlock rb = {expert, 0, a.seg.num_rows};
+    if (a.seg.offsets != nullptr) {
+        rb.first = a.seg.offsets[expert];
+        rb.rows = a.seg.counts != nullptr ? a.seg.counts[expert] : a.seg.offsets[expert + 1] - rb.first;
+        bound_rows(rb, a.seg.num_rows);
+        if (rb.rows < 0) rb.rows = 0;
+    }
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int p0 = wave / WQ * (PB * 32), q0 = wave % WQ * (QB * 32);
+    const int64_t k0 = (int64_t)tile_k * BP, n0 = (int64_t)tile_n * BQ;
+
+    P p;
+    Q q;
+    p.init(k0, a.k);
+    q.init(n0, a.n);
+    const char* gr[Q::kLoads];
+    const int64_t ld_g = a.ld_grad * 2, ld_x = a.ld_x * 2;
+#pragma unroll
+    for (int i = 0; i < Q::kLoads; ++i)
+        gr[i] = reinterpret_cast<const char*>(a.grad) + (rb.first + q.row + i * Q::kRowStep) * ld_g;
+    auto g_row = [&](int s) { return [&, s](int i) { return gr[i] + s * 64 * ld_g; }; };
+    // this thread's rows of x for the coming step
+    int xi[P::kLoads];
+    auto find_x = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < P::kLoads; ++i) {
+            const int in = s * 64 + p.row + i * P::kRowStep;
+            xi[i] = rb.first + (in < rb.rows ? in : 0);
+            if (a.src != nullptr) xi[i] = a.src[xi[i]];
+        }
+    };
+    auto x_row = [&](int i) {
+        const int64_t r = xi[i] < 0 || xi[i] >= a.x_rows ? 0 : xi[i];
+        return reinterpret_cast<const char*>(a.x) + r * ld_x;
+    };
+
+    f32x16_t acc[PB][QB];
+#pragma unroll
+    for (int i = 0; i < PB; ++i)
+#pragma unroll
+        for (int j = 0; j < QB; ++j) acc[i][j] = f32x16_t{};
+
+    const int steps = (rb.rows + 63) / 64;
+    if (steps > 0) {
+        find_x(0);
+        if constexpr (DIRECT) {
+            const uint32_t at = lds_address(lds) + wave * 1024;
+            p.load(at, rb.rows, x_row);
+            q.load(at + P::kBytes, rb.rows, g_row(0));
+            if (steps > 1) find_x(1);
+            for (int s = 0; s < steps; ++s) {
+                wait_barrier();
+                const int now = (s & 1) * kStage, next = kStage - now;
+                if (s + 1 < steps) {
+                    // the indices have arrived with the loads waited for; so
+                    // that the compiler knows before loads it does not count
+#pragma unroll
+                    for (int i = 0; i < P::kLoads; ++i) asm volatile("" : "+v"(xi[i]));
+                    p.load(at + next, rb.rows - (s + 1) * 64, x_row);
+                    q.load(at + next + P::kBytes, rb.rows - (s + 1) * 64, g_row(s + 1));
+                    if (s + 2 < steps) find_x(s + 2);
+                }
+                multiply<T, P, Q>(lds + now, lds + now + P::kBytes, p0, q0, acc);
+            }
+        } else {
+            uint4 pv[P::kLoads], qv[Q::kLoads];
+            p.template fetch<T>(pv, rb.rows, x_row);
+            q.template fetch<T>(qv, rb.rows, g_row(0));
+            P::put(lds, pv);
+            Q::put(lds + P::kBytes, qv);
+            for (int s = 0; s < steps; ++s) {
+                __syncthreads();
+                const int now = (s & 1) * kStage, next = kStage - now;
+                if (s + 1 < steps) {
+                    find_x(s + 1);
+                    p.template fetch<T>(pv, rb.rows - (s + 1) * 64, x_row);
+                    q.template fetch<T>(qv, rb.rows - (s + 1) * 64, g_row(s + 1));
+                }
+                multiply<T, P, Q>(lds + now, lds + now + P::kBytes, p0, q0, acc);
+                if (s + 1 < steps) {
+                    P::put(lds + next, pv);
+                    Q::put(lds + next + P::kBytes, qv);
+                }
+            }
+        }
+    }
+
+    O* out = static_cast<O*>(a.out) + (int64_t)expert * a.n * a.k;
+#pragma unroll
+    for (int j = 0; j < QB; ++j) {
+        const int64_t n = n0 + q0 + j * 32 + (lane & 31);
+        const bool live = n < a.n;
+#pragma unroll
+        for (int i = 0; i < PB; ++i)
+            store_block(acc[i][j], out + (live ? n : 0) * a.k, k0 + p0 + i * 32, a.k, live);
+    }
+}
+
+// Both halves' gradients, a row's units of 8 outputs per thread.  Memory
+// bound: reads 3, writes 2 values an output.  d is rounded to 16 bits, the
+// type the matrix cores take; it costs half a step relative to each term of
+// the sums that follow.
+template <typename T>
+__global__ __launch_bounds__(256)
+void glu_backward_kernel(const T* __restrict__ grad, int64_t ld_grad, const T* __restrict__ pre, int64_t ld_pre,
+                         int64_t num_rows, int half, T* __restrict__ out, int64_t ld_out, int units)
+{
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t row = at / units;
+    if (row >= num_rows) return;
+    const int c = (int)(at % units) * 8;
+    const T* g = grad + row * ld_grad + c;
+    const T* p = pre + row * ld_pre + c;
+    T* o = out + row * ld_out + c;
+    const int left = half - c;
+    auto both = [](float g, float gate, float up, float& d_gate, float& d_up) {
+        const float s = sigmoid_of(gate), gs = g * s;
+        d_gate = gs * up * (1.0f + gate * (1.0f - s));
+        d_up = gs * gate;
+    };
+    if (left >= 8) {
+        float gv[8], gate[8], up[8], dg[8], du[8];
+        unpack<T>(fetch16<T>(reinterpret_cast<const char*>(g), 8), gv);
+        unpack<T>(fetch16<T>(reinterpret_cast<const char*>(p), 8), gate);
+        unpack<T>(fetch16<T>(reinterpret_cast<const char*>(p + half), 8), up);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) both(gv[i], gate[i], up[i], dg[i], du[i]);
+        const uint4 a = pack<T>(dg), b = pack<T>(du);
+        __builtin_memcpy(o, &a, 16);
+        __builtin_memcpy(o + half, &b, 16);
+    } else {
+        for (int i = 0; i < 8 && i < left; ++i) {
+            float dg, du;
+            both(to_float(g[i]), to_float(p[i]), to_float(p[half + i]), dg, du);
+            o[i] = from_float<T>(dg);
+            o[half + i] = from_float<T>(du);
+        }
+    }
+    if (c == 0)     // the row's padding
+        for (int64_t i = 2 * (int64_t)half; i < ld_out; ++i) out[row * ld_out + i] = T{0};
+}
+
+template <typename T, bool DIRECT, int BP, int BQ, int WP, int WQ>
+hipError_t launch_rows(const ExpertBackwardArgs& a, hipStream_t stream)
+{
+    RowsGrad<T> p = {static_cast<const T*>(a.grad), a.ld_grad, static_cast<const T*>(a.w), a.n, a.k,
+                     {a.offsets, a.counts, a.num_experts, (int)a.num_rows},
+                     static_cast<T*>(a.grad_rows), a.ld_grad_rows, (a.k + BP - 1) / BP, 8};
+    const int64_t items = max_row_blocks(a.num_rows, a.num_experts, BQ);
+    hipLaunchKernelGGL((rows_grad_kernel<T, DIRECT, BP, BQ, WP, WQ>),
+                       dim3((unsigned)tile_grid(items, p.group, p.col_tiles)), dim3(WP * WQ * 64), 0, stream, p);
+    return hipGetLastError();
+}
+
+template <typename T, typename O, bool DIRECT, int BP, int BQ, int WP, int WQ>
+hipError_t launch_weights(const ExpertBackwardArgs& a, hipStream_t stream)
+{
+    WeightGrad<T> p = {static_cast<const T*>(a.grad), a.ld_grad, static_cast<const T*>(a.x), a.ld_x, a.x_rows, a.src,
+                       a.n, a.k, {a.offsets, a.counts, a.num_experts, (int)a.num_rows},
+                       a.grad_w, (a.k + BP - 1) / BP, (a.n + BQ - 1) / BQ};
+    hipLaunchKernelGGL((weight_grad_kernel<T, O, DIRECT, BP, BQ, WP, WQ>),
+                       dim3((unsigned)tile_grid(a.num_experts, 1, p.k_tiles * p.n_tiles)), dim3(WP * WQ * 64), 0,
+                       stream, p);
+    return hipGetLastError();
+}
+
+bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
+
+template <typename T, typename O>
+hipError_t weights_sized(const ExpertBackwardArgs& a, hipStream_t stream)
+{
+    const bool direct = a.k % 8 == 0 && a.ld_x % 8 == 0 && (a.n % 8 == 0 || a.padded) && a.ld_grad % 8 == 0 &&
+                        !off16(a.x) && !off16(a.grad);
+    if (!direct) return launch_weights<T, O, false, 128, 128, 2, 2>(a, stream);
+    if (a.num_rows / a.num_experts >= 192) return launch_weights<T, O, true, 256, 256, 2, 4>(a, stream);
+    return launch_weights<T, O, true, 128, 128, 2, 2>(a, stream);
+}
+
+template <typename T>
+hipError_t backward(const ExpertBackwardArgs& a, hipStream_t stream)
+{
+    if (a.grad_rows != nullptr && a.num_rows > 0) {
+        const bool direct = a.k % 8 == 0 && (a.n % 8 == 0 || a.padded) && a.ld_grad % 8 == 0 && !off16(a.w) &&
+                            !off16(a.grad);
+        const int64_t hold = a.num_rows < a.num_experts ? a.num_rows : a.num_experts;
+        const hipError_t err = !direct ? launch_rows<T, false, 128, 128, 2, 2>(a, stream)
+                               : a.num_rows / hold >= 192 ? launch_rows<T, true, 256, 256, 2, 4>(a, stream)
+                                                          : launch_rows<T, true, 128, 128, 2, 2>(a, stream);
+        if (err != hipSuccess) return err;
+    }
+    if (a.grad_w == nullptr) return hipSuccess;
+    return a.wide_w ? weights_sized<T, float>(a, stream) : weights_sized<T, T>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_expert_backward(int dtype, const ExpertBackwardArgs& a, hipStream_t stream)
+{
+    return dtype == 0 ? backward<Bf16>(a, stream) : backward<Fp16>(a, stream);
+}
+
+int64_t expert_backward_max_blocks(const ExpertBackwardArgs& a)
+{
+    const int64_t rows = tile_grid(max_row_blocks(a.num_rows, a.num_experts, 128), 8, (a.k + 127) / 128);
+    const int64_t tiles = ((int64_t)a.k + 127) / 128 * ((a.n + 127) / 128);
+    const int64_t weights = tiles > INT32_MAX ? tiles : tile_grid(a.num_experts, 1, (int)tiles);
+    return rows > weights ? rows : weights;
+}
+
+hipError_t launch_glu_backward(int dtype, const GluBackwardArgs& a, hipStream_t stream)
+{
+    if (a.num_rows == 0) return hipSuccess;
+    const int half = a.n / 2, units = (half + 7) / 8;
+    const unsigned blocks = (unsigned)((a.num_rows * units + 255) / 256);
+    if (dtype == 0)
+        hipLaunchKernelGGL((glu_backward_kernel<Bf16>), dim3(blocks), dim3(256), 0, stream,
+                           static_cast<const Bf16*>(a.grad), a.ld_grad, static_cast<const Bf16*>(a.pre), a.ld_pre,
+                           a.num_rows, half, static_cast<Bf16*>(a.out), a.ld_out, units);
+    else
+        hipLaunchKernelGGL((glu_backward_kernel<Fp16>), dim3(blocks), dim3(256), 0, stream,
+                           static_cast<const Fp16*>(a.grad), a.ld_grad, static_cast<const Fp16*>(a.pre), a.ld_pre,
+                           a.num_rows, half, static_cast<Fp16*>(a.out), a.ld_out, units);
+    return hipGetLastError();
+}
+
+}  // namespace ep

@@ -44,6 +44,7 @@ EP_MAX_ALIGNMENT = 4096
 EP_MAX_RANKS = 64
 EP_MAX_GROUPS = 64
 EP_MAX_W4_ROWS = 1 << 20
+EP_MAX_OUT_FEATURES = 1 << 20
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # ep_dtype_t
 _SCORES = {"softmax": 0, "sigmoid": 1}
 
@@ -58,7 +59,9 @@ SYMBOLS = ("ep_version", "ep_status_string", "ep_last_error", "ep_layout_workspa
            "ep_dispatch_ranked_backward", "ep_dispatch_colmajor_workspace_size",
            "ep_dispatch_colmajor_scales", "ep_dispatch_prequantized_colmajor",
            "ep_router", "ep_router_backward", "ep_permute", "ep_permute_backward", "ep_unpermute",
-           "ep_unpermute_backward", "ep_w4_packed_size", "ep_w4_pack", "ep_expert_matmul_w4")
+           "ep_unpermute_backward", "ep_w4_packed_size", "ep_w4_pack", "ep_expert_matmul_w4",
+           "ep_expert_matmul", "ep_expert_glu", "ep_expert_matmul_backward",
+           "ep_expert_glu_backward_workspace_size", "ep_expert_glu_backward", "ep_expert_matmul_fp8")
 
 
 class EpError(RuntimeError):
@@ -163,6 +166,22 @@ def lib() -> ctypes.CDLL:
         L.ep_expert_matmul_w4.argtypes = [P, i32, i64, i64, P, P, sz, i32, i32, i32, i32, i32, i32,
                                           P, P, i64, P, i64, P]
         L.ep_expert_matmul_w4.restype = i32
+        L.ep_expert_matmul.argtypes = [P, i32, i64, i64, P, P, i32, i32, i32, P, P, i64, P, i64, P]
+        L.ep_expert_matmul.restype = i32
+        L.ep_expert_glu.argtypes = [P, i32, i64, i64, P, P, i32, i32, i32, P, P, i64, P, i64, P, i64,
+                                    P]
+        L.ep_expert_glu.restype = i32
+        L.ep_expert_matmul_backward.argtypes = [P, i32, i64, P, i64, i64, P, P, i32, i32, i32, P, P,
+                                                i64, P, i64, P, i32, P]
+        L.ep_expert_matmul_backward.restype = i32
+        L.ep_expert_glu_backward_workspace_size.argtypes = [i64, i32]
+        L.ep_expert_glu_backward_workspace_size.restype = sz
+        L.ep_expert_glu_backward.argtypes = [P, i32, i64, P, i64, P, i64, i64, P, P, i32, i32, i32, P,
+                                             P, i64, P, i64, P, i32, P, sz, P]
+        L.ep_expert_glu_backward.restype = i32
+        L.ep_expert_matmul_fp8.argtypes = [P, i32, i64, i64, P, i32, i64, i64, P, P, P, i32, i32, i32,
+                                           i32, P, P, i64, P, i32, i64, P]
+        L.ep_expert_matmul_fp8.restype = i32
         _lib = L
     return _lib
 
@@ -1443,6 +1462,246 @@ def ep_expert_matmul_w4(x: torch.Tensor, weights: W4Weights, offsets: Optional[t
             x.shape[0], _ptr(src), w.packed.data_ptr(), w.packed.numel(), w.num_experts,
             w.out_features, w.in_features, w.group_size, int(w.has_zeros), int(w.gated),
             _ptr(offsets), _ptr(counts), R, out.data_ptr(), ld_out)
+    return out
+
+
+# ------------------------------------------ full-width and 8-bit products --
+
+_HALVES = (torch.bfloat16, torch.float16)
+
+
+def _expert_weights(t, name, dtype, device):
+    _need_on(t, name, dtype, device)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be 3-D [num_experts, out_features, in_features]")
+    return t.shape
+
+
+def _segments_of(E, offsets, counts, device):
+    if offsets is not None:
+        _need_on(offsets, "offsets", torch.int32, device, E + 1)
+    if counts is not None:
+        _need_on(counts, "counts", torch.int32, device, E)
+
+
+def _out_of(on, out, name, R, cols, dtype, device):
+    if out is None:
+        return on.empty((R, cols), dtype), cols
+    ld = _rows_of(out, name, dtype, cols, device)
+    if out.shape[0] < R:
+        raise ValueError(f"{name} has {out.shape[0]} rows, needs {R}")
+    return out, ld
+
+
+def _expert_rows(x, weights, offsets, src, counts, rows):
+    """(E, N, K, x's row stride, rows of the product) of a 16-bit product."""
+    if isinstance(x, torch.Tensor) and x.dtype not in _HALVES:
+        raise TypeError(f"x must be bfloat16 or float16, got {x.dtype}")
+    ld = _rows_of(x, "x")
+    dev = x.device
+    E, N, K = _expert_weights(weights, "weights", x.dtype, dev)
+    if x.shape[1] != K:
+        raise ValueError(f"x must have {K} columns, has {x.shape[1]}")
+    if src is not None:
+        _need_on(src, "src", torch.int32, dev, rows)
+    R = int(rows) if rows is not None else (src.numel() if src is not None else x.shape[0])
+    _segments_of(E, offsets, counts, dev)
+    return E, N, K, ld, R
+
+
+def ep_expert_matmul(x: torch.Tensor, weights: torch.Tensor, offsets: Optional[torch.Tensor] = None, *,
+                     src: Optional[torch.Tensor] = None, counts=None, rows: Optional[int] = None,
+                     out=None, stream=None):
+    """The experts' products: row r of expert e (rows ``offsets[e]`` to
+    ``offsets[e+1]``, or ``counts[e]`` of them) gives ``out[r] = W[e] @ x[r]``,
+    or ``W[e] @ x[src[r]]`` with ``src`` (the layout's).
+
+    ``x`` is bf16 or fp16 and may have strided rows, ``weights`` [E, N, K] has
+    its type; ``offsets`` may be left out with one expert.  ``rows`` is the
+    layout's row bound (src's length, or x's rows).  Returns out [rows, N],
+    outside autograd: its gradients are ep_expert_matmul_backward.  Rows of no
+    expert are not written."""
+    E, N, K, ld, R = _expert_rows(x, weights, offsets, src, counts, rows)
+    dev, dt = x.device, x.dtype
+    on = _On(dev, stream)
+    out, ld_out = _out_of(on, out, "out", R, N, dt, dev)
+    on.call("ep_expert_matmul", lib().ep_expert_matmul, x.data_ptr(), _DTYPES[dt], ld, x.shape[0],
+            _ptr(src), weights.data_ptr(), E, N, K, _ptr(offsets), _ptr(counts), R, out.data_ptr(),
+            ld_out)
+    return out
+
+
+def ep_expert_glu(x: torch.Tensor, weights: torch.Tensor, offsets: Optional[torch.Tensor] = None, *,
+                  src: Optional[torch.Tensor] = None, counts=None, rows: Optional[int] = None,
+                  out=None, pre=None, want_pre: bool = False, stream=None):
+    """The experts' gated block: ``out[r] = silu(gate) * up``, gate and up the
+    two halves of ``W[e] @ x[r]`` (the rows of ``weights`` [E, N, K] are gate,
+    then up), in one kernel; arguments as ep_expert_matmul.
+
+    Returns (out [rows, N/2], pre): with ``want_pre`` or a ``pre`` buffer
+    [rows, N] gate and up, which ep_expert_glu_backward takes, else None."""
+    E, N, K, ld, R = _expert_rows(x, weights, offsets, src, counts, rows)
+    if N % 2:
+        raise ValueError(f"gated weights have two halves, got {N} rows")
+    dev, dt = x.device, x.dtype
+    on = _On(dev, stream)
+    out, ld_out = _out_of(on, out, "out", R, N // 2, dt, dev)
+    ld_pre = 0
+    if pre is not None or want_pre:
+        pre, ld_pre = _out_of(on, pre, "pre", R, N, dt, dev)
+    on.call("ep_expert_glu", lib().ep_expert_glu, x.data_ptr(), _DTYPES[dt], ld, x.shape[0],
+            _ptr(src), weights.data_ptr(), E, N, K, _ptr(offsets), _ptr(counts), R, out.data_ptr(),
+            ld_out, _ptr(pre), ld_pre)
+    return out, pre
+
+
+def ep_expert_glu_backward_workspace_size(num_rows: int, out_features: int) -> int:
+    """Bytes of ep_expert_glu_backward's workspace (0 if the shape is invalid)."""
+    return int(lib().ep_expert_glu_backward_workspace_size(int(num_rows), int(out_features)))
+
+
+def _expert_backward(grad_out, x, weights, offsets, src, counts, grad_rows, grad_weights, want_rows,
+                     want_weights, weights_dtype, stream, cols_of):
+    E, N, K, ld_x, _ = _expert_rows(x, weights, offsets, src, counts, None)
+    dev, dt = x.device, x.dtype
+    ld_g = _rows_of(grad_out, "grad_out", dt, cols_of(N), dev)
+    R = grad_out.shape[0]
+    if src is not None and src.numel() < R:
+        raise ValueError(f"src has {src.numel()} elements, needs {R}")
+    if src is None and x.shape[0] < R:
+        raise ValueError(f"x has {x.shape[0]} rows, grad_out {R}")
+    want_rows, want_weights = want_rows or grad_rows is not None, want_weights or grad_weights is not None
+    if not want_rows and not want_weights:
+        raise ValueError("neither gradient is wanted")
+    if weights_dtype is None:
+        weights_dtype = dt if grad_weights is None else grad_weights.dtype
+    if weights_dtype not in (dt, torch.float32):
+        raise TypeError(f"the weights' gradient must be {dt} or float32, not {weights_dtype}")
+    on = _On(dev, stream)
+    ld_gr = 0
+    if want_rows:
+        grad_rows, ld_gr = _out_of(on, grad_rows, "grad_rows", R, K, dt, dev)
+    if want_weights:
+        if grad_weights is None:
+            grad_weights = on.empty((E, N, K), weights_dtype)
+        else:
+            _need_on(grad_weights, "grad_weights", weights_dtype, dev)
+            if tuple(grad_weights.shape) != (E, N, K):
+                raise ValueError(f"grad_weights must be {(E, N, K)}, is {tuple(grad_weights.shape)}")
+    tail = (x.data_ptr(), ld_x, x.shape[0], _ptr(src), weights.data_ptr(), E, N, K, _ptr(offsets),
+            _ptr(counts), R, _ptr(grad_rows), ld_gr, _ptr(grad_weights), _DTYPES[weights_dtype])
+    return on, N, R, ld_g, tail, grad_rows, grad_weights
+
+
+def ep_expert_matmul_backward(grad_out: torch.Tensor, x: torch.Tensor, weights: torch.Tensor,
+                              offsets: Optional[torch.Tensor] = None, *,
+                              src: Optional[torch.Tensor] = None, counts=None, grad_rows=None,
+                              grad_weights=None, want_rows: bool = True, want_weights: bool = True,
+                              weights_dtype: Optional[torch.dtype] = None, stream=None):
+    """Backward of ep_expert_matmul from ``grad_out`` [rows, N]: (grad_rows
+    [rows, K], grad_weights [E, N, K]); the latter in ``weights_dtype``, the
+    weights' own type or float32 (summed in fp32 either way), zeros for experts
+    without rows.
+
+    With ``src`` the rows' gradients still come per row of the layout;
+    ep_permute_backward sums them per token.  ``want_rows`` / ``want_weights``
+    False leaves one out (None).  Rows of no expert are not written."""
+    on, N, R, ld_g, tail, grad_rows, grad_weights = _expert_backward(
+        grad_out, x, weights, offsets, src, counts, grad_rows, grad_weights, want_rows, want_weights,
+        weights_dtype, stream, lambda n: n)
+    on.call("ep_expert_matmul_backward", lib().ep_expert_matmul_backward, grad_out.data_ptr(),
+            _DTYPES[grad_out.dtype], ld_g, *tail)
+    return grad_rows, grad_weights
+
+
+def ep_expert_glu_backward(grad_out: torch.Tensor, pre: torch.Tensor, x: torch.Tensor,
+                           weights: torch.Tensor, offsets: Optional[torch.Tensor] = None, *,
+                           src: Optional[torch.Tensor] = None, counts=None, grad_rows=None,
+                           grad_weights=None, want_rows: bool = True, want_weights: bool = True,
+                           weights_dtype: Optional[torch.dtype] = None, workspace=None, stream=None):
+    """Backward of ep_expert_glu from ``grad_out`` [rows, N/2] and the ``pre``
+    [rows, N] that it left; otherwise as ep_expert_matmul_backward.
+
+    ``workspace`` (uint8, ep_expert_glu_backward_workspace_size bytes) holds
+    the gradients of gate and up, in the rows' type; torch allocates it when
+    it is not given."""
+    on, N, R, ld_g, tail, grad_rows, grad_weights = _expert_backward(
+        grad_out, x, weights, offsets, src, counts, grad_rows, grad_weights, want_rows, want_weights,
+        weights_dtype, stream, lambda n: n // 2)
+    if N % 2:
+        raise ValueError(f"gated weights have two halves, got {N} rows")
+    dev = x.device
+    ld_p = _rows_of(pre, "pre", x.dtype, N, dev)
+    if pre.shape[0] < R:
+        raise ValueError(f"pre has {pre.shape[0]} rows, grad_out {R}")
+    need = ep_expert_glu_backward_workspace_size(R, N)
+    if workspace is None:
+        workspace = on.empty(need, torch.uint8)
+    else:
+        _need_on(workspace, "workspace", torch.uint8, dev, need)
+    on.call("ep_expert_glu_backward", lib().ep_expert_glu_backward, grad_out.data_ptr(),
+            _DTYPES[grad_out.dtype], ld_g, pre.data_ptr(), ld_p, *tail, workspace.data_ptr(),
+            workspace.numel())
+    return grad_rows, grad_weights
+
+
+def ep_expert_matmul_fp8(x: torch.Tensor, x_scales: torch.Tensor, weights: torch.Tensor,
+                         weight_scales: torch.Tensor, offsets: Optional[torch.Tensor] = None, *,
+                         fmt: str = "e4m3", gated: bool = False,
+                         src: Optional[torch.Tensor] = None, counts=None, rows: Optional[int] = None,
+                         dtype: torch.dtype = torch.bfloat16, out=None, stream=None):
+    """The experts' products of 8-bit rows and weights, scaled per 128 inputs:
+    ``out[r, n] = sum_b x_scales[r, b] * weight_scales[e, n // 128, b] *
+    sum_{k in b} x[r, k] * W[e, n, k]``, or silu(gate) * up of its halves with
+    ``gated``.
+
+    ``x`` uint8 [M, K]: codes of ``fmt`` ("e4m3" or "e5m2") as ep_dispatch
+    writes them, rows may be strided; ``x_scales`` [M, ceil(K / 128)] fp32, or
+    uint8 powers of two (UE8M0), of any strides (``scales.t()[:M]`` for
+    column-major ones); ``weights`` uint8 [E, N, K] E4M3 codes;
+    ``weight_scales`` fp32 [E, ceil(N / 128), ceil(K / 128)].  The rest as
+    ep_expert_matmul.  Returns out [rows, N] (N/2 if gated) in ``dtype``
+    (bfloat16 or float16), outside autograd and without a backward call."""
+    if fmt not in _FORMATS:
+        raise ValueError(f"unknown fmt {fmt!r} (e4m3 or e5m2)")
+    if not isinstance(x, torch.Tensor) or x.dtype != torch.uint8:
+        raise TypeError("x must be uint8 codes")
+    if not x.is_cuda:
+        raise ValueError("x must be a device tensor")
+    dev = x.device
+    E, N, K = _expert_weights(weights, "weights", torch.uint8, dev)
+    if x.dim() != 2 or x.shape[1] != K:
+        raise ValueError(f"x must be 2-D with {K} columns, is {tuple(x.shape)}")
+    M = x.shape[0]
+    ld = x.stride(0) if M > 1 else (K + 15) // 16 * 16
+    if (K > 1 and x.stride(1) != 1) or ld < K:
+        raise ValueError(f"x must have contiguous rows that do not overlap (strides {tuple(x.stride())})")
+    if gated and N % 2:
+        raise ValueError(f"gated weights have two halves, got {N} rows")
+    blocks = (K + 127) // 128
+    if not isinstance(x_scales, torch.Tensor) or x_scales.dtype not in (torch.float32, torch.uint8):
+        raise TypeError("x_scales must be float32 or uint8")
+    if x_scales.device != dev:
+        raise ValueError(f"x_scales is on {x_scales.device}, not on {dev}")
+    if tuple(x_scales.shape) != (M, blocks):
+        raise ValueError(f"x_scales must be {(M, blocks)}, is {tuple(x_scales.shape)}")
+    _need_on(weight_scales, "weight_scales", torch.float32, dev)
+    if tuple(weight_scales.shape) != (E, (N + 127) // 128, blocks):
+        raise ValueError(f"weight_scales must be {(E, (N + 127) // 128, blocks)}, is "
+                         f"{tuple(weight_scales.shape)}")
+    if dtype not in _HALVES:
+        raise TypeError(f"dtype must be bfloat16 or float16, got {dtype}")
+    if src is not None:
+        _need_on(src, "src", torch.int32, dev, rows)
+    R = int(rows) if rows is not None else (src.numel() if src is not None else M)
+    _segments_of(E, offsets, counts, dev)
+    on = _On(dev, stream)
+    out, ld_out = _out_of(on, out, "out", R, N // 2 if gated else N, dtype, dev)
+    on.call("ep_expert_matmul_fp8", lib().ep_expert_matmul_fp8, x.data_ptr(), _FORMATS[fmt], ld, M,
+            x_scales.data_ptr(), EP_SCALE_UE8M0 if x_scales.dtype == torch.uint8 else EP_SCALE_FP32,
+            x_scales.stride(0), x_scales.stride(1), _ptr(src), weights.data_ptr(),
+            weight_scales.data_ptr(), E, N, K, int(bool(gated)), _ptr(offsets), _ptr(counts), R,
+            out.data_ptr(), _DTYPES[dtype], ld_out)
     return out
 
 

@@ -914,6 +914,141 @@ ep_status_t ep_expert_matmul_w4(const void *x, int dtype, int64_t ld_x, int64_t 
                                 const int32_t *counts, int64_t num_rows, void *out, int64_t ld_out,
                                 void *stream);
 
+/* ---- full-width and 8-bit expert products ------------------------------ */
+
+#define EP_MAX_OUT_FEATURES (1 << 20) /* out_features of the products below */
+
+/*
+ * ep_expert_matmul / ep_expert_glu -- the experts' products on the rows as
+ * the layout groups them, with weights of the rows' type:
+ *
+ *   ep_expert_matmul  out[r] = W[e] x[r]
+ *   ep_expert_glu     out[r] = silu(gate) * up, gate and up the two halves of
+ *                     W[e] x[r], in one kernel
+ *
+ * for the rows r of each expert e.  One expert is a plain matrix product.
+ *
+ * In:  x        dtype (EP_BF16 or EP_FP16) rows of in_features, row stride
+ *               ld_x, num_x_rows of them, aligned to the element.
+ *      src      int32 [num_rows] or NULL: row r of the product is x[src[r]]
+ *               (ep_layout's src: the tokens need not be dispatched first),
+ *               else x[r].
+ *      weights  dtype [num_experts, out_features, in_features], packed; for
+ *               ep_expert_glu the rows are two halves, gate then up
+ *               (out_features even).
+ *      offsets  int32 [num_experts + 1] of the layout, or NULL with one
+ *               expert (all rows).
+ *      counts   int32 [num_experts] or NULL: rows of each expert (for aligned
+ *               or fixed-stride layouts), else offsets[e + 1] - offsets[e].
+ *      num_rows  rows of the layout; it bounds every row: rows past it are
+ *               neither read nor written.  The launch is fitted to it.
+ * Out: out      dtype [num_rows, out_features] (out_features / 2 columns of
+ *               ep_expert_glu), row stride ld_out.
+ *      pre      ep_expert_glu: NULL, or dtype [num_rows, out_features], row
+ *               stride ld_pre: gate and up, for the backward.
+ * Rows that belong to no expert are not written.  Sums are fp32, in a fixed
+ * order; the result (after the activation, in fp32) is rounded once.  src
+ * outside [0, num_x_rows) reads row 0.  No output may overlap an input.
+ * Rows and weights that start on 16 bytes and are whole 16-byte vectors are
+ * fastest.
+ */
+ep_status_t ep_expert_matmul(const void *x, int dtype, int64_t ld_x, int64_t num_x_rows,
+                             const int32_t *src, const void *weights, int num_experts,
+                             int out_features, int in_features, const int32_t *offsets,
+                             const int32_t *counts, int64_t num_rows, void *out, int64_t ld_out,
+                             void *stream);
+ep_status_t ep_expert_glu(const void *x, int dtype, int64_t ld_x, int64_t num_x_rows,
+                          const int32_t *src, const void *weights, int num_experts,
+                          int out_features, int in_features, const int32_t *offsets,
+                          const int32_t *counts, int64_t num_rows, void *out, int64_t ld_out,
+                          void *pre, int64_t ld_pre, void *stream);
+
+/*
+ * ep_expert_matmul_backward / ep_expert_glu_backward -- their gradients: with
+ * d[r] the gradient of W[e] x[r],
+ *
+ *   grad_rows[r]    = W[e]^T d[r]
+ *   grad_weights[e] = sum_r d[r] x[r]^T over the rows of expert e (zeros for
+ *                     an expert without rows)
+ *
+ * d is grad_out for ep_expert_matmul; for ep_expert_glu it is made from
+ * grad_out and pre in fp32 and rounded to dtype (the matrix cores' type), and
+ * lies in the workspace.
+ *
+ * In:  grad_out   dtype [num_rows, out_features] (out_features / 2 columns
+ *                 for ep_expert_glu), row stride ld_grad_out.
+ *      pre        dtype [num_rows, out_features], as ep_expert_glu left it.
+ *      x, src, weights, offsets, counts, num_rows  as given to the forward.
+ * Out: grad_rows  NULL, or dtype [num_rows, in_features], row stride
+ *                 ld_grad_rows: per row of the layout, also with src
+ *                 (ep_permute_backward sums them per token).  Rows that belong
+ *                 to no expert are not written.
+ *      grad_weights  NULL, or [num_experts, out_features, in_features], packed,
+ *                 of grad_weights_dtype: dtype or EP_FP32.
+ *      workspace  ep_expert_glu_backward_workspace_size(...) bytes, 16-byte
+ *                 aligned, for the call's duration (two calls that may overlap
+ *                 in time need one each).
+ * At least one of grad_rows and grad_weights is given; weights may be NULL
+ * without grad_rows, x without grad_weights.  Sums are fp32, in a fixed order,
+ * rounded once.
+ * ep_expert_glu_backward_workspace_size is host arithmetic; 0 for an invalid
+ * shape.
+ */
+ep_status_t ep_expert_matmul_backward(const void *grad_out, int dtype, int64_t ld_grad_out,
+                                      const void *x, int64_t ld_x, int64_t num_x_rows,
+                                      const int32_t *src, const void *weights, int num_experts,
+                                      int out_features, int in_features, const int32_t *offsets,
+                                      const int32_t *counts, int64_t num_rows, void *grad_rows,
+                                      int64_t ld_grad_rows, void *grad_weights,
+                                      int grad_weights_dtype, void *stream);
+size_t ep_expert_glu_backward_workspace_size(int64_t num_rows, int out_features);
+ep_status_t ep_expert_glu_backward(const void *grad_out, int dtype, int64_t ld_grad_out,
+                                   const void *pre, int64_t ld_pre, const void *x, int64_t ld_x,
+                                   int64_t num_x_rows, const int32_t *src, const void *weights,
+                                   int num_experts, int out_features, int in_features,
+                                   const int32_t *offsets, const int32_t *counts, int64_t num_rows,
+                                   void *grad_rows, int64_t ld_grad_rows, void *grad_weights,
+                                   int grad_weights_dtype, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/*
+ * ep_expert_matmul_fp8 -- the same products of rows and weights held in 8-bit
+ * floating point, as ep_dispatch_ex and its kin leave them, scaled per 128
+ * inputs:
+ *
+ *   y[r, n] = sum_b x_scales[r, b] weight_scales[e, n / 128, b]
+ *             sum_{k in b} x[r, k] weights[e, n, k],  b = k / 128
+ *   out[r] = y[r], or silu(gate) * up of its halves if gated
+ *
+ * In:  x        bytes, codes of x_format (EP_OUT_FP8_E4M3 or EP_OUT_FP8_E5M2),
+ *               rows of in_features, row stride ld_x (a multiple of 16),
+ *               num_x_rows of them, 16-byte aligned.
+ *      x_scales  fp32 (EP_SCALE_FP32, EP_SCALE_FP32_POW2) or bytes
+ *               (EP_SCALE_UE8M0, value 2^(byte - 127)): the scale of row r and
+ *               block b at r * scale_row_stride + b * scale_block_stride
+ *               (elements), so row-major and column-major scales both fit.
+ *      src      as ep_expert_matmul; it picks codes and scales.
+ *      weights  bytes, E4M3 codes [num_experts, out_features, in_features],
+ *               packed, 16-byte aligned.
+ *      weight_scales  fp32 [num_experts, ceil(out_features / 128),
+ *               ceil(in_features / 128)], packed.
+ *      gated    1: the rows of the weights are two halves, gate then up.
+ *      offsets, counts, num_rows  as ep_expert_matmul.
+ * Out: out      out_dtype (EP_BF16 or EP_FP16) [num_rows, out_features], or
+ *               out_features / 2 columns if gated, row stride ld_out.
+ * in_features: a multiple of 16, at most EP_MAX_HIDDEN.  Products of codes
+ * are exact; their sums over a block, the product of the two scales and the
+ * sums over blocks are fp32, in a fixed order, and the result is rounded once.
+ * Rows that belong to no expert are not written.
+ */
+ep_status_t ep_expert_matmul_fp8(const void *x, int x_format, int64_t ld_x, int64_t num_x_rows,
+                                 const void *x_scales, int scale_format, int64_t scale_row_stride,
+                                 int64_t scale_block_stride, const int32_t *src,
+                                 const void *weights, const float *weight_scales, int num_experts,
+                                 int out_features, int in_features, int gated,
+                                 const int32_t *offsets, const int32_t *counts, int64_t num_rows,
+                                 void *out, int out_dtype, int64_t ld_out, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
