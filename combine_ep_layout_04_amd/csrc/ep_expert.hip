@@ -29,18 +29,20 @@ struct Product {
     int col_tiles, group;
 };
 
-// WP x WQ wavefronts.  DIRECT: rows and weights in whole 16-byte chunks,
-// loaded into LDS directly; else by way of registers.
-template <typename T, bool GLU, bool DIRECT, int BP, int BQ, int WP, int WQ>
+// WP x WQ wavefronts, a ring of RING operand tiles.  DIRECT: rows and weights
+// in whole 16-byte chunks and in reach of 32-bit offsets, loaded into LDS
+// directly; else by way of registers.
+template <typename T, bool GLU, bool DIRECT, int BP, int BQ, int WP, int WQ, int RING>
 __global__ __launch_bounds__(WP * WQ * 64)
 void expert_kernel(Product<T> a)
 {
     constexpr int kThreads = WP * WQ * 64;
     constexpr int PB = BP / WP / 32, QB = BQ / WQ / 32;
-    using P = RowOperand<BP, kThreads>;
-    using Q = RowOperand<BQ, kThreads>;
-    constexpr int kStage = P::kBytes + Q::kBytes;
-    __shared__ __attribute__((aligned(128))) char lds[2 * kStage];
+    using Off = std::conditional_t<DIRECT, uint32_t, uint64_t>;
+    using P = RowOperand<BP, kThreads, Off>;
+    using Q = RowOperand<BQ, kThreads, Off>;
+    using S = Steps<T, P, Q, PB, QB, RING>;
+    __shared__ __attribute__((aligned(128))) char lds[S::kLds];
 
     int item, tile;
     place_of(a.group, a.col_tiles, item, tile);
@@ -51,27 +53,30 @@ void expert_kernel(Product<T> a)
     const int p0 = wave / WQ * (PB * 32), q0 = wave % WQ * (QB * 32);
     const int half = a.n / 2;
     const int n0 = tile * (GLU ? BP / 2 : BP);
+    const int bytes = a.k * 2;
 
     P p;
     Q q;
-    const T* w = a.w + (int64_t)rb.expert * a.n * a.k;
-    p.init([&](int i) {
+    // offsets from the tile's first row (of the gate half)
+    const T* w = a.w + ((int64_t)rb.expert * a.n + n0) * a.k;
+    p.init(reinterpret_cast<const char*>(w), bytes, [&](int i) {
         int n;
         if constexpr (GLU) {
-            n = n0 + i / 64 * 32 + (i & 31);
-            n = (n < half ? n : half - 1) + (i & 32 ? half : 0);
+            n = i / 64 * 32 + (i & 31);
+            n = (n0 + n < half ? n : half - 1 - n0) + (i & 32 ? half : 0);
         } else {
-            n = n0 + i < a.n ? n0 + i : a.n - 1;
+            n = n0 + i < a.n ? i : a.n - 1 - n0;
         }
-        return reinterpret_cast<const char*>(w + (int64_t)n * a.k);
+        return (Off)n * (Off)bytes;
     });
-    q.init([&](int i) {
-        int64_t r = rb.first + (i < rb.rows ? i : 0);
+    const T* x = a.src != nullptr ? a.x : a.x + rb.first * a.ld_x;
+    q.init(reinterpret_cast<const char*>(x), bytes, [&](int i) {
+        int r = i < rb.rows ? i : 0;
         if (a.src != nullptr) {
-            r = a.src[r];
+            r = a.src[rb.first + r];
             if (r < 0 || r >= a.x_rows) r = 0;
         }
-        return reinterpret_cast<const char*>(a.x + r * a.ld_x);
+        return (Off)r * (Off)(a.ld_x * 2);
     });
 
     f32x16_t acc[PB][QB];
@@ -79,40 +84,12 @@ void expert_kernel(Product<T> a)
     for (int i = 0; i < PB; ++i)
 #pragma unroll
         for (int j = 0; j < QB; ++j) acc[i][j] = f32x16_t{};
-
-    const int bytes = a.k * 2, steps = (bytes + 127) / 128;
+    const int steps = (bytes + 127) / 128;
     if constexpr (DIRECT) {
-        const uint32_t at = lds_address(lds) + wave * 1024;
-        p.load(at, 0, bytes);
-        q.load(at + P::kBytes, 0, bytes);
-        for (int s = 0; s < steps; ++s) {
-            wait_barrier();
-            const int now = (s & 1) * kStage, next = kStage - now;
-            if (s + 1 < steps) {
-                p.load(at + next, s + 1, bytes);
-                q.load(at + next + P::kBytes, s + 1, bytes);
-            }
-            multiply<T, P, Q>(lds + now, lds + now + P::kBytes, p0, q0, acc);
-        }
+        S run(p, q, lds, p0, q0, steps);
+        run.run(acc, bytes / 128);
     } else {
-        uint4 pv[P::kLoads], qv[Q::kLoads];
-        p.template fetch<T>(pv, 0, bytes);
-        q.template fetch<T>(qv, 0, bytes);
-        P::put(lds, pv);
-        Q::put(lds + P::kBytes, qv);
-        for (int s = 0; s < steps; ++s) {
-            __syncthreads();
-            const int now = (s & 1) * kStage, next = kStage - now;
-            if (s + 1 < steps) {
-                p.template fetch<T>(pv, s + 1, bytes);
-                q.template fetch<T>(qv, s + 1, bytes);
-            }
-            multiply<T, P, Q>(lds + now, lds + now + P::kBytes, p0, q0, acc);
-            if (s + 1 < steps) {
-                P::put(lds + next, pv);
-                Q::put(lds + next + P::kBytes, qv);
-            }
-        }
+        steps_by_registers<T, P, Q, PB, QB, kThreads>(p, q, lds, steps, p0, q0, acc);
     }
 
 #pragma unroll
@@ -141,7 +118,7 @@ void expert_kernel(Product<T> a)
     }
 }
 
-template <typename T, bool GLU, bool DIRECT, int BP, int BQ, int WP, int WQ>
+template <typename T, bool GLU, bool DIRECT, int BP, int BQ, int WP, int WQ, int RING>
 hipError_t launch(const ExpertArgs& a, hipStream_t stream)
 {
     Product<T> p = {static_cast<const T*>(a.x), a.ld_x, a.x_rows, a.src, static_cast<const T*>(a.w), a.n, a.k,
@@ -151,20 +128,24 @@ hipError_t launch(const ExpertArgs& a, hipStream_t stream)
     const int n = GLU ? a.n / 2 : a.n;
     p.col_tiles = (n + kCols - 1) / kCols;
     const int64_t items = max_row_blocks(a.num_rows, a.num_experts, BQ);
-    hipLaunchKernelGGL((expert_kernel<T, GLU, DIRECT, BP, BQ, WP, WQ>),
+    hipLaunchKernelGGL((expert_kernel<T, GLU, DIRECT, BP, BQ, WP, WQ, RING>),
                        dim3((unsigned)tile_grid(items, p.group, p.col_tiles)), dim3(WP * WQ * 64), 0, stream, p);
     return hipGetLastError();
 }
 
+// Elements of 16 bits that 32-bit offsets reach.
+bool in_reach(int64_t elements) { return elements <= (int64_t)1 << 31; }
+
 template <typename T, bool GLU>
 hipError_t sized(const ExpertArgs& a, hipStream_t stream)
 {
-    const bool direct = a.k % 8 == 0 && a.ld_x % 8 == 0 &&
+    const int64_t reach = (a.src != nullptr ? a.x_rows : 256) * a.ld_x, gate = GLU ? (a.n / 2 + 256) * (int64_t)a.k : 0;
+    const bool direct = a.k % 8 == 0 && a.ld_x % 8 == 0 && in_reach(reach) && in_reach(gate) &&
                         ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.w)) & 15) == 0;
-    if (!direct) return launch<T, GLU, false, 128, 128, 2, 2>(a, stream);
+    if (!direct) return launch<T, GLU, false, 128, 128, 2, 2, 4>(a, stream);
     const int64_t hold = a.num_rows < a.num_experts ? a.num_rows : a.num_experts;
-    if (a.num_rows / hold >= 192) return launch<T, GLU, true, 256, 256, 2, 4>(a, stream);
-    return launch<T, GLU, true, 128, 128, 2, 2>(a, stream);
+    if (a.num_rows / hold >= 192) return launch<T, GLU, true, 256, 256, 2, 2, 5>(a, stream);
+    return launch<T, GLU, true, 128, 128, 2, 2, 5>(a, stream);
 }
 
 }  // namespace

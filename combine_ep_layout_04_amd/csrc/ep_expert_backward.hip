@@ -31,16 +31,17 @@ struct RowsGrad {
 };
 
 // A tile of BP columns (k) by BQ rows; the reduction goes along n.
-template <typename T, bool DIRECT, int BP, int BQ, int WP, int WQ>
+template <typename T, bool DIRECT, int BP, int BQ, int WP, int WQ, int RING>
 __global__ __launch_bounds__(WP * WQ * 64)
 void rows_grad_kernel(RowsGrad<T> a)
 {
     constexpr int kThreads = WP * WQ * 64;
     constexpr int PB = BP / WP / 32, QB = BQ / WQ / 32;
-    using P = ColOperand<BP, kThreads>;
-    using Q = RowOperand<BQ, kThreads>;
-    constexpr int kStage = P::kBytes + Q::kBytes;
-    __shared__ __attribute__((aligned(128))) char lds[2 * kStage];
+    using Off = std::conditional_t<DIRECT, uint32_t, uint64_t>;
+    using P = ColOperand<BP, kThreads, false, Off>;
+    using Q = RowOperand<BQ, kThreads, Off>;
+    using S = Steps<T, P, Q, PB, QB, RING>;
+    __shared__ __attribute__((aligned(128))) char lds[S::kLds];
 
     int item, tile;
     place_of(a.group, a.col_tiles, item, tile);
@@ -51,21 +52,14 @@ void rows_grad_kernel(RowsGrad<T> a)
     const int p0 = wave / WQ * (PB * 32), q0 = wave % WQ * (QB * 32);
     const int64_t k0 = (int64_t)tile * BP;
 
+    // a chunk that ends past n reads what lies behind the row: the caller keeps
+    // zeros there (DIRECT)
+    const int bytes = DIRECT ? (a.n * 2 + 15) / 16 * 16 : a.n * 2;
     P p;
     Q q;
-    p.init(k0, a.k);
-    q.init([&](int i) {
-        const int64_t r = rb.first + (i < rb.rows ? i : 0);
-        return reinterpret_cast<const char*>(a.grad + r * a.ld_grad);
-    });
-    // this thread's rows of the weights
-    const char* wr[P::kLoads];
-    const int64_t ld_w = (int64_t)a.k * 2;
-#pragma unroll
-    for (int i = 0; i < P::kLoads; ++i)
-        wr[i] = reinterpret_cast<const char*>(a.w) +
-                ((int64_t)rb.expert * a.n + p.row + i * P::kRowStep) * ld_w;
-    auto w_row = [&](int s) { return [&, s](int i) { return wr[i] + s * 64 * ld_w; }; };
+    p.init(reinterpret_cast<const char*>(a.w + (int64_t)rb.expert * a.n * a.k), (int64_t)a.k * 2, a.n, k0, a.k);
+    q.init(reinterpret_cast<const char*>(a.grad + rb.first * a.ld_grad), bytes,
+           [&](int i) { return (Off)(i < rb.rows ? i : 0) * (Off)(a.ld_grad * 2); });
 
     f32x16_t acc[PB][QB];
 #pragma unroll
@@ -73,42 +67,12 @@ void rows_grad_kernel(RowsGrad<T> a)
 #pragma unroll
         for (int j = 0; j < QB; ++j) acc[i][j] = f32x16_t{};
 
-    const int bytes = a.n * 2, steps = (a.n + 63) / 64;
+    const int steps = (a.n + 63) / 64;
     if constexpr (DIRECT) {
-        const uint32_t at = lds_address(lds) + wave * 1024;
-        // a chunk that ends past n reads what lies behind the row: the caller
-        // keeps zeros there
-        const int chunks = (bytes + 15) / 16 * 16;
-        p.load(at, a.n, w_row(0));
-        q.load(at + P::kBytes, 0, chunks);
-        for (int s = 0; s < steps; ++s) {
-            wait_barrier();
-            const int now = (s & 1) * kStage, next = kStage - now;
-            if (s + 1 < steps) {
-                p.load(at + next, a.n - (s + 1) * 64, w_row(s + 1));
-                q.load(at + next + P::kBytes, s + 1, chunks);
-            }
-            multiply<T, P, Q>(lds + now, lds + now + P::kBytes, p0, q0, acc);
-        }
+        S run(p, q, lds, p0, q0, steps);
+        run.run(acc, a.n / 64);
     } else {
-        uint4 pv[P::kLoads], qv[Q::kLoads];
-        p.template fetch<T>(pv, a.n, w_row(0));
-        q.template fetch<T>(qv, 0, bytes);
-        P::put(lds, pv);
-        Q::put(lds + P::kBytes, qv);
-        for (int s = 0; s < steps; ++s) {
-            __syncthreads();
-            const int now = (s & 1) * kStage, next = kStage - now;
-            if (s + 1 < steps) {
-                p.template fetch<T>(pv, a.n - (s + 1) * 64, w_row(s + 1));
-                q.template fetch<T>(qv, s + 1, bytes);
-            }
-            multiply<T, P, Q>(lds + now, lds + now + P::kBytes, p0, q0, acc);
-            if (s + 1 < steps) {
-                P::put(lds + next, pv);
-                Q::put(lds + next + P::kBytes, qv);
-            }
-        }
+        steps_by_registers<T, P, Q, PB, QB, kThreads>(p, q, lds, steps, p0, q0, acc);
     }
 
 #pragma unroll
@@ -137,16 +101,17 @@ struct WeightGrad {
 
 // A tile of BP columns (k) by BQ outputs (n) of one expert; the reduction
 // goes over its rows.  Experts without rows get zeros.
-template <typename T, typename O, bool DIRECT, int BP, int BQ, int WP, int WQ>
+template <typename T, typename O, bool DIRECT, bool GATHER, int BP, int BQ, int WP, int WQ, int RING>
 __global__ __launch_bounds__(WP * WQ * 64)
 void weight_grad_kernel(WeightGrad<T> a)
 {
     constexpr int kThreads = WP * WQ * 64;
     constexpr int PB = BP / WP / 32, QB = BQ / WQ / 32;
-    using P = ColOperand<BP, kThreads>;
-    using Q = ColOperand<BQ, kThreads>;
-    constexpr int kStage = P::kBytes + Q::kBytes;
-    __shared__ __attribute__((aligned(128))) char lds[2 * kStage];
+    using Off = std::conditional_t<DIRECT, uint32_t, uint64_t>;
+    using P = ColOperand<BP, kThreads, GATHER, Off>;
+    using Q = ColOperand<BQ, kThreads, false, Off>;
+    using S = Steps<T, P, Q, PB, QB, RING>;
+    __shared__ __attribute__((aligned(128))) char lds[S::kLds];
 
     const unsigned place = run_place(), tiles = (unsigned)a.k_tiles * (unsigned)a.n_tiles;
     const int expert = (int)(place / tiles);
@@ -164,79 +129,25 @@ void weight_grad_kernel(WeightGrad<T> a)
     const int p0 = wave / WQ * (PB * 32), q0 = wave % WQ * (QB * 32);
     const int64_t k0 = (int64_t)tile_k * BP, n0 = (int64_t)tile_n * BQ;
 
-    P p;
-    Q q;
-    p.init(k0, a.k);
-    q.init(n0, a.n);
-    const char* gr[Q::kLoads];
-    const int64_t ld_g = a.ld_grad * 2, ld_x = a.ld_x * 2;
-#pragma unroll
-    for (int i = 0; i < Q::kLoads; ++i)
-        gr[i] = reinterpret_cast<const char*>(a.grad) + (rb.first + q.row + i * Q::kRowStep) * ld_g;
-    auto g_row = [&](int s) { return [&, s](int i) { return gr[i] + s * 64 * ld_g; }; };
-    // this thread's rows of x for the coming step
-    int xi[P::kLoads];
-    auto find_x = [&](int s) {
-#pragma unroll
-        for (int i = 0; i < P::kLoads; ++i) {
-            const int in = s * 64 + p.row + i * P::kRowStep;
-            xi[i] = rb.first + (in < rb.rows ? in : 0);
-            if (a.src != nullptr) xi[i] = a.src[xi[i]];
-        }
-    };
-    auto x_row = [&](int i) {
-        const int64_t r = xi[i] < 0 || xi[i] >= a.x_rows ? 0 : xi[i];
-        return reinterpret_cast<const char*>(a.x) + r * ld_x;
-    };
-
     f32x16_t acc[PB][QB];
 #pragma unroll
     for (int i = 0; i < PB; ++i)
 #pragma unroll
         for (int j = 0; j < QB; ++j) acc[i][j] = f32x16_t{};
-
-    const int steps = (rb.rows + 63) / 64;
-    if (steps > 0) {
-        find_x(0);
+    if (rb.rows > 0) {
+        P p;
+        Q q;
+        if constexpr (GATHER)
+            p.init(reinterpret_cast<const char*>(a.x), a.ld_x * 2, rb.rows, k0, a.k, a.src + rb.first, a.x_rows);
+        else
+            p.init(reinterpret_cast<const char*>(a.x + rb.first * a.ld_x), a.ld_x * 2, rb.rows, k0, a.k);
+        q.init(reinterpret_cast<const char*>(a.grad + rb.first * a.ld_grad), a.ld_grad * 2, rb.rows, n0, a.n);
+        const int steps = (rb.rows + 63) / 64;
         if constexpr (DIRECT) {
-            const uint32_t at = lds_address(lds) + wave * 1024;
-            p.load(at, rb.rows, x_row);
-            q.load(at + P::kBytes, rb.rows, g_row(0));
-            if (steps > 1) find_x(1);
-            for (int s = 0; s < steps; ++s) {
-                wait_barrier();
-                const int now = (s & 1) * kStage, next = kStage - now;
-                if (s + 1 < steps) {
-                    // the indices have arrived with the loads waited for; so
-                    // that the compiler knows before loads it does not count
-#pragma unroll
-                    for (int i = 0; i < P::kLoads; ++i) asm volatile("" : "+v"(xi[i]));
-                    p.load(at + next, rb.rows - (s + 1) * 64, x_row);
-                    q.load(at + next + P::kBytes, rb.rows - (s + 1) * 64, g_row(s + 1));
-                    if (s + 2 < steps) find_x(s + 2);
-                }
-                multiply<T, P, Q>(lds + now, lds + now + P::kBytes, p0, q0, acc);
-            }
+            S run(p, q, lds, p0, q0, steps);
+            run.run(acc, rb.rows / 64);
         } else {
-            uint4 pv[P::kLoads], qv[Q::kLoads];
-            p.template fetch<T>(pv, rb.rows, x_row);
-            q.template fetch<T>(qv, rb.rows, g_row(0));
-            P::put(lds, pv);
-            Q::put(lds + P::kBytes, qv);
-            for (int s = 0; s < steps; ++s) {
-                __syncthreads();
-                const int now = (s & 1) * kStage, next = kStage - now;
-                if (s + 1 < steps) {
-                    find_x(s + 1);
-                    p.template fetch<T>(pv, rb.rows - (s + 1) * 64, x_row);
-                    q.template fetch<T>(qv, rb.rows - (s + 1) * 64, g_row(s + 1));
-                }
-                multiply<T, P, Q>(lds + now, lds + now + P::kBytes, p0, q0, acc);
-                if (s + 1 < steps) {
-                    P::put(lds + next, pv);
-                    Q::put(lds + next + P::kBytes, qv);
-                }
-            }
+            steps_by_registers<T, P, Q, PB, QB, kThreads>(p, q, lds, steps, p0, q0, acc);
         }
     }
 
@@ -295,56 +206,61 @@ void glu_backward_kernel(const T* __restrict__ grad, int64_t ld_grad, const T* _
         for (int64_t i = 2 * (int64_t)half; i < ld_out; ++i) out[row * ld_out + i] = T{0};
 }
 
-template <typename T, bool DIRECT, int BP, int BQ, int WP, int WQ>
+template <typename T, bool DIRECT, int BP, int BQ, int WP, int WQ, int RING>
 hipError_t launch_rows(const ExpertBackwardArgs& a, hipStream_t stream)
 {
     RowsGrad<T> p = {static_cast<const T*>(a.grad), a.ld_grad, static_cast<const T*>(a.w), a.n, a.k,
                      {a.offsets, a.counts, a.num_experts, (int)a.num_rows},
                      static_cast<T*>(a.grad_rows), a.ld_grad_rows, (a.k + BP - 1) / BP, 8};
     const int64_t items = max_row_blocks(a.num_rows, a.num_experts, BQ);
-    hipLaunchKernelGGL((rows_grad_kernel<T, DIRECT, BP, BQ, WP, WQ>),
+    hipLaunchKernelGGL((rows_grad_kernel<T, DIRECT, BP, BQ, WP, WQ, RING>),
                        dim3((unsigned)tile_grid(items, p.group, p.col_tiles)), dim3(WP * WQ * 64), 0, stream, p);
     return hipGetLastError();
 }
 
-template <typename T, typename O, bool DIRECT, int BP, int BQ, int WP, int WQ>
+template <typename T, typename O, bool DIRECT, bool GATHER, int BP, int BQ, int WP, int WQ, int RING>
 hipError_t launch_weights(const ExpertBackwardArgs& a, hipStream_t stream)
 {
     WeightGrad<T> p = {static_cast<const T*>(a.grad), a.ld_grad, static_cast<const T*>(a.x), a.ld_x, a.x_rows, a.src,
                        a.n, a.k, {a.offsets, a.counts, a.num_experts, (int)a.num_rows},
                        a.grad_w, (a.k + BP - 1) / BP, (a.n + BQ - 1) / BQ};
-    hipLaunchKernelGGL((weight_grad_kernel<T, O, DIRECT, BP, BQ, WP, WQ>),
+    hipLaunchKernelGGL((weight_grad_kernel<T, O, DIRECT, GATHER, BP, BQ, WP, WQ, RING>),
                        dim3((unsigned)tile_grid(a.num_experts, 1, p.k_tiles * p.n_tiles)), dim3(WP * WQ * 64), 0,
                        stream, p);
     return hipGetLastError();
 }
 
+// Elements of 16 bits that 32-bit offsets reach.
+bool in_reach(int64_t elements) { return elements <= (int64_t)1 << 31; }
 bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
 
-template <typename T, typename O>
+template <typename T, typename O, bool GATHER>
 hipError_t weights_sized(const ExpertBackwardArgs& a, hipStream_t stream)
 {
     const bool direct = a.k % 8 == 0 && a.ld_x % 8 == 0 && (a.n % 8 == 0 || a.padded) && a.ld_grad % 8 == 0 &&
-                        !off16(a.x) && !off16(a.grad);
-    if (!direct) return launch_weights<T, O, false, 128, 128, 2, 2>(a, stream);
-    if (a.num_rows / a.num_experts >= 192) return launch_weights<T, O, true, 256, 256, 2, 4>(a, stream);
-    return launch_weights<T, O, true, 128, 128, 2, 2>(a, stream);
+                        in_reach((GATHER ? a.x_rows : 64) * a.ld_x) && in_reach(64 * a.ld_grad) && !off16(a.x) &&
+                        !off16(a.grad);
+    if (!direct) return launch_weights<T, O, false, GATHER, 128, 128, 2, 2, 4>(a, stream);
+    if (a.num_rows / a.num_experts >= 192) return launch_weights<T, O, true, GATHER, 256, 256, 2, 2, 5>(a, stream);
+    return launch_weights<T, O, true, GATHER, 128, 128, 2, 2, 5>(a, stream);
 }
 
 template <typename T>
 hipError_t backward(const ExpertBackwardArgs& a, hipStream_t stream)
 {
     if (a.grad_rows != nullptr && a.num_rows > 0) {
-        const bool direct = a.k % 8 == 0 && (a.n % 8 == 0 || a.padded) && a.ld_grad % 8 == 0 && !off16(a.w) &&
-                            !off16(a.grad);
+        const bool direct = a.k % 8 == 0 && (a.n % 8 == 0 || a.padded) && a.ld_grad % 8 == 0 &&
+                            in_reach(256 * a.ld_grad) && !off16(a.w) && !off16(a.grad);
         const int64_t hold = a.num_rows < a.num_experts ? a.num_rows : a.num_experts;
-        const hipError_t err = !direct ? launch_rows<T, false, 128, 128, 2, 2>(a, stream)
-                               : a.num_rows / hold >= 192 ? launch_rows<T, true, 256, 256, 2, 4>(a, stream)
-                                                          : launch_rows<T, true, 128, 128, 2, 2>(a, stream);
+        const hipError_t err = !direct ? launch_rows<T, false, 128, 128, 2, 2, 4>(a, stream)
+                               : a.num_rows / hold >= 192 ? launch_rows<T, true, 256, 256, 2, 2, 5>(a, stream)
+                                                          : launch_rows<T, true, 128, 128, 2, 2, 5>(a, stream);
         if (err != hipSuccess) return err;
     }
     if (a.grad_w == nullptr) return hipSuccess;
-    return a.wide_w ? weights_sized<T, float>(a, stream) : weights_sized<T, T>(a, stream);
+    if (a.src != nullptr)
+        return a.wide_w ? weights_sized<T, float, true>(a, stream) : weights_sized<T, T, true>(a, stream);
+    return a.wide_w ? weights_sized<T, float, false>(a, stream) : weights_sized<T, T, false>(a, stream);
 }
 
 }  // namespace

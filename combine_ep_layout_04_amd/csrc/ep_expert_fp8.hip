@@ -107,16 +107,25 @@ __device__ __forceinline__ Codes codes_part(const char* lds, int row0, int b, in
                  *reinterpret_cast<const uint4*>(p + (((4 * s + 2 + h) ^ turn) << 4))};
 }
 
+template <int I, typename O>
+__device__ __forceinline__ void load_operand(O& o, uint32_t to, int s)
+{
+    if constexpr (I < O::kLoads) {
+        o.template load_end<I>(to, s);
+        load_operand<I + 1>(o, to, s);
+    }
+}
+
 // SPLIT: the gated product's halves whose second does not start with a block
 // of 128 outputs; a tile's rows of it then lie in two blocks.
-template <typename T, int FORMAT, bool GLU, bool SPLIT, int BP, int BQ, int WP, int WQ>
+template <typename T, int FORMAT, bool GLU, bool SPLIT, typename OFF, int BP, int BQ, int WP, int WQ>
 __global__ __launch_bounds__(WP * WQ * 64)
 void fp8_kernel(Scaled a)
 {
     constexpr int kThreads = WP * WQ * 64;
     constexpr int PB = BP / WP / 32, QB = BQ / WQ / 32;
-    using P = RowOperand<BP, kThreads>;
-    using Q = RowOperand<BQ, kThreads>;
+    using P = RowOperand<BP, kThreads, OFF>;
+    using Q = RowOperand<BQ, kThreads, OFF>;
     constexpr int kStage = P::kBytes + Q::kBytes;
     __shared__ __attribute__((aligned(128))) char lds[2 * kStage];
 
@@ -132,32 +141,34 @@ void fp8_kernel(Scaled a)
 
     P p;
     Q q;
-    const char* w = a.w + (int64_t)rb.expert * a.n * a.k;
-    p.init([&](int i) {
+    // offsets from the tile's first row (of the gate half)
+    p.init(a.w + ((int64_t)rb.expert * a.n + n0) * a.k, a.k, [&](int i) {
         int n;
         if constexpr (GLU) {
-            n = n0 + i / 64 * 32 + (i & 31);
-            n = (n < half ? n : half - 1) + (i & 32 ? half : 0);
+            n = i / 64 * 32 + (i & 31);
+            n = (n0 + n < half ? n : half - 1 - n0) + (i & 32 ? half : 0);
         } else {
-            n = n0 + i < a.n ? n0 + i : a.n - 1;
+            n = n0 + i < a.n ? i : a.n - 1 - n0;
         }
-        return w + (int64_t)n * a.k;
+        return (OFF)n * (OFF)a.k;
     });
+    // a row of the tile, from the first (of all of x with src)
     auto x_row = [&](int i) {
-        int64_t r = rb.first + (i < rb.rows ? i : 0);
+        int r = i < rb.rows ? i : 0;
         if (a.src != nullptr) {
-            r = a.src[r];
+            r = a.src[rb.first + r];
             if (r < 0 || r >= a.x_rows) r = 0;
         }
         return r;
     };
-    q.init([&](int i) { return a.x + x_row(i) * a.ld_x; });
+    const int64_t x0 = a.src != nullptr ? 0 : rb.first;
+    q.init(a.x + x0 * a.ld_x, a.k, [&](int i) { return (OFF)x_row(i) * (OFF)a.ld_x; });
 
     // scales: of this lane's rows, and of the tile's weights (the gate's and
     // the up's, or the first and second 128 outputs of this wavefront's)
     int64_t xs_at[QB];
 #pragma unroll
-    for (int j = 0; j < QB; ++j) xs_at[j] = x_row(q0 + j * 32 + (lane & 31)) * a.scale_row;
+    for (int j = 0; j < QB; ++j) xs_at[j] = (x0 + x_row(q0 + j * 32 + (lane & 31))) * a.scale_row;
     constexpr int kW = GLU ? (SPLIT ? 3 : 2) : 1;
     const float* ws_row[kW];
     const float* ws = a.w_scales + (int64_t)rb.expert * a.n_blocks * a.k_blocks;
@@ -191,8 +202,11 @@ void fp8_kernel(Scaled a)
 
     const int steps = a.k_blocks;
     const uint32_t at = lds_address(lds) + wave * 1024;
-    p.load(at, 0, a.k);
-    q.load(at + P::kBytes, 0, a.k);
+    auto load_all = [&](uint32_t to, int s) {
+        load_operand<0>(p, to, s);
+        load_operand<0>(q, to + P::kBytes, s);
+    };
+    load_all(at, 0);
     load_scales(0);
     for (int s = 0; s < steps; ++s) {
         wait_barrier();
@@ -211,8 +225,7 @@ void fp8_kernel(Scaled a)
         }
         const int now = (s & 1) * kStage, next = kStage - now;
         if (s + 1 < steps) {
-            p.load(at + next, s + 1, a.k);
-            q.load(at + next + P::kBytes, s + 1, a.k);
+            load_all(at + next, s + 1);
             load_scales(s + 1);
         }
         const char* pl = lds + now;
@@ -393,14 +406,14 @@ Scaled scaled(const ExpertFp8Args& a)
                   {a.offsets, a.counts, a.num_experts, (int)a.num_rows}, a.out, a.ld_out, 0, 8};
 }
 
-template <typename T, int FORMAT, bool GLU, bool SPLIT, int BP, int BQ, int WP, int WQ>
+template <typename T, int FORMAT, bool GLU, bool SPLIT, typename OFF, int BP, int BQ, int WP, int WQ>
 hipError_t launch(const ExpertFp8Args& a, hipStream_t stream)
 {
     Scaled p = scaled(a);
     constexpr int kCols = GLU ? BP / 2 : BP;
     p.col_tiles = ((GLU ? a.n / 2 : a.n) + kCols - 1) / kCols;
     const int64_t items = max_row_blocks(a.num_rows, a.num_experts, BQ);
-    hipLaunchKernelGGL((fp8_kernel<T, FORMAT, GLU, SPLIT, BP, BQ, WP, WQ>),
+    hipLaunchKernelGGL((fp8_kernel<T, FORMAT, GLU, SPLIT, OFF, BP, BQ, WP, WQ>),
                        dim3((unsigned)tile_grid(items, p.group, p.col_tiles)), dim3(WP * WQ * 64), 0, stream, p);
     return hipGetLastError();
 }
@@ -425,9 +438,12 @@ hipError_t sized(const ExpertFp8Args& a, hipStream_t stream)
     const int64_t each = a.num_rows / hold;
     if (each <= 16) return launch_few<T, FORMAT, GLU, 2, 1, 8>(a, stream);
     if (each <= 32) return launch_few<T, FORMAT, GLU, 2, 2, 4>(a, stream);
-    if (GLU && a.n / 2 % 128 != 0) return launch<T, FORMAT, GLU, GLU, 128, 128, 2, 2>(a, stream);
-    if (each >= 192) return launch<T, FORMAT, GLU, false, 256, 256, 2, 4>(a, stream);
-    return launch<T, FORMAT, GLU, false, 128, 128, 2, 2>(a, stream);
+    // rows that 32-bit offsets do not reach, or two scales a tile: the general form
+    const int64_t reach = (a.src != nullptr ? a.x_rows : 256) * a.ld_x, gate = GLU ? (a.n / 2 + 256) * (int64_t)a.k : 0;
+    if ((GLU && a.n / 2 % 128 != 0) || reach >= (int64_t)1 << 32 || gate >= (int64_t)1 << 32)
+        return launch<T, FORMAT, GLU, GLU, uint64_t, 128, 128, 2, 2>(a, stream);
+    if (each >= 192) return launch<T, FORMAT, GLU, false, uint32_t, 256, 256, 2, 4>(a, stream);
+    return launch<T, FORMAT, GLU, false, uint32_t, 128, 128, 2, 2>(a, stream);
 }
 
 template <typename T>

@@ -14,13 +14,15 @@
 // reads of the matrix operands meet every bank once:
 //
 //   * an operand that lies along the reduction in memory (RowOperand): rows of
-//     8 chunks; chunk c of row r at place c ^ ((r / 2) % 8).  A lane reads 16
+//     8 chunks, chunk c of row r at place c ^ ((r / 2) % 8).  A lane reads 16
 //     bytes of its row.
 //   * an operand that lies across it (ColOperand): a row of the tile is one
 //     step of the reduction, in 64-byte groups; group g of row r at place
 //     g ^ (r % 4).  Lanes read it with the transposing LDS load (16 lanes, 4
 //     rows of 16 elements: lane i gets column i).
 #pragma once
+
+#include <type_traits>
 
 #include "ep_device.h"
 #include "ep_types.h"
@@ -181,21 +183,34 @@ __device__ __forceinline__ void place_of(int group, int col_tiles, int& item, in
 // What lanes read in place of chunks past the end.
 __device__ const uint4 kZeroChunk[1] = {{0u, 0u, 0u, 0u}};
 
-// 16 bytes a lane from global memory to LDS: lane l's go to lds + 16 l.  The
-// compiler does not count these loads: wait_barrier() waits for them.
-__device__ __forceinline__ void load_lds(uint32_t lds, const char* from)
+// 16 bytes a lane from global memory to LDS, from base + off: lane l's go to
+// lds + AT + 16 l.  The compiler does not count these loads: wait_barrier()
+// waits for them.
+template <int AT>
+__device__ __forceinline__ void load_lds(uint32_t lds, const char* base, uint32_t off)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+    asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3"
                  :
-                 : "s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(from)
-                 : "memory", "m0");
+                 : "s"(lds), "n"(AT), "v"(off), "s"(base)
+                 : "m0", "scc");
+}
+// The same where some lanes have nothing to read: zeros for these.
+template <int AT>
+__device__ __forceinline__ void load_lds_or_zero(uint32_t lds, const char* base, uint64_t off, bool live)
+{
+    const char* from = live ? base + off : reinterpret_cast<const char*>(kZeroChunk);
+    asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, off"
+                 :
+                 : "s"(lds), "n"(AT), "v"(from)
+                 : "m0", "scc");
 }
 
-// This wavefront's loads into LDS have arrived and its LDS accesses are done,
-// then so are those of the whole workgroup.
+// This wavefront's loads into LDS have arrived but for the last LEFT, and its
+// LDS accesses are done; then so are those of the whole workgroup.
+template <int LEFT = 0>
 __device__ __forceinline__ void wait_barrier()
 {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
 }
 
 __device__ __forceinline__ uint32_t lds_address(const char* p)
@@ -217,103 +232,174 @@ __device__ __forceinline__ uint4 fetch16(const char* p, int valid)
 }
 
 // An operand that lies along the reduction: ROWS rows by 128 bytes.
-template <int ROWS, int THREADS>
+// OFF holds the rows' offsets; with 32 bits a load takes no address arithmetic.
+template <int ROWS, int THREADS, typename OFF = uint32_t>
 struct RowOperand {
     static constexpr int kLoads = ROWS * 8 / THREADS;
     static constexpr int kBytes = ROWS * 128;
-    const char* at[kLoads];
-    int chunk;
+    static constexpr int kRowStep = THREADS / 8;    // a multiple of 16: the turn is the same for all
+    static_assert(kRowStep % 16 == 0, "rows of a thread share their turn");
+    const char* base;
+    OFF off[kLoads];
+    int chunk, bytes;
 
-    // row_at(i): the start of row i of the tile.
+    // What the places of row r's chunks are turned by.
+    __device__ __forceinline__ static int turn(int r) { return (r >> 1) & 7; }
+
+    // Rows of `length` bytes; row i of the tile starts off_of(i) bytes behind
+    // `from` (the same in every lane).
     template <typename F>
-    __device__ __forceinline__ void init(F row_at)
+    __device__ __forceinline__ void init(const char* from, int length, F off_of)
     {
         const int t = threadIdx.x;
-        chunk = (t & 7) ^ ((t >> 4) & 7);
+        base = from;
+        bytes = length;
+        chunk = (t & 7) ^ turn(t / 8);
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) at[i] = row_at(t / 8 + i * (THREADS / 8)) + chunk * 16;
+        for (int i = 0; i < kLoads; ++i) off[i] = off_of(t / 8 + i * kRowStep) + chunk * 16;
     }
-    // Step `step` into LDS; of the reduction `bytes` are there (a whole
-    // number of chunks).
-    __device__ __forceinline__ void load(uint32_t lds, int step, int bytes) const
+    // This thread's I-th chunk of step s into LDS.
+    template <int I>
+    __device__ __forceinline__ void load(uint32_t lds, int s) const
     {
-        const bool out = step * 128 + 128 > bytes && step * 128 + chunk * 16 >= bytes;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            load_lds(lds + i * THREADS * 16,
-                     out ? reinterpret_cast<const char*>(kZeroChunk) : at[i] + (int64_t)step * 128);
+        if constexpr (sizeof(OFF) == 4) load_lds<I * THREADS * 16>(lds, base + (int64_t)s * 128, off[I]);
+        else load_lds_or_zero<I * THREADS * 16>(lds, base + (int64_t)s * 128, off[I], true);
     }
-    // The same by way of registers, for rows that do not start on 16 bytes
-    // or do not end with a chunk.
+    // The same for a step that may be the last, of a reduction that is a whole
+    // number of chunks.
+    template <int I>
+    __device__ __forceinline__ void load_end(uint32_t lds, int s) const
+    {
+        load_lds_or_zero<I * THREADS * 16>(lds, base + (int64_t)s * 128, off[I], s * 128 + chunk * 16 < bytes);
+    }
+    __device__ __forceinline__ void found() const {}
+    // By way of registers, for rows that do not start on 16 bytes or do not
+    // end with a chunk.
     template <typename T>
-    __device__ __forceinline__ void fetch(uint4 (&v)[kLoads], int step, int bytes) const
+    __device__ __forceinline__ void fetch(uint4 (&v)[kLoads], int s) const
     {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
-            v[i] = fetch16<T>(at[i] + (int64_t)step * 128, (bytes - step * 128 - chunk * 16) / 2);
+            v[i] = fetch16<T>(base + (int64_t)s * 128 + off[i], (bytes - s * 128 - chunk * 16) / 2);
     }
-    __device__ __forceinline__ static void put(char* lds, const uint4 (&v)[kLoads])
+    // Chunk c of the row of this lane in block b of the wavefront's rows.
+    __device__ __forceinline__ static uint4 chunk_of(const char* lds, int row0, int b, int c)
     {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            *reinterpret_cast<uint4*>(lds + (i * THREADS + threadIdx.x) * 16) = v[i];
+        const int r = threadIdx.x & 31;
+        return *reinterpret_cast<const uint4*>(lds + (row0 + r) * 128 + b * 4096 + ((c ^ turn(r)) << 4));
     }
     // Operand of a 32-row matrix instruction: 8 elements of 16 bits, part s
-    // (of 4) of the step, rows 32 b .. of this wavefront's.
+    // of the step.
     __device__ __forceinline__ static uint4 part(const char* lds, int row0, int b, int s)
     {
-        const int l = threadIdx.x & 63, r = l & 31;
-        return *reinterpret_cast<const uint4*>(lds + (row0 + r) * 128 + b * 4096 +
-                                               (((2 * s + (l >> 5)) ^ ((r >> 1) & 7)) << 4));
+        return chunk_of(lds, row0, b, 2 * s + ((threadIdx.x >> 5) & 1));
     }
 };
 
 // An operand of 16-bit elements that lies across the reduction: 64 rows (its
-// steps) by COLS columns.
-template <int COLS, int THREADS>
+// steps) by COLS columns.  With GATHER the rows are picked by an index each.
+template <int COLS, int THREADS, bool GATHER = false, typename OFF = uint32_t>
 struct ColOperand {
     static constexpr int kChunks = COLS / 8;
     static constexpr int kLoads = 64 * kChunks / THREADS;
     static constexpr int kBytes = 64 * COLS * 2;
-    static constexpr int kRowStep = THREADS / kChunks;      // a multiple of 4: the turn is the same for all
+    static constexpr int kRowStep = THREADS / kChunks;  // a multiple of 4: the turn is the same for all
+    static constexpr int kSide = 64 / kChunks;          // rows a wavefront loads at a time
     static_assert(kRowStep % 4 == 0, "rows of a thread share their turn");
-    int row;            // of the tile, this thread's first
-    int64_t column;     // byte offset of its chunk in a row
-    int valid;          // elements of it that are there
+    typedef const __attribute__((address_space(4))) int32_t* scalar_ptr;
+    const char* base;
+    OFF off[kLoads];
+    int64_t ld;                 // bytes
+    int row, rows;              // of the tile this thread's first; of the reduction
+    int valid;                  // elements of its chunk that are there
+    int wave_row;
+    scalar_ptr index;           // GATHER: of the reduction's rows, below `bound`
+    int64_t bound;
+    int next[GATHER ? kLoads : 1][kSide];   // of the coming step's rows
 
-    // Columns first .. of `cols`.
-    __device__ __forceinline__ void init(int64_t first, int64_t cols)
+    // `count` rows, `stride` bytes apart, from `from` on (GATHER: picked by
+    // `pick`, below `limit`); columns first .. of `cols`.
+    __device__ __forceinline__ void init(const char* from, int64_t stride, int count, int64_t first, int64_t cols,
+                                         const int32_t* pick = nullptr, int64_t limit = 0)
     {
         const int t = threadIdx.x, p = t % kChunks;
         row = t / kChunks;
+        wave_row = __builtin_amdgcn_readfirstlane(row);
+        base = from;
+        ld = stride;
+        rows = count;
+        index = (scalar_ptr)pick;
+        bound = limit;
         const int64_t c = first + ((((p >> 2) ^ (row & 3)) << 2) | (p & 3)) * 8;
         valid = c + 8 <= cols ? 8 : c < cols ? (int)(cols - c) : 0;
-        column = valid > 0 ? c * 2 : 0;
+        const OFF column = valid > 0 ? (OFF)c * 2 : 0;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) off[i] = (GATHER ? 0 : (OFF)((row + i * kRowStep) * ld)) + column;
+        if constexpr (GATHER) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) find(0, i);
+        }
     }
-    // row_at(i): the start of this thread's i-th row of this step (row +
-    // i kRowStep); `left` rows are there.
-    template <typename F>
-    __device__ __forceinline__ void load(uint32_t lds, int left, F row_at) const
+    // GATHER: the indices are read ahead, by scalar loads, whose waiting does
+    // not touch the loads into LDS.
+    __device__ __forceinline__ void find(int s, int i)
+    {
+#pragma unroll
+        for (int j = 0; j < kSide; ++j) {
+            const int in = s * 64 + wave_row + i * kRowStep + j;
+            next[i][j] = index[in < rows ? in : 0];
+        }
+    }
+    // Makes the compiler wait for them here.
+    __device__ __forceinline__ void found()
+    {
+        if constexpr (GATHER) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+                for (int j = 0; j < kSide; ++j) asm volatile("" : "+s"(next[i][j]));
+        }
+    }
+    // The offset of this thread's i-th row of the coming step, from `base`;
+    // reads the index after it.
+    __device__ __forceinline__ uint32_t gathered(int s, int i)
+    {
+        uint32_t o = 0;
+#pragma unroll
+        for (int j = 0; j < kSide; ++j) {
+            const int r = next[i][j];
+            const uint32_t at = r < 0 || r >= bound ? 0u : (uint32_t)r * (uint32_t)ld;
+            o = j == 0 || (int)(threadIdx.x & 63) / kChunks == j ? at : o;
+        }
+        find(s + 1, i);
+        return o;
+    }
+    template <int I>
+    __device__ __forceinline__ void load(uint32_t lds, int s)
+    {
+        if constexpr (GATHER) load_lds<I * THREADS * 16>(lds, base, gathered(s, I) + off[I]);
+        else load_lds<I * THREADS * 16>(lds, base + s * 64 * ld, off[I]);
+    }
+    template <int I>
+    __device__ __forceinline__ void load_end(uint32_t lds, int s)
+    {
+        const bool live = s * 64 + row + I * kRowStep < rows;
+        if constexpr (GATHER) load_lds_or_zero<I * THREADS * 16>(lds, base, gathered(s, I) + off[I], live);
+        else load_lds_or_zero<I * THREADS * 16>(lds, base + s * 64 * ld, off[I], live);
+    }
+    template <typename T>
+    __device__ __forceinline__ void fetch(uint4 (&v)[kLoads], int s)
     {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const char* p = row_at(i) + column;
-            load_lds(lds + i * THREADS * 16,
-                     row + i * kRowStep < left ? p : reinterpret_cast<const char*>(kZeroChunk));
+            const int in = s * 64 + row + i * kRowStep;
+            const char* from = base + (int64_t)s * 64 * ld + off[i];
+            if constexpr (GATHER) {
+                const int r = index[in < rows ? in : 0];
+                from = base + (r < 0 || r >= bound ? 0 : r * ld) + off[i];
+            }
+            v[i] = fetch16<T>(from, in < rows ? valid : 0);
         }
-    }
-    template <typename T, typename F>
-    __device__ __forceinline__ void fetch(uint4 (&v)[kLoads], int left, F row_at) const
-    {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            v[i] = fetch16<T>(row_at(i) + column, row + i * kRowStep < left ? valid : 0);
-    }
-    __device__ __forceinline__ static void put(char* lds, const uint4 (&v)[kLoads])
-    {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            *reinterpret_cast<uint4*>(lds + (i * THREADS + threadIdx.x) * 16) = v[i];
     }
     // Operand of a 32-column matrix instruction: part s of the step, columns
     // col0 + 32 b ...
@@ -331,22 +417,243 @@ struct ColOperand {
     }
 };
 
-// One step: PB x QB blocks of 32 x 32 from the operands' tiles.
-template <typename T, typename P, typename Q, int PB, int QB>
-__device__ __forceinline__ void multiply(const char* p_lds, const char* q_lds, int p0, int q0,
-                                         f32x16_t (&acc)[PB][QB])
+// A thread's chunks from registers to its operand's place in LDS.
+template <int THREADS, int LOADS>
+__device__ __forceinline__ void put_chunks(char* lds, const uint4 (&v)[LOADS])
 {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-        uint4 p[PB], q[QB];
+    for (int i = 0; i < LOADS; ++i) *reinterpret_cast<uint4*>(lds + (i * THREADS + threadIdx.x) * 16) = v[i];
+}
+
+// ---- the steps
+
+// A tile's steps: PB x QB blocks of 32 x 32 per wavefront over the reduction,
+// 128 bytes of it a step, from LDS.
+//
+// The two operands' tiles of a step take turns in a ring of RING places
+// (P of step 0, Q of 0, P of 1, ...; with 5 places of 32 KiB all of LDS): an
+// odd ring keeps more than a step in flight where LDS does not hold three.
+//
+// Two sets of operands in registers: those of a part (16 elements of the
+// reduction, 32 bytes) are read while the part before it is multiplied.  The
+// step changes before its last part, whose operands are in registers by then:
+// its multiplications cover the first reads of the next step.  From there to
+// the next such place the loads into the two places that became free go out,
+// dealt out evenly: sent in one go they fill the queue of the memory pipeline,
+// and the wavefront stands still before its matrix instructions.  Reads and
+// loads take their turns after matrix instructions, by hand.
+template <typename T, typename P, typename Q, int PB, int QB, int RING>
+struct Steps {
+    static constexpr int kPlace = P::kBytes > Q::kBytes ? P::kBytes : Q::kBytes;
+    static constexpr int kMuls = PB * QB, kReads = PB + QB;
+    static constexpr int kLds = kPlace * RING;
+    static constexpr int kLoads = P::kLoads + Q::kLoads;
+    static constexpr bool kOdd = RING % 2 == 1;
+    // loads that may be under way when a step changes: those of the tiles
+    // behind the next step's
+    static constexpr int kLeft = (RING - 4) / 2 * kLoads + (kOdd ? P::kLoads : 0);
+    static_assert(RING >= 4, "two steps at least");
+
+    P& first;
+    Q& second;
+    char* lds;
+    uint32_t at;
+    int p0, q0, steps;
+    uint4 p[2][PB], q[2][QB];
+
+    __device__ __forceinline__ Steps(P& a, Q& b, char* shared, int p_row, int q_row, int num_steps)
+        : first(a), second(b), lds(shared), p0(p_row), q0(q_row), steps(num_steps)
+    {
+        at = lds_address(lds) + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) * 1024;
+    }
+
+    __device__ __forceinline__ static int place(int v) { return v >= RING * kPlace ? v - RING * kPlace : v; }
+
+    // The I-th load of those that go out from step s's last part on, into the
+    // places of step s: `now` (P) and behind it (Q).
+    template <int I, bool END>
+    __device__ __forceinline__ void load_one(int s, int now)
+    {
+        if constexpr (kOdd) {
+            // Q's next tile falls on P's place and comes first
+            if constexpr (I < Q::kLoads) {
+                const int to = s + RING / 2;
+                if constexpr (END) {
+                    if (to < steps) second.template load_end<I>(at + now, to);
+                } else {
+                    second.template load<I>(at + now, to);
+                }
+            } else {
+                const int to = s + RING / 2 + 1;
+                if constexpr (END) {
+                    if (to < steps) first.template load_end<I - Q::kLoads>(at + place(now + kPlace), to);
+                } else {
+                    first.template load<I - Q::kLoads>(at + place(now + kPlace), to);
+                }
+            }
+        } else {
+            const int to = s + RING / 2;
+            if constexpr (I < P::kLoads) {
+                if constexpr (END) {
+                    if (to < steps) first.template load_end<I>(at + now, to);
+                } else {
+                    first.template load<I>(at + now, to);
+                }
+            } else {
+                if constexpr (END) {
+                    if (to < steps) second.template load_end<I - P::kLoads>(at + place(now + kPlace), to);
+                } else {
+                    second.template load<I - P::kLoads>(at + place(now + kPlace), to);
+                }
+            }
+        }
+    }
+    template <int I, int UPTO, bool END>
+    __device__ __forceinline__ void load_some(int s, int now)
+    {
+        if constexpr (I < UPTO) {
+            load_one<I, END>(s, now);
+            load_some<I + 1, UPTO, END>(s, now);
+        }
+    }
+
+    template <int R>
+    __device__ __forceinline__ void read_one(int set, int now, int part)
+    {
+        if constexpr (R < QB) q[set][R] = Q::part(lds + place(now + kPlace), q0, R, part);
+        else p[set][R - QB] = P::part(lds + now, p0, R - QB, part);
+    }
+    template <int R, int UPTO>
+    __device__ __forceinline__ void read_some(int set, int now, int part)
+    {
+        if constexpr (R < UPTO) {
+            read_one<R>(set, now, part);
+            read_some<R + 1, UPTO>(set, now, part);
+        }
+    }
+
+    // Matrix instruction M of a part and what takes its turn after it: reads of
+    // part `next` of the step at `then` into the other set, and the SHARE-th
+    // quarter of the loads that follow step s at `now`.  LOADS: 0 none, 1 of
+    // full steps, 2 of steps that may be the last or behind it.
+    template <int SET, bool READ, int LOADS, int SHARE, int M = 0>
+    __device__ __forceinline__ void part(f32x16_t (&acc)[PB][QB], int then, int next, int s, int now)
+    {
+        if constexpr (M < kMuls) {
+            constexpr int i = M / QB, j = M % QB;
+            acc[i][j] = mma32(p[SET][i], q[SET][j], acc[i][j], static_cast<const T*>(nullptr));
+            if constexpr (READ) {
+                // all reads within the first three quarters
+                constexpr int kFrom = kReads * M * 4 / (kMuls * 3), kTo = kReads * (M + 1) * 4 / (kMuls * 3);
+                read_some<(kFrom < kReads ? kFrom : kReads), (kTo < kReads ? kTo : kReads)>(SET ^ 1, then, next);
+            }
+            if constexpr (LOADS != 0) {
+                constexpr int kOf = kLoads * SHARE / 4, kCount = kLoads * (SHARE + 1) / 4 - kOf;
+                load_some<kOf + kCount * M / kMuls, kOf + kCount * (M + 1) / kMuls, LOADS == 2>(s, now);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            part<SET, READ, LOADS, SHARE, M + 1>(acc, then, next, s, now);
+        }
+    }
+
+    // Step s, whose P lies at `now`.  REST, MORE: the loads that go out in its
+    // first three parts and its last (as LOADS of part()); LEFT: loads that may
+    // be under way when it changes; NEXT: another step follows.
+    template <int REST, int MORE, int LEFT, bool NEXT>
+    __device__ __forceinline__ void step(f32x16_t (&acc)[PB][QB], int s, int now)
+    {
+        const int before = now - 2 * kPlace < 0 ? now + (RING - 2) * kPlace : now - 2 * kPlace;
+        const int then = place(now + 2 * kPlace);
+        part<0, true, REST, 1>(acc, now, 1, s - 1, before);
+        part<1, true, REST, 2>(acc, now, 2, s - 1, before);
+        part<0, true, REST, 3>(acc, now, 3, s - 1, before);
+        if constexpr (NEXT) wait_barrier<LEFT>();
+        if constexpr (MORE != 0) {
+            first.found();
+            second.found();
+        }
+        part<1, NEXT, MORE, 0>(acc, then, 0, s, now);
+    }
+
+    // full: steps that are whole (all, or all but the last).
+    __device__ __forceinline__ void run(f32x16_t (&acc)[PB][QB], int full)
+    {
+        constexpr int kLast = (RING - 1) / 2;       // the last tile in the ring belongs to this step from now
+        constexpr int kAhead = (RING + 1) / 2;      // the last load that follows a step to this one
+        start<0>();
+        if (steps > kLast) wait_barrier<(RING - 2) / 2 * kLoads + (kOdd ? P::kLoads : 0)>();
+        else wait_barrier();
+        read_some<0, kReads>(0, 0, 0);
+        int s = 0, now = 0;
+        auto turn = [&] {
+            ++s;
+            now = place(now + 2 * kPlace);
+        };
+        if (steps > kLast) {
+            step<0, 2, kLeft, true>(acc, s, now);
+            turn();
+            for (; s + kAhead < full; turn()) step<1, 1, kLeft, true>(acc, s, now);
+            for (; s + kLast < steps; turn()) step<2, 2, kLeft, true>(acc, s, now);
+        }
+        for (; s + 1 < steps; turn()) step<2, 2, 0, true>(acc, s, now);
+        step<0, 0, 0, false>(acc, s, now);
+    }
+    template <int U>
+    __device__ __forceinline__ void start()
+    {
+        if constexpr (U < RING) {
+            if (U / 2 < steps) {
+                if constexpr (U % 2 == 0) all<0, P>(first, U * kPlace, U / 2);
+                else all<0, Q>(second, U * kPlace, U / 2);
+            }
+            start<U + 1>();
+        }
+    }
+    template <int I, typename O>
+    __device__ __forceinline__ void all(O& o, int to, int s)
+    {
+        if constexpr (I < O::kLoads) {
+            o.template load_end<I>(at + to, s);
+            all<I + 1, O>(o, to, s);
+        }
+    }
+};
+
+// The same by way of registers, for operands off 16 bytes: two stages.
+template <typename T, typename P, typename Q, int PB, int QB, int THREADS>
+__device__ __forceinline__ void steps_by_registers(P& first, Q& second, char* lds, int steps, int p0, int q0,
+                                                   f32x16_t (&acc)[PB][QB])
+{
+    constexpr int kStage = P::kBytes + Q::kBytes;
+    uint4 pv[P::kLoads], qv[Q::kLoads];
+    auto fetch = [&](int s) {
+        first.template fetch<T>(pv, s);
+        second.template fetch<T>(qv, s);
+    };
+    auto put = [&](int s) {
+        put_chunks<THREADS>(lds + (s & 1) * kStage, pv);
+        put_chunks<THREADS>(lds + (s & 1) * kStage + P::kBytes, qv);
+    };
+    fetch(0);
+    put(0);
+    for (int s = 0; s < steps; ++s) {
+        __syncthreads();
+        const char* now = lds + (s & 1) * kStage;
+        if (s + 1 < steps) fetch(s + 1);
 #pragma unroll
-        for (int j = 0; j < QB; ++j) q[j] = Q::part(q_lds, q0, j, s);
+        for (int part = 0; part < 4; ++part) {
+            uint4 p[PB], q[QB];
 #pragma unroll
-        for (int i = 0; i < PB; ++i) p[i] = P::part(p_lds, p0, i, s);
+            for (int j = 0; j < QB; ++j) q[j] = Q::part(now + P::kBytes, q0, j, part);
 #pragma unroll
-        for (int i = 0; i < PB; ++i)
+            for (int i = 0; i < PB; ++i) p[i] = P::part(now, p0, i, part);
 #pragma unroll
-            for (int j = 0; j < QB; ++j) acc[i][j] = mma32(p[i], q[j], acc[i][j], static_cast<const T*>(nullptr));
+            for (int i = 0; i < PB; ++i)
+#pragma unroll
+                for (int j = 0; j < QB; ++j)
+                    acc[i][j] = mma32(p[i], q[j], acc[i][j], static_cast<const T*>(nullptr));
+        }
+        if (s + 1 < steps) put(s + 1);
     }
 }
 
@@ -356,8 +663,9 @@ __device__ __forceinline__ void multiply(const char* p_lds, const char* q_lds, i
 template <typename T>
 __device__ __forceinline__ uint2 pack4(float a, float b, float c, float d)
 {
-    const T q[4] = {from_float<T>(a), from_float<T>(b), from_float<T>(c), from_float<T>(d)};
-    return make_uint2(q[0].bits | (uint32_t)q[1].bits << 16, q[2].bits | (uint32_t)q[3].bits << 16);
+    typedef std::conditional_t<std::is_same_v<T, Bf16>, bf16x2_t, fp16x2_t> pair;
+    return make_uint2(__builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), pair)),
+                      __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{c, d}), pair)));
 }
 
 // A 32 x 32 block: this lane's output row `row` (at its column 0), columns
