@@ -1351,8 +1351,7 @@ static ep_status_t expert_backward(const void* grad_out, int dtype, int64_t ld_g
     ep::ExpertBackwardArgs a = {grad_out, ld_grad_out, false, x, ld_x, num_x_rows, src, weights,
                                 num_experts, out_features, in_features, offsets, counts, num_rows,
                                 grad_rows, ld_grad_rows, grad_weights, grad_weights_dtype == EP_FP32};
-    if (ep::expert_backward_max_blocks(a) > INT32_MAX ||
-        num_rows * ((out_features + 15) / 16) / 256 >= INT32_MAX)
+    if (gated && num_rows * ((out_features + 15) / 16) / 256 >= INT32_MAX)
         return fail(EP_UNSUPPORTED, "the gradients need more than 2^31 workgroups");
     if (gated) {
         a.grad = workspace;

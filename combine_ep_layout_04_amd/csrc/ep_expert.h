@@ -48,7 +48,6 @@ struct ExpertBackwardArgs {
     bool wide_w;            // grad_w in fp32, else in dtype
 };
 hipError_t launch_expert_backward(int dtype, const ExpertBackwardArgs& a, hipStream_t stream);
-int64_t expert_backward_max_blocks(const ExpertBackwardArgs& a);
 
 // Gradient of silu(gate) * up: out [num_rows, ld_out] holds both halves (n / 2
 // each) side by side, its columns past n cleared.

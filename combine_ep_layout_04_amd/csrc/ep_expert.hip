@@ -26,7 +26,8 @@ struct Product {
     int64_t ld_out;
     T* pre;
     int64_t ld_pre;
-    int col_tiles, group;
+    TileWalk walk;
+    bool turned;        // tiles begin at different steps of the reduction
 };
 
 // WP x WQ wavefronts, a ring of RING operand tiles.  DIRECT: rows and weights
@@ -41,81 +42,84 @@ void expert_kernel(Product<T> a)
     using Off = std::conditional_t<DIRECT, uint32_t, uint64_t>;
     using P = RowOperand<BP, kThreads, Off>;
     using Q = RowOperand<BQ, kThreads, Off>;
-    using S = Steps<T, P, Q, PB, QB, RING>;
-    __shared__ __attribute__((aligned(128))) char lds[S::kLds];
+    using R = Ring<T, P, Q, PB, QB, RING>;
+    __shared__ __attribute__((aligned(128))) char lds[DIRECT ? R::kLds : 2 * (P::kBytes + Q::kBytes)];
 
-    int item, tile;
-    place_of(a.group, a.col_tiles, item, tile);
-    const RowBlock rb = find_rows(a.seg, BQ, item);
-    if (rb.rows <= 0) return;
-    const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int p0 = wave / WQ * (PB * 32), q0 = wave % WQ * (QB * 32);
     const int half = a.n / 2;
-    const int n0 = tile * (GLU ? BP / 2 : BP);
-    const int bytes = a.k * 2;
 
-    P p;
-    Q q;
-    // offsets from the tile's first row (of the gate half)
-    const T* w = a.w + ((int64_t)rb.expert * a.n + n0) * a.k;
-    p.init(reinterpret_cast<const char*>(w), bytes, [&](int i) {
-        int n;
-        if constexpr (GLU) {
-            n = i / 64 * 32 + (i & 31);
-            n = (n0 + n < half ? n : half - 1 - n0) + (i & 32 ? half : 0);
-        } else {
-            n = n0 + i < a.n ? i : a.n - 1 - n0;
-        }
-        return (Off)n * (Off)bytes;
-    });
-    const T* x = a.src != nullptr ? a.x : a.x + rb.first * a.ld_x;
-    q.init(reinterpret_cast<const char*>(x), bytes, [&](int i) {
-        int r = i < rb.rows ? i : 0;
-        if (a.src != nullptr) {
-            r = a.src[rb.first + r];
-            if (r < 0 || r >= a.x_rows) r = 0;
-        }
-        return (Off)r * (Off)(a.ld_x * 2);
-    });
-
-    f32x16_t acc[PB][QB];
-#pragma unroll
-    for (int i = 0; i < PB; ++i)
-#pragma unroll
-        for (int j = 0; j < QB; ++j) acc[i][j] = f32x16_t{};
-    const int steps = (bytes + 127) / 128;
-    if constexpr (DIRECT) {
-        S run(p, q, lds, p0, q0, steps);
-        run.run(acc, bytes / 128);
-    } else {
-        steps_by_registers<T, P, Q, PB, QB, kThreads>(p, q, lds, steps, p0, q0, acc);
-    }
-
-#pragma unroll
-    for (int j = 0; j < QB; ++j) {
-        const int r = q0 + j * 32 + (lane & 31);
-        const bool live = r < rb.rows;
-        const int64_t row = rb.first + (live ? r : 0);
-        if constexpr (GLU) {
-#pragma unroll
-            for (int i = 0; i < PB; i += 2) {
-                const int64_t c = n0 + (p0 + i * 32) / 2;
-                f32x16_t f;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) f[e] = silu_of(acc[i][j][e]) * acc[i + 1][j][e];
-                store_block(f, a.out + row * a.ld_out, c, half, live);
-                if (a.pre != nullptr) {
-                    store_block(acc[i][j], a.pre + row * a.ld_pre, c, half, live);
-                    store_block(acc[i + 1][j], a.pre + row * a.ld_pre + half, c, half, live);
-                }
+    struct Tile {
+        RowBlock rb;
+        int n0;
+    };
+    int i = 0;
+    auto find = [&](Tile& t) {
+        int col;
+        if (!next_tile(a.walk, a.seg, BQ, i, t.rb, col)) return false;
+        t.n0 = col * (GLU ? BP / 2 : BP);
+        return true;
+    };
+    auto prepare = [&](Work<P, Q>& w, const Tile& t) {
+        const int bytes = a.k * 2, steps = (bytes + 127) / 128;
+        // offsets from the tile's first row (of the gate half)
+        const T* from = a.w + ((int64_t)t.rb.expert * a.n + t.n0) * a.k;
+        w.p.init(reinterpret_cast<const char*>(from), bytes, [&](int r) {
+            int n;
+            if constexpr (GLU) {
+                n = r / 64 * 32 + (r & 31);
+                n = (t.n0 + n < half ? n : half - 1 - t.n0) + (r & 32 ? half : 0);
+            } else {
+                n = t.n0 + r < a.n ? r : a.n - 1 - t.n0;
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < PB; ++i)
-                store_block(acc[i][j], a.out + row * a.ld_out, n0 + p0 + i * 32, a.n, live);
+            return (Off)n * (Off)bytes;
+        });
+        const T* x = a.src != nullptr ? a.x : a.x + t.rb.first * a.ld_x;
+        w.q.init(reinterpret_cast<const char*>(x), bytes, [&](int i) {
+            int r = i < t.rb.rows ? i : 0;
+            if (a.src != nullptr) {
+                r = a.src[t.rb.first + r];
+                if (r < 0 || r >= a.x_rows) r = 0;
+            }
+            return (Off)r * (Off)(a.ld_x * 2);
+        });
+        w.steps = steps > R::kFewestSteps ? steps : R::kFewestSteps;
+        w.whole = bytes / 128;
+        w.turn = 0;
+        if (a.turned && w.steps == steps) {
+            w.turn = (int)((unsigned)(t.n0 / 32 * 5 + t.rb.expert * 3) % (unsigned)steps);
+            if (w.whole < steps) w.whole = 0;
         }
-    }
+    };
+    auto store = [&](const f32x16_t (&acc)[PB][QB], const Tile& t) {
+        const int lane = opaque(threadIdx.x) & 63;
+#pragma unroll
+        for (int j = 0; j < QB; ++j) {
+            const int r = q0 + j * 32 + (lane & 31);
+            const bool live = r < t.rb.rows;
+            const int64_t row = t.rb.first + (live ? r : 0);
+            if constexpr (GLU) {
+#pragma unroll
+                for (int i = 0; i < PB; i += 2) {
+                    const int64_t c = t.n0 + (p0 + i * 32) / 2;
+                    f32x16_t f;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) f[e] = silu_of(acc[i][j][e]) * acc[i + 1][j][e];
+                    store_block(f, a.out + row * a.ld_out, c, half, live);
+                    if (a.pre != nullptr) {
+                        store_block(acc[i][j], a.pre + row * a.ld_pre, c, half, live);
+                        store_block(acc[i + 1][j], a.pre + row * a.ld_pre + half, c, half, live);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < PB; ++i)
+                    store_block(acc[i][j], a.out + row * a.ld_out, t.n0 + p0 + i * 32, a.n, live);
+            }
+        }
+    };
+
+    tiles<T, DIRECT, P, Q, PB, QB, RING, kThreads, Tile>(lds, p0, q0, find, prepare, store, (a.k + 63) / 64);
 }
 
 template <typename T, bool GLU, bool DIRECT, int BP, int BQ, int WP, int WQ, int RING>
@@ -123,13 +127,14 @@ hipError_t launch(const ExpertArgs& a, hipStream_t stream)
 {
     Product<T> p = {static_cast<const T*>(a.x), a.ld_x, a.x_rows, a.src, static_cast<const T*>(a.w), a.n, a.k,
                     {a.offsets, a.counts, a.num_experts, (int)a.num_rows},
-                    static_cast<T*>(a.out), a.ld_out, static_cast<T*>(a.pre), a.ld_pre, 0, 8};
+                    static_cast<T*>(a.out), a.ld_out, static_cast<T*>(a.pre), a.ld_pre, {}, BQ <= 128};
     constexpr int kCols = GLU ? BP / 2 : BP;
     const int n = GLU ? a.n / 2 : a.n;
-    p.col_tiles = (n + kCols - 1) / kCols;
-    const int64_t items = max_row_blocks(a.num_rows, a.num_experts, BQ);
+    p.walk.group = 8;
+    p.walk.col_tiles = (n + kCols - 1) / kCols;
+    p.walk.tiles = tile_count(max_row_blocks(a.num_rows, a.num_experts, BQ), p.walk.group, p.walk.col_tiles);
     hipLaunchKernelGGL((expert_kernel<T, GLU, DIRECT, BP, BQ, WP, WQ, RING>),
-                       dim3((unsigned)tile_grid(items, p.group, p.col_tiles)), dim3(WP * WQ * 64), 0, stream, p);
+                       dim3(tile_grid(p.walk.tiles, BQ <= 128 ? 2 : 1)), dim3(WP * WQ * 64), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -161,10 +166,9 @@ hipError_t launch_expert(int dtype, const ExpertArgs& a, hipStream_t stream)
 
 int64_t expert_max_blocks(const ExpertArgs& a)
 {
-    // the smallest tiles of ep_expert_few.hip, and the tiles above
-    const int64_t few = max_row_blocks(a.num_rows, a.num_experts, 16) * ((a.n + 31) / 32 + 1);
-    const int64_t tiles = tile_grid(max_row_blocks(a.num_rows, a.num_experts, 128), 8, (a.n + 127) / 128 + 1);
-    return few > tiles ? few : tiles;
+    // of ep_expert_few.hip's smallest tiles; the tiles above have as many
+    // workgroups as the chip holds
+    return max_row_blocks(a.num_rows, a.num_experts, 16) * ((a.n + 31) / 32 + 1);
 }
 
 }  // namespace ep

@@ -27,7 +27,8 @@ struct RowsGrad {
     Segments seg;
     T* out;
     int64_t ld_out;
-    int col_tiles, group;
+    TileWalk walk;
+    bool turned;        // tiles begin at different steps of the reduction
 };
 
 // A tile of BP columns (k) by BQ rows; the reduction goes along n.
@@ -40,50 +41,53 @@ void rows_grad_kernel(RowsGrad<T> a)
     using Off = std::conditional_t<DIRECT, uint32_t, uint64_t>;
     using P = ColOperand<BP, kThreads, false, Off>;
     using Q = RowOperand<BQ, kThreads, Off>;
-    using S = Steps<T, P, Q, PB, QB, RING>;
-    __shared__ __attribute__((aligned(128))) char lds[S::kLds];
+    using R = Ring<T, P, Q, PB, QB, RING>;
+    __shared__ __attribute__((aligned(128))) char lds[DIRECT ? R::kLds : 2 * (P::kBytes + Q::kBytes)];
 
-    int item, tile;
-    place_of(a.group, a.col_tiles, item, tile);
-    const RowBlock rb = find_rows(a.seg, BQ, item);
-    if (rb.rows <= 0) return;
-    const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int p0 = wave / WQ * (PB * 32), q0 = wave % WQ * (QB * 32);
-    const int64_t k0 = (int64_t)tile * BP;
 
-    // a chunk that ends past n reads what lies behind the row: the caller keeps
-    // zeros there (DIRECT)
-    const int bytes = DIRECT ? (a.n * 2 + 15) / 16 * 16 : a.n * 2;
-    P p;
-    Q q;
-    p.init(reinterpret_cast<const char*>(a.w + (int64_t)rb.expert * a.n * a.k), (int64_t)a.k * 2, a.n, k0, a.k);
-    q.init(reinterpret_cast<const char*>(a.grad + rb.first * a.ld_grad), bytes,
-           [&](int i) { return (Off)(i < rb.rows ? i : 0) * (Off)(a.ld_grad * 2); });
-
-    f32x16_t acc[PB][QB];
+    struct Tile {
+        RowBlock rb;
+        int64_t k0;
+    };
+    int i = 0;
+    auto find = [&](Tile& t) {
+        int col;
+        if (!next_tile(a.walk, a.seg, BQ, i, t.rb, col)) return false;
+        t.k0 = (int64_t)col * BP;
+        return true;
+    };
+    auto prepare = [&](Work<P, Q>& w, const Tile& t) {
+        const int steps = (a.n + 63) / 64;
+        w.p.init(reinterpret_cast<const char*>(a.w + (int64_t)t.rb.expert * a.n * a.k), (int64_t)a.k * 2, a.n, t.k0,
+                 a.k);
+        // DIRECT: a chunk that ends past n reads what lies behind the row,
+        // where the caller keeps zeros
+        w.q.init(reinterpret_cast<const char*>(a.grad + t.rb.first * a.ld_grad),
+                 DIRECT ? (a.n * 2 + 15) / 16 * 16 : a.n * 2,
+                 [&](int i) { return (Off)(i < t.rb.rows ? i : 0) * (Off)(a.ld_grad * 2); });
+        w.steps = steps > R::kFewestSteps ? steps : R::kFewestSteps;
+        w.whole = a.n / 64;
+        w.turn = 0;
+        if (a.turned && w.steps == steps) {
+            w.turn = (int)((unsigned)(t.k0 / 32 * 5 + t.rb.expert * 3) % (unsigned)steps);
+            if (w.whole < steps) w.whole = 0;
+        }
+    };
+    auto store = [&](const f32x16_t (&acc)[PB][QB], const Tile& t) {
+        const int lane = opaque(threadIdx.x) & 63;
 #pragma unroll
-    for (int i = 0; i < PB; ++i)
+        for (int j = 0; j < QB; ++j) {
+            const int r = q0 + j * 32 + (lane & 31);
+            const bool live = r < t.rb.rows;
+            const int64_t row = t.rb.first + (live ? r : 0);
 #pragma unroll
-        for (int j = 0; j < QB; ++j) acc[i][j] = f32x16_t{};
-
-    const int steps = (a.n + 63) / 64;
-    if constexpr (DIRECT) {
-        S run(p, q, lds, p0, q0, steps);
-        run.run(acc, a.n / 64);
-    } else {
-        steps_by_registers<T, P, Q, PB, QB, kThreads>(p, q, lds, steps, p0, q0, acc);
-    }
-
-#pragma unroll
-    for (int j = 0; j < QB; ++j) {
-        const int r = q0 + j * 32 + (lane & 31);
-        const bool live = r < rb.rows;
-        const int64_t row = rb.first + (live ? r : 0);
-#pragma unroll
-        for (int i = 0; i < PB; ++i)
-            store_block(acc[i][j], a.out + row * a.ld_out, k0 + p0 + i * 32, a.k, live);
-    }
+            for (int i = 0; i < PB; ++i)
+                store_block(acc[i][j], a.out + row * a.ld_out, t.k0 + p0 + i * 32, a.k, live);
+        }
+    };
+    tiles<T, DIRECT, P, Q, PB, QB, RING, kThreads, Tile>(lds, p0, q0, find, prepare, store, (a.n + 63) / 64);
 }
 
 template <typename T>
@@ -97,6 +101,7 @@ struct WeightGrad {
     Segments seg;
     void* out;
     int k_tiles, n_tiles;
+    int64_t tiles;
 };
 
 // A tile of BP columns (k) by BQ outputs (n) of one expert; the reduction
@@ -110,56 +115,60 @@ void weight_grad_kernel(WeightGrad<T> a)
     using Off = std::conditional_t<DIRECT, uint32_t, uint64_t>;
     using P = ColOperand<BP, kThreads, GATHER, Off>;
     using Q = ColOperand<BQ, kThreads, false, Off>;
-    using S = Steps<T, P, Q, PB, QB, RING>;
-    __shared__ __attribute__((aligned(128))) char lds[S::kLds];
+    using R = Ring<T, P, Q, PB, QB, RING>;
+    __shared__ __attribute__((aligned(128))) char lds[DIRECT ? R::kLds : 2 * (P::kBytes + Q::kBytes)];
 
-    const unsigned place = run_place(), tiles = (unsigned)a.k_tiles * (unsigned)a.n_tiles;
-    const int expert = (int)(place / tiles);
-    if (expert >= a.seg.num_experts) return;
-    const int tile_n = (int)(place % tiles / (unsigned)a.k_tiles), tile_k = (int)(place % tiles % (unsigned)a.k_tiles);
-    RowBlock rb = {expert, 0, a.seg.num_rows};
-    if (a.seg.offsets != nullptr) {
-        rb.first = a.seg.offsets[expert];
-        rb.rows = a.seg.counts != nullptr ? a.seg.counts[expert] : a.seg.offsets[expert + 1] - rb.first;
-        bound_rows(rb, a.seg.num_rows);
-        if (rb.rows < 0) rb.rows = 0;
-    }
-    const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int p0 = wave / WQ * (PB * 32), q0 = wave % WQ * (QB * 32);
-    const int64_t k0 = (int64_t)tile_k * BP, n0 = (int64_t)tile_n * BQ;
 
-    f32x16_t acc[PB][QB];
+    struct Tile {
+        RowBlock rb;
+        int64_t k0, n0;
+    };
+    int i = 0;
+    O* const out = static_cast<O*>(a.out);
+    auto store = [&](const f32x16_t (&acc)[PB][QB], const Tile& t) {
+        const int lane = opaque(threadIdx.x) & 63;
+        O* to = out + (int64_t)t.rb.expert * a.n * a.k;
 #pragma unroll
-    for (int i = 0; i < PB; ++i)
+        for (int j = 0; j < QB; ++j) {
+            const int64_t n = t.n0 + q0 + j * 32 + (lane & 31);
+            const bool live = n < a.n;
 #pragma unroll
-        for (int j = 0; j < QB; ++j) acc[i][j] = f32x16_t{};
-    if (rb.rows > 0) {
-        P p;
-        Q q;
-        if constexpr (GATHER)
-            p.init(reinterpret_cast<const char*>(a.x), a.ld_x * 2, rb.rows, k0, a.k, a.src + rb.first, a.x_rows);
-        else
-            p.init(reinterpret_cast<const char*>(a.x + rb.first * a.ld_x), a.ld_x * 2, rb.rows, k0, a.k);
-        q.init(reinterpret_cast<const char*>(a.grad + rb.first * a.ld_grad), a.ld_grad * 2, rb.rows, n0, a.n);
-        const int steps = (rb.rows + 63) / 64;
-        if constexpr (DIRECT) {
-            S run(p, q, lds, p0, q0, steps);
-            run.run(acc, rb.rows / 64);
-        } else {
-            steps_by_registers<T, P, Q, PB, QB, kThreads>(p, q, lds, steps, p0, q0, acc);
+            for (int i = 0; i < PB; ++i)
+                store_block(acc[i][j], to + (live ? n : 0) * a.k, t.k0 + p0 + i * 32, a.k, live);
         }
-    }
-
-    O* out = static_cast<O*>(a.out) + (int64_t)expert * a.n * a.k;
-#pragma unroll
-    for (int j = 0; j < QB; ++j) {
-        const int64_t n = n0 + q0 + j * 32 + (lane & 31);
-        const bool live = n < a.n;
-#pragma unroll
-        for (int i = 0; i < PB; ++i)
-            store_block(acc[i][j], out + (live ? n : 0) * a.k, k0 + p0 + i * 32, a.k, live);
-    }
+    };
+    auto find = [&](Tile& t) {
+        const int64_t at = tile_of(i++);
+        if (at >= a.tiles) return false;
+        const int64_t per = (int64_t)a.k_tiles * a.n_tiles;
+        const int expert = (int)(at / per);
+        const unsigned of = (unsigned)(at % per);
+        t.n0 = (int64_t)(of / (unsigned)a.k_tiles) * BQ;
+        t.k0 = (int64_t)(of % (unsigned)a.k_tiles) * BP;
+        t.rb = RowBlock{expert, 0, a.seg.num_rows};
+        if (a.seg.offsets != nullptr) {
+            t.rb.first = uniform(a.seg.offsets[expert]);
+            t.rb.rows = uniform(a.seg.counts != nullptr ? a.seg.counts[expert]
+                                                        : a.seg.offsets[expert + 1] - t.rb.first);
+            bound_rows(t.rb, a.seg.num_rows);
+        }
+        if (t.rb.rows <= 0) t.rb.rows = t.rb.first = 0;     // no rows: steps of zeros
+        return true;
+    };
+    auto prepare = [&](Work<P, Q>& w, const Tile& t) {
+        const int steps = (t.rb.rows + 63) / 64;
+        if constexpr (GATHER)
+            w.p.init(reinterpret_cast<const char*>(a.x), a.ld_x * 2, t.rb.rows, t.k0, a.k, a.src + t.rb.first, a.x_rows);
+        else
+            w.p.init(reinterpret_cast<const char*>(a.x + t.rb.first * a.ld_x), a.ld_x * 2, t.rb.rows, t.k0, a.k);
+        w.q.init(reinterpret_cast<const char*>(a.grad + t.rb.first * a.ld_grad), a.ld_grad * 2, t.rb.rows, t.n0, a.n);
+        w.steps = DIRECT && steps < R::kFewestSteps ? R::kFewestSteps : steps;
+        w.whole = t.rb.rows / 64;
+        w.turn = 0;
+    };
+    tiles<T, DIRECT, P, Q, PB, QB, RING, kThreads, Tile>(lds, p0, q0, find, prepare, store, 0);
 }
 
 // Both halves' gradients, a row's units of 8 outputs per thread.  Memory
@@ -211,10 +220,12 @@ hipError_t launch_rows(const ExpertBackwardArgs& a, hipStream_t stream)
 {
     RowsGrad<T> p = {static_cast<const T*>(a.grad), a.ld_grad, static_cast<const T*>(a.w), a.n, a.k,
                      {a.offsets, a.counts, a.num_experts, (int)a.num_rows},
-                     static_cast<T*>(a.grad_rows), a.ld_grad_rows, (a.k + BP - 1) / BP, 8};
-    const int64_t items = max_row_blocks(a.num_rows, a.num_experts, BQ);
+                     static_cast<T*>(a.grad_rows), a.ld_grad_rows, {}, BQ <= 128};
+    p.walk.group = 8;
+    p.walk.col_tiles = (a.k + BP - 1) / BP;
+    p.walk.tiles = tile_count(max_row_blocks(a.num_rows, a.num_experts, BQ), p.walk.group, p.walk.col_tiles);
     hipLaunchKernelGGL((rows_grad_kernel<T, DIRECT, BP, BQ, WP, WQ, RING>),
-                       dim3((unsigned)tile_grid(items, p.group, p.col_tiles)), dim3(WP * WQ * 64), 0, stream, p);
+                       dim3(tile_grid(p.walk.tiles, BQ <= 128 ? 2 : 1)), dim3(WP * WQ * 64), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -223,10 +234,10 @@ hipError_t launch_weights(const ExpertBackwardArgs& a, hipStream_t stream)
 {
     WeightGrad<T> p = {static_cast<const T*>(a.grad), a.ld_grad, static_cast<const T*>(a.x), a.ld_x, a.x_rows, a.src,
                        a.n, a.k, {a.offsets, a.counts, a.num_experts, (int)a.num_rows},
-                       a.grad_w, (a.k + BP - 1) / BP, (a.n + BQ - 1) / BQ};
+                       a.grad_w, (a.k + BP - 1) / BP, (a.n + BQ - 1) / BQ, 0};
+    p.tiles = (int64_t)a.num_experts * p.k_tiles * p.n_tiles;
     hipLaunchKernelGGL((weight_grad_kernel<T, O, DIRECT, GATHER, BP, BQ, WP, WQ, RING>),
-                       dim3((unsigned)tile_grid(a.num_experts, 1, p.k_tiles * p.n_tiles)), dim3(WP * WQ * 64), 0,
-                       stream, p);
+                       dim3(tile_grid(p.tiles, BQ <= 128 ? 2 : 1)), dim3(WP * WQ * 64), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -258,7 +269,7 @@ hipError_t backward(const ExpertBackwardArgs& a, hipStream_t stream)
         if (err != hipSuccess) return err;
     }
     if (a.grad_w == nullptr) return hipSuccess;
-    if (a.src != nullptr)
+    if (a.src != nullptr && a.num_rows > 0)
         return a.wide_w ? weights_sized<T, float, true>(a, stream) : weights_sized<T, T, true>(a, stream);
     return a.wide_w ? weights_sized<T, float, false>(a, stream) : weights_sized<T, T, false>(a, stream);
 }
@@ -268,14 +279,6 @@ hipError_t backward(const ExpertBackwardArgs& a, hipStream_t stream)
 hipError_t launch_expert_backward(int dtype, const ExpertBackwardArgs& a, hipStream_t stream)
 {
     return dtype == 0 ? backward<Bf16>(a, stream) : backward<Fp16>(a, stream);
-}
-
-int64_t expert_backward_max_blocks(const ExpertBackwardArgs& a)
-{
-    const int64_t rows = tile_grid(max_row_blocks(a.num_rows, a.num_experts, 128), 8, (a.k + 127) / 128);
-    const int64_t tiles = ((int64_t)a.k + 127) / 128 * ((a.n + 127) / 128);
-    const int64_t weights = tiles > INT32_MAX ? tiles : tile_grid(a.num_experts, 1, (int)tiles);
-    return rows > weights ? rows : weights;
 }
 
 hipError_t launch_glu_backward(int dtype, const GluBackwardArgs& a, hipStream_t stream)

@@ -83,6 +83,7 @@ struct Scaled {
     void* out;
     int64_t ld_out;
     int col_tiles, group;
+    int64_t tiles;
 };
 
 // A scale as it lies in memory, and its value: 2^(byte - 127).
@@ -129,10 +130,9 @@ void fp8_kernel(Scaled a)
     constexpr int kStage = P::kBytes + Q::kBytes;
     __shared__ __attribute__((aligned(128))) char lds[2 * kStage];
 
-    int item, tile;
-    place_of(a.group, a.col_tiles, item, tile);
-    const RowBlock rb = find_rows(a.seg, BQ, item);
-    if (rb.rows <= 0) return;
+    int i = 0, tile;
+    RowBlock rb;
+    if (!next_tile(TileWalk{a.tiles, a.col_tiles, a.group}, a.seg, BQ, i, rb, tile)) return;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int p0 = wave / WQ * (PB * 32), q0 = wave % WQ * (QB * 32);
@@ -403,7 +403,7 @@ Scaled scaled(const ExpertFp8Args& a)
     return Scaled{static_cast<const char*>(a.x), a.ld_x, a.x_rows, a.src, a.x_scales, a.scale_bytes,
                   a.scale_row, a.scale_block, static_cast<const char*>(a.w), a.w_scales, a.n, a.k,
                   (a.n + 127) / 128, (a.k + 127) / 128,
-                  {a.offsets, a.counts, a.num_experts, (int)a.num_rows}, a.out, a.ld_out, 0, 8};
+                  {a.offsets, a.counts, a.num_experts, (int)a.num_rows}, a.out, a.ld_out, 0, 8, 0};
 }
 
 template <typename T, int FORMAT, bool GLU, bool SPLIT, typename OFF, int BP, int BQ, int WP, int WQ>
@@ -412,9 +412,9 @@ hipError_t launch(const ExpertFp8Args& a, hipStream_t stream)
     Scaled p = scaled(a);
     constexpr int kCols = GLU ? BP / 2 : BP;
     p.col_tiles = ((GLU ? a.n / 2 : a.n) + kCols - 1) / kCols;
-    const int64_t items = max_row_blocks(a.num_rows, a.num_experts, BQ);
+    p.tiles = tile_count(max_row_blocks(a.num_rows, a.num_experts, BQ), p.group, p.col_tiles);
     hipLaunchKernelGGL((fp8_kernel<T, FORMAT, GLU, SPLIT, OFF, BP, BQ, WP, WQ>),
-                       dim3((unsigned)tile_grid(items, p.group, p.col_tiles)), dim3(WP * WQ * 64), 0, stream, p);
+                       dim3((unsigned)((p.tiles + 255) / 256 * 256)), dim3(WP * WQ * 64), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -464,7 +464,7 @@ hipError_t launch_expert_fp8(int dtype, const ExpertFp8Args& a, hipStream_t stre
 int64_t expert_fp8_max_blocks(const ExpertFp8Args& a)
 {
     const int64_t few = max_row_blocks(a.num_rows, a.num_experts, 16) * ((a.n + 31) / 32 + 1);
-    const int64_t tiles = tile_grid(max_row_blocks(a.num_rows, a.num_experts, 128), 8, (a.n + 127) / 128 + 1);
+    const int64_t tiles = tile_count(max_row_blocks(a.num_rows, a.num_experts, 128), 8, (a.n + 127) / 128 + 1);
     return few > tiles ? few : tiles;
 }
 

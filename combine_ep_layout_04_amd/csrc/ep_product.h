@@ -89,14 +89,17 @@ __device__ __forceinline__ void bound_rows(RowBlock& b, int num_rows)
 }
 
 // The item-th block of at most TM rows, in expert order, found by a whole
-// wavefront, 256 experts at a time; rows 0 past the last.
+// wavefront, 256 experts at a time.  Past the last one rows is 0, expert -1
+// and first the number of blocks.
 __device__ __forceinline__ RowBlock find_rows(const Segments& s, int TM, int item)
 {
     const int lane = threadIdx.x & 63;
-    RowBlock b = {0, 0, 0};
+    RowBlock b = {-1, 0, 0};
     if (s.offsets == nullptr) {
         const int64_t first = (int64_t)item * TM;
+        b.first = (s.num_rows + TM - 1) / TM;
         if (first >= s.num_rows) return b;
+        b.expert = 0;
         b.first = (int)first;
         b.rows = s.num_rows - b.first < TM ? s.num_rows - b.first : TM;
         return b;
@@ -144,7 +147,8 @@ __device__ __forceinline__ RowBlock find_rows(const Segments& s, int TM, int ite
         }
         done = __builtin_amdgcn_readlane(upto, 63);
     }
-    bound_rows(b, s.num_rows);
+    if (b.expert < 0) b.first = done;
+    else bound_rows(b, s.num_rows);
     return b;
 }
 
@@ -157,31 +161,73 @@ inline int64_t max_row_blocks(int64_t num_rows, int num_experts, int TM)
 
 // Workgroup b runs on XCD b % 8.  Each XCD takes runs of kRun tiles, which
 // its 32 CUs work on together: `group` row blocks by kRun / group column
-// tiles, so both operands are read into that XCD's L2 a few times only.
-constexpr int kRun = 32;
-inline int64_t tile_grid(int64_t items, int group, int col_tiles)
+// tiles, so both operands are read into that XCD's L2 a few times only.  A
+// workgroup takes its place in every run of its XCD in turn; two or more to a
+// CU take neighbouring runs.
+constexpr int kRun = 32, kXcds = 8;
+
+inline int64_t tile_count(int64_t items, int group, int col_tiles)
 {
-    const int64_t all = (items + group - 1) / group * group * col_tiles;
-    return (all + 8 * kRun - 1) / (8 * kRun) * (8 * kRun);
+    return (items + group - 1) / group * group * col_tiles;
 }
-__device__ __forceinline__ unsigned run_place()
+// Workgroups for so many tiles, `per_cu` to a CU.
+inline unsigned tile_grid(int64_t tiles, int per_cu)
 {
-    const unsigned j = blockIdx.x >> 3, xcd = blockIdx.x & 7;
-    return (j / kRun * 8 + xcd) * kRun + j % kRun;
+    const int64_t runs = (tiles + kRun - 1) / kRun, most = kXcds * per_cu;
+    return (unsigned)(((runs < most ? (runs + kXcds - 1) / kXcds * kXcds : most)) * kRun);
 }
-__device__ __forceinline__ void place_of(int group, int col_tiles, int& item, int& col)
+// The i-th tile of this workgroup.
+__device__ __forceinline__ int64_t tile_of(int i)
 {
-    const unsigned at = run_place();
-    const unsigned per = (unsigned)group * (unsigned)col_tiles;
-    const unsigned rest = at % per;
-    item = (int)(at / per * group + rest % group);
-    col = (int)(rest / group);
+    const unsigned xcd = blockIdx.x % kXcds, j = blockIdx.x / kXcds;
+    const unsigned runs = gridDim.x / (kXcds * kRun);       // of an XCD at a time
+    return (((int64_t)i * runs + j / kRun) * kXcds + xcd) * kRun + j % kRun;
+}
+
+// Row blocks and column tiles: the walk over the tiles of a call.
+struct TileWalk {
+    int64_t tiles;
+    int col_tiles, group;
+};
+// This workgroup's next tile with rows from its i-th on; false past the last.
+__device__ __forceinline__ bool next_tile(const TileWalk& t, const Segments& seg, int TM, int& i, RowBlock& rb,
+                                          int& col)
+{
+    for (;; ++i) {
+        const int64_t at = tile_of(i), per = (int64_t)t.group * t.col_tiles;
+        if (at >= t.tiles) return false;
+        const int64_t of = at / per * t.group;
+        const unsigned rest = (unsigned)(at % per);
+        rb = find_rows(seg, TM, (int)(of + rest % t.group));
+        if (rb.rows > 0) {
+            col = (int)(rest / t.group);
+            ++i;
+            return true;
+        }
+        if (rb.expert < 0 && of >= rb.first) return false;      // the whole group lies past the last block
+    }
 }
 
 // ---- operand tiles
 
+// v, whose origin the compiler does not see: what follows from it is computed
+// where it is used, and not kept in registers through the steps of a tile.
+__device__ __forceinline__ int opaque(int v)
+{
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 // What lanes read in place of chunks past the end.
 __device__ const uint4 kZeroChunk[1] = {{0u, 0u, 0u, 0u}};
+
+// A value that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ const char* uniform(const char* p)
+{
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    return reinterpret_cast<const char*>((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
+}
 
 // 16 bytes a lane from global memory to LDS, from base + off: lane l's go to
 // lds + AT + 16 l.  The compiler does not count these loads: wait_barrier()
@@ -191,7 +237,7 @@ __device__ __forceinline__ void load_lds(uint32_t lds, const char* base, uint32_
 {
     asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3"
                  :
-                 : "s"(lds), "n"(AT), "v"(off), "s"(base)
+                 : "s"(lds), "n"(AT), "v"(off), "s"(uniform(base))
                  : "m0", "scc");
 }
 // The same where some lanes have nothing to read: zeros for these.
@@ -251,8 +297,8 @@ struct RowOperand {
     template <typename F>
     __device__ __forceinline__ void init(const char* from, int length, F off_of)
     {
-        const int t = threadIdx.x;
-        base = from;
+        const int t = opaque(threadIdx.x);
+        base = uniform(from);
         bytes = length;
         chunk = (t & 7) ^ turn(t / 8);
 #pragma unroll
@@ -322,10 +368,10 @@ struct ColOperand {
     __device__ __forceinline__ void init(const char* from, int64_t stride, int count, int64_t first, int64_t cols,
                                          const int32_t* pick = nullptr, int64_t limit = 0)
     {
-        const int t = threadIdx.x, p = t % kChunks;
+        const int t = opaque(threadIdx.x), p = t % kChunks;
         row = t / kChunks;
         wave_row = __builtin_amdgcn_readfirstlane(row);
-        base = from;
+        base = uniform(from);
         ld = stride;
         rows = count;
         index = (scalar_ptr)pick;
@@ -357,7 +403,8 @@ struct ColOperand {
 #pragma unroll
             for (int i = 0; i < kLoads; ++i)
 #pragma unroll
-                for (int j = 0; j < kSide; ++j) asm volatile("" : "+s"(next[i][j]));
+                for (int j = 0; j < kSide; ++j)
+                    asm volatile("" ::"s"(__builtin_amdgcn_readfirstlane(next[i][j])));
         }
     }
     // The offset of this thread's i-th row of the coming step, from `base`;
@@ -427,12 +474,26 @@ __device__ __forceinline__ void put_chunks(char* lds, const uint4 (&v)[LOADS])
 
 // ---- the steps
 
-// A tile's steps: PB x QB blocks of 32 x 32 per wavefront over the reduction,
-// 128 bytes of it a step, from LDS.
+// A tile's operands and its length: steps of the reduction (at least
+// kFewestSteps: what is not there is zeros), and how many of them are known to
+// be whole.  The steps are taken from `turn` on, round.
+template <typename P, typename Q>
+struct Work {
+    P p;
+    Q q;
+    int steps, whole, turn;
+
+    __device__ __forceinline__ int step(int s) const { return s + turn < steps ? s + turn : s + turn - steps; }
+};
+
+// Tiles one after another: PB x QB blocks of 32 x 32 per wavefront over the
+// reduction, 128 bytes of it a step, from LDS.
 //
 // The two operands' tiles of a step take turns in a ring of RING places
 // (P of step 0, Q of 0, P of 1, ...; with 5 places of 32 KiB all of LDS): an
 // odd ring keeps more than a step in flight where LDS does not hold three.
+// The ring does not stop between tiles: the last steps of one send the loads
+// of the first steps of the next, which arrive while results are stored.
 //
 // Two sets of operands in registers: those of a part (16 elements of the
 // reduction, 32 bytes) are read while the part before it is multiplied.  The
@@ -443,7 +504,8 @@ __device__ __forceinline__ void put_chunks(char* lds, const uint4 (&v)[LOADS])
 // and the wavefront stands still before its matrix instructions.  Reads and
 // loads take their turns after matrix instructions, by hand.
 template <typename T, typename P, typename Q, int PB, int QB, int RING>
-struct Steps {
+struct Ring {
+    using W = Work<P, Q>;
     static constexpr int kPlace = P::kBytes > Q::kBytes ? P::kBytes : Q::kBytes;
     static constexpr int kMuls = PB * QB, kReads = PB + QB;
     static constexpr int kLds = kPlace * RING;
@@ -452,92 +514,72 @@ struct Steps {
     // loads that may be under way when a step changes: those of the tiles
     // behind the next step's
     static constexpr int kLeft = (RING - 4) / 2 * kLoads + (kOdd ? P::kLoads : 0);
+    static constexpr int kAhead = (RING + 1) / 2;   // steps to the last load that follows a step
+    static constexpr int kFewestSteps = kAhead;     // so that loads never reach past the next tile
     static_assert(RING >= 4, "two steps at least");
 
-    P& first;
-    Q& second;
     char* lds;
     uint32_t at;
-    int p0, q0, steps;
+    int p0, q0, now;        // now: the place of the step's P; Q's is behind it
     uint4 p[2][PB], q[2][QB];
 
-    __device__ __forceinline__ Steps(P& a, Q& b, char* shared, int p_row, int q_row, int num_steps)
-        : first(a), second(b), lds(shared), p0(p_row), q0(q_row), steps(num_steps)
+    __device__ __forceinline__ Ring(char* shared, int p_row, int q_row) : lds(shared), p0(p_row), q0(q_row), now(0)
     {
         at = lds_address(lds) + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) * 1024;
     }
 
     __device__ __forceinline__ static int place(int v) { return v >= RING * kPlace ? v - RING * kPlace : v; }
 
-    // The I-th load of those that go out from step s's last part on, into the
-    // places of step s: `now` (P) and behind it (Q).
-    template <int I, bool END>
-    __device__ __forceinline__ void load_one(int s, int now)
+    template <int I, typename O>
+    __device__ __forceinline__ static void load_near(O& mine, O& next, const W& w, const W& nw, uint32_t to, int s)
     {
-        if constexpr (kOdd) {
-            // Q's next tile falls on P's place and comes first
-            if constexpr (I < Q::kLoads) {
-                const int to = s + RING / 2;
-                if constexpr (END) {
-                    if (to < steps) second.template load_end<I>(at + now, to);
-                } else {
-                    second.template load<I>(at + now, to);
-                }
-            } else {
-                const int to = s + RING / 2 + 1;
-                if constexpr (END) {
-                    if (to < steps) first.template load_end<I - Q::kLoads>(at + place(now + kPlace), to);
-                } else {
-                    first.template load<I - Q::kLoads>(at + place(now + kPlace), to);
-                }
-            }
+        if (s < w.steps) mine.template load_end<I>(to, w.step(s));
+        else next.template load_end<I>(to, nw.step(s - w.steps));
+    }
+    // The I-th of the loads that follow step s, whose P lies at `here`.  KIND
+    // 1: of whole steps of this tile; 2: of steps that may be the last, or the
+    // next tile's.
+    template <int I, int KIND>
+    __device__ __forceinline__ void load_one(W& w, W& nw, int s, int here)
+    {
+        // in an odd ring Q's next tile falls on P's place and comes first
+        constexpr bool kIsQ = kOdd ? I < Q::kLoads : I >= P::kLoads;
+        constexpr int kOf = kOdd ? (kIsQ ? I : I - Q::kLoads) : (kIsQ ? I - P::kLoads : I);
+        constexpr int kSecond = kOdd ? !kIsQ : kIsQ;
+        const int to = s + RING / 2 + (kOdd && !kIsQ ? 1 : 0);
+        const uint32_t where = at + (kSecond ? place(here + kPlace) : here);
+        if constexpr (KIND == 1) {
+            if constexpr (kIsQ) w.q.template load<kOf>(where, w.step(to));
+            else w.p.template load<kOf>(where, w.step(to));
         } else {
-            const int to = s + RING / 2;
-            if constexpr (I < P::kLoads) {
-                if constexpr (END) {
-                    if (to < steps) first.template load_end<I>(at + now, to);
-                } else {
-                    first.template load<I>(at + now, to);
-                }
-            } else {
-                if constexpr (END) {
-                    if (to < steps) second.template load_end<I - P::kLoads>(at + place(now + kPlace), to);
-                } else {
-                    second.template load<I - P::kLoads>(at + place(now + kPlace), to);
-                }
-            }
+            if constexpr (kIsQ) load_near<kOf>(w.q, nw.q, w, nw, where, to);
+            else load_near<kOf>(w.p, nw.p, w, nw, where, to);
         }
     }
-    template <int I, int UPTO, bool END>
-    __device__ __forceinline__ void load_some(int s, int now)
+    template <int I, int UPTO, int KIND>
+    __device__ __forceinline__ void load_some(W& w, W& nw, int s, int here)
     {
         if constexpr (I < UPTO) {
-            load_one<I, END>(s, now);
-            load_some<I + 1, UPTO, END>(s, now);
+            load_one<I, KIND>(w, nw, s, here);
+            load_some<I + 1, UPTO, KIND>(w, nw, s, here);
         }
     }
-
-    template <int R>
-    __device__ __forceinline__ void read_one(int set, int now, int part)
-    {
-        if constexpr (R < QB) q[set][R] = Q::part(lds + place(now + kPlace), q0, R, part);
-        else p[set][R - QB] = P::part(lds + now, p0, R - QB, part);
-    }
     template <int R, int UPTO>
-    __device__ __forceinline__ void read_some(int set, int now, int part)
+    __device__ __forceinline__ void read_some(int set, int here, int part)
     {
         if constexpr (R < UPTO) {
-            read_one<R>(set, now, part);
-            read_some<R + 1, UPTO>(set, now, part);
+            if constexpr (R < QB) q[set][R] = Q::part(lds + place(here + kPlace), q0, R, part);
+            else p[set][R - QB] = P::part(lds + here, p0, R - QB, part);
+            read_some<R + 1, UPTO>(set, here, part);
         }
     }
 
     // Matrix instruction M of a part and what takes its turn after it: reads of
-    // part `next` of the step at `then` into the other set, and the SHARE-th
-    // quarter of the loads that follow step s at `now`.  LOADS: 0 none, 1 of
-    // full steps, 2 of steps that may be the last or behind it.
-    template <int SET, bool READ, int LOADS, int SHARE, int M = 0>
-    __device__ __forceinline__ void part(f32x16_t (&acc)[PB][QB], int then, int next, int s, int now)
+    // part `next` of the step at `there` into the other set, and the SHARE-th
+    // quarter of the loads that follow step s at `here`.
+    template <int SET, bool READ, int KIND, int SHARE, int M = 0>
+    __device__ __forceinline__ void part(f32x16_t (&acc)[PB][QB], W& w, W& nw, int there, int next, int s,
+                                         int here)
     {
         if constexpr (M < kMuls) {
             constexpr int i = M / QB, j = M % QB;
@@ -545,79 +587,88 @@ struct Steps {
             if constexpr (READ) {
                 // all reads within the first three quarters
                 constexpr int kFrom = kReads * M * 4 / (kMuls * 3), kTo = kReads * (M + 1) * 4 / (kMuls * 3);
-                read_some<(kFrom < kReads ? kFrom : kReads), (kTo < kReads ? kTo : kReads)>(SET ^ 1, then, next);
+                read_some<(kFrom < kReads ? kFrom : kReads), (kTo < kReads ? kTo : kReads)>(SET ^ 1, there, next);
             }
-            if constexpr (LOADS != 0) {
+            if constexpr (KIND != 0) {
                 constexpr int kOf = kLoads * SHARE / 4, kCount = kLoads * (SHARE + 1) / 4 - kOf;
-                load_some<kOf + kCount * M / kMuls, kOf + kCount * (M + 1) / kMuls, LOADS == 2>(s, now);
+                load_some<kOf + kCount * M / kMuls, kOf + kCount * (M + 1) / kMuls, KIND>(w, nw, s, here);
             }
             __builtin_amdgcn_sched_barrier(0);
-            part<SET, READ, LOADS, SHARE, M + 1>(acc, then, next, s, now);
+            part<SET, READ, KIND, SHARE, M + 1>(acc, w, nw, there, next, s, here);
         }
     }
 
-    // Step s, whose P lies at `now`.  REST, MORE: the loads that go out in its
-    // first three parts and its last (as LOADS of part()); LEFT: loads that may
-    // be under way when it changes; NEXT: another step follows.
-    template <int REST, int MORE, int LEFT, bool NEXT>
-    __device__ __forceinline__ void step(f32x16_t (&acc)[PB][QB], int s, int now)
+    template <int KIND>
+    __device__ __forceinline__ void step(f32x16_t (&acc)[PB][QB], W& w, W& nw, int s)
     {
         const int before = now - 2 * kPlace < 0 ? now + (RING - 2) * kPlace : now - 2 * kPlace;
         const int then = place(now + 2 * kPlace);
-        part<0, true, REST, 1>(acc, now, 1, s - 1, before);
-        part<1, true, REST, 2>(acc, now, 2, s - 1, before);
-        part<0, true, REST, 3>(acc, now, 3, s - 1, before);
-        if constexpr (NEXT) wait_barrier<LEFT>();
-        if constexpr (MORE != 0) {
-            first.found();
-            second.found();
-        }
-        part<1, NEXT, MORE, 0>(acc, then, 0, s, now);
+        part<0, true, KIND, 1>(acc, w, nw, now, 1, s - 1, before);
+        part<1, true, KIND, 2>(acc, w, nw, now, 2, s - 1, before);
+        part<0, true, KIND, 3>(acc, w, nw, now, 3, s - 1, before);
+        wait_barrier<kLeft>();
+        w.p.found();
+        if constexpr (KIND == 2) nw.p.found();
+        part<1, true, KIND, 0>(acc, w, nw, then, 0, s, now);
+        now = then;
     }
 
-    // full: steps that are whole (all, or all but the last).
-    __device__ __forceinline__ void run(f32x16_t (&acc)[PB][QB], int full)
+    // The first tile's first loads: what the steps before it would have sent.
+    __device__ __forceinline__ void begin(W& w)
     {
-        constexpr int kLast = (RING - 1) / 2;       // the last tile in the ring belongs to this step from now
-        constexpr int kAhead = (RING + 1) / 2;      // the last load that follows a step to this one
-        start<0>();
-        if (steps > kLast) wait_barrier<(RING - 2) / 2 * kLoads + (kOdd ? P::kLoads : 0)>();
-        else wait_barrier();
-        read_some<0, kReads>(0, 0, 0);
-        int s = 0, now = 0;
-        auto turn = [&] {
-            ++s;
-            now = place(now + 2 * kPlace);
-        };
-        if (steps > kLast) {
-            step<0, 2, kLeft, true>(acc, s, now);
-            turn();
-            for (; s + kAhead < full; turn()) step<1, 1, kLeft, true>(acc, s, now);
-            for (; s + kLast < steps; turn()) step<2, 2, kLeft, true>(acc, s, now);
-        }
-        for (; s + 1 < steps; turn()) step<2, 2, 0, true>(acc, s, now);
-        step<0, 0, 0, false>(acc, s, now);
+        start<0>(w);
+        load_some<0, kLoads / 4, 2>(w, w, -1, place(now + (RING - 2) * kPlace));
+        wait_barrier<kLeft + kLoads / 4>();
+        read_some<0, kReads>(0, now, 0);
     }
     template <int U>
-    __device__ __forceinline__ void start()
+    __device__ __forceinline__ void start(W& w)
     {
-        if constexpr (U < RING) {
-            if (U / 2 < steps) {
-                if constexpr (U % 2 == 0) all<0, P>(first, U * kPlace, U / 2);
-                else all<0, Q>(second, U * kPlace, U / 2);
-            }
-            start<U + 1>();
+        if constexpr (U < RING - 2) {
+            if constexpr (U % 2 == 0) all<0>(w.p, at + U * kPlace, w.step(U / 2));
+            else all<0>(w.q, at + U * kPlace, w.step(U / 2));
+            start<U + 1>(w);
         }
     }
     template <int I, typename O>
-    __device__ __forceinline__ void all(O& o, int to, int s)
+    __device__ __forceinline__ void all(O& o, uint32_t to, int s)
     {
         if constexpr (I < O::kLoads) {
-            o.template load_end<I>(at + to, s);
-            all<I + 1, O>(o, to, s);
+            o.template load_end<I>(to, s);
+            all<I + 1>(o, to, s);
         }
     }
+
+    // A whole tile, and the first loads of the next, which prepare(nw) finds
+    // when they come near (so that it takes no registers before).
+    template <typename Prepare>
+    __device__ __forceinline__ void tile(f32x16_t (&acc)[PB][QB], W& w, W& nw, Prepare prepare)
+    {
+        int s = 0;
+        for (; s + kAhead < w.whole; ++s) step<1>(acc, w, w, s);
+        prepare(nw);
+        for (; s < w.steps; ++s) step<2>(acc, w, nw, s);
+    }
 };
+
+// Keeps sums in the accumulation registers here: between tiles too, so that
+// results are fetched from there one block at a time.
+template <int PB, int QB>
+__device__ __forceinline__ void hold(f32x16_t (&acc)[PB][QB])
+{
+#pragma unroll
+    for (int i = 0; i < PB; ++i)
+#pragma unroll
+        for (int j = 0; j < QB; ++j) asm volatile("" : "+a"(acc[i][j]));
+}
+template <int PB, int QB>
+__device__ __forceinline__ void clear(f32x16_t (&acc)[PB][QB])
+{
+#pragma unroll
+    for (int i = 0; i < PB; ++i)
+#pragma unroll
+        for (int j = 0; j < QB; ++j) acc[i][j] = f32x16_t{};
+}
 
 // The same by way of registers, for operands off 16 bytes: two stages.
 template <typename T, typename P, typename Q, int PB, int QB, int THREADS>
@@ -657,6 +708,55 @@ __device__ __forceinline__ void steps_by_registers(P& first, Q& second, char* ld
     }
 }
 
+// The tiles of a workgroup.  find(t): the next one; prepare(work, t): its
+// operands; store(acc, t).  By way of registers `steps` is their length, or 0:
+// the work's.
+template <typename T, bool DIRECT, typename P, typename Q, int PB, int QB, int RING, int THREADS, typename Tile,
+          typename Find, typename Prepare, typename Store>
+__device__ __forceinline__ void tiles(char* lds, int p0, int q0, Find find, Prepare prepare, Store store, int steps)
+{
+    Tile t;
+    if (!find(t)) return;
+    f32x16_t acc[PB][QB];
+    if constexpr (DIRECT) {
+        Tile nt;
+        Work<P, Q> w, nw;
+        Ring<T, P, Q, PB, QB, RING> ring(lds, p0, q0);
+        prepare(w, t);
+        ring.begin(w);
+        bool more = true;
+        clear(acc);
+        for (;;) {
+            // behind the last tile its own first steps are loaded again, and
+            // waited for, so that every tile runs the same code
+            ring.tile(acc, w, nw, [&](Work<P, Q>& next) {
+                nt = t;
+                Tile found;
+                more = find(found);
+                if (more) nt = found;
+                prepare(next, nt);
+            });
+            hold(acc);
+            store(acc, t);
+            if (!more) break;
+            clear(acc);
+            hold(acc);
+            w = nw;
+            t = nt;
+        }
+        wait_barrier();
+    } else {
+        do {
+            Work<P, Q> w;
+            prepare(w, t);
+            clear(acc);
+            steps_by_registers<T, P, Q, PB, QB, THREADS>(w.p, w.q, lds, steps > 0 ? steps : w.steps, p0, q0, acc);
+            store(acc, t);
+            __syncthreads();
+        } while (find(t));
+    }
+}
+
 // ---- results
 
 // Two packed pairs of 16-bit results.
@@ -675,7 +775,7 @@ __device__ __forceinline__ uint2 pack4(float a, float b, float c, float d)
 template <typename T>
 __device__ __forceinline__ void store_block(const f32x16_t& v, T* row, int64_t col, int64_t cols, bool live)
 {
-    const int h = (threadIdx.x >> 5) & 1;
+    const int h = (opaque(threadIdx.x) >> 5) & 1;
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
         const uint2 a = pack4<T>(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
@@ -684,35 +784,36 @@ __device__ __forceinline__ void store_block(const f32x16_t& v, T* row, int64_t c
         const auto y = __builtin_amdgcn_permlane32_swap(a.y, b.y, false, false);
         const uint4 q = make_uint4(x[0], y[0], x[1], y[1]);
         const int64_t c = col + 8 * i + 8 * h;
-        if (live) {
-            if (c + 8 <= cols) {
-                __builtin_memcpy(row + c, &q, 16);
-            } else {
-                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (c + k < cols) row[c + k] = T{(uint16_t)(w[k / 2] >> (16 * (k & 1)))};
+        if (live && c + 8 <= cols) {
+            __builtin_memcpy(row + c, &q, 16);
+        } else if (live && c < cols) {
+            uint64_t lo = q.x | (uint64_t)q.y << 32, hi = q.z | (uint64_t)q.w << 32;
+#pragma clang loop unroll(disable)
+            for (int64_t k = c; k < cols; ++k) {
+                row[k] = T{(uint16_t)lo};
+                lo = lo >> 16 | hi << 48;
+                hi >>= 16;
             }
         }
     }
+    __builtin_amdgcn_sched_barrier(0);      // one block's values at a time
 }
 __device__ __forceinline__ void store_block(const f32x16_t& v, float* row, int64_t col, int64_t cols, bool live)
 {
-    const int h = (threadIdx.x >> 5) & 1;
+    const int h = (opaque(threadIdx.x) >> 5) & 1;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int64_t c = col + 8 * i + 4 * h;
-        if (live) {
+        if (live && c + 4 <= cols) {
             const f32x4_t q = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
-            if (c + 4 <= cols) {
-                __builtin_memcpy(row + c, &q, 16);
-            } else {
+            __builtin_memcpy(row + c, &q, 16);
+        } else if (live) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (c + k < cols) row[c + k] = q[k];
-            }
+            for (int k = 0; k < 3; ++k)
+                if (c + k < cols) row[c + k] = v[4 * i + k];
         }
     }
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 }  // namespace ep
