@@ -1290,15 +1290,24 @@ ep_status_t ep_expert_glu(const void* x, int dtype, int64_t ld_x, int64_t num_x_
                           stream, "ep_expert_glu launch");
 }
 
-// Row stride of the gated backward's workspace: whole 16-byte vectors.
-static int64_t glu_workspace_ld(int out_features) { return ((int64_t)out_features + 7) / 8 * 8; }
+// Row stride of rows in the backward's workspace: whole 16-byte vectors.
+static int64_t expert_workspace_ld(int features) { return ((int64_t)features + 7) / 8 * 8; }
 
-size_t ep_expert_glu_backward_workspace_size(int64_t num_rows, int out_features)
+// The workspace holds the gradient of the product's outputs where it is made
+// (gated) or laid out, and behind it the rows of x where these are laid out.
+static bool lays_out_grad(int out_features, bool gated) { return gated || out_features % 8 != 0; }
+static bool lays_out_x(int in_features, bool gathered) { return gathered || in_features % 8 != 0; }
+
+size_t ep_expert_backward_workspace_size(int64_t num_rows, int out_features, int in_features, int gated,
+                                         int gathered)
 {
-    if (num_rows < 0 || num_rows >= ((int64_t)1 << 31) || out_features < 2 ||
-        out_features > EP_MAX_OUT_FEATURES || out_features % 2 != 0)
+    if (num_rows < 0 || num_rows >= ((int64_t)1 << 31) || out_features < 1 ||
+        out_features > EP_MAX_OUT_FEATURES || (gated && out_features % 2 != 0) || in_features < 1 ||
+        in_features > EP_MAX_HIDDEN)
         return 0;
-    return (size_t)num_rows * (size_t)glu_workspace_ld(out_features) * 2;
+    const size_t grad = lays_out_grad(out_features, gated != 0) ? (size_t)expert_workspace_ld(out_features) : 0;
+    const size_t x = lays_out_x(in_features, gathered != 0) ? (size_t)expert_workspace_ld(in_features) : 0;
+    return (size_t)num_rows * (grad + x) * 2;
 }
 
 static ep_status_t expert_backward(const void* grad_out, int dtype, int64_t ld_grad_out,
@@ -1341,21 +1350,30 @@ static ep_status_t expert_backward(const void* grad_out, int dtype, int64_t ld_g
         if (gated) {
             st = check_matrix(pre, ld_pre, out_features, dtype, "pre");
             if (st) return st;
-            const size_t need = ep_expert_glu_backward_workspace_size(num_rows, out_features);
-            if (!workspace || !aligned16(workspace) || workspace_bytes < need)
-                return fail(EP_INVALID_ARGUMENT,
-                            "workspace must be 16-byte aligned and hold %zu bytes, holds %zu", need,
-                            workspace ? workspace_bytes : (size_t)0);
         }
+        const size_t need = ep_expert_backward_workspace_size(num_rows, out_features, in_features, gated,
+                                                              src != nullptr);
+        if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need))
+            return fail(EP_INVALID_ARGUMENT,
+                        "workspace must be 16-byte aligned and hold %zu bytes, holds %zu", need,
+                        workspace ? workspace_bytes : (size_t)0);
     }
-    ep::ExpertBackwardArgs a = {grad_out, ld_grad_out, false, x, ld_x, num_x_rows, src, weights,
+    ep::ExpertBackwardArgs a = {grad_out, ld_grad_out, false, x, ld_x, num_x_rows, src, false, weights,
                                 num_experts, out_features, in_features, offsets, counts, num_rows,
-                                grad_rows, ld_grad_rows, grad_weights, grad_weights_dtype == EP_FP32};
-    if (gated && num_rows * ((out_features + 15) / 16) / 256 >= INT32_MAX)
+                                grad_rows, ld_grad_rows, grad_weights, grad_weights_dtype == EP_FP32,
+                                nullptr, nullptr};
+    char* const work = static_cast<char*>(workspace);
+    const bool grad_there = lays_out_grad(out_features, gated);
+    if (num_rows > 0 && grad_there && !gated) a.grad_copy = work;
+    if (num_rows > 0 && lays_out_x(in_features, src != nullptr))
+        a.x_copy = work + (grad_there ? num_rows * expert_workspace_ld(out_features) * 2 : 0);
+    // workgroups of 256 threads with a 16-byte vector each
+    if (num_rows * (expert_workspace_ld(out_features > in_features ? out_features : in_features) / 8) / 256 >=
+        INT32_MAX)
         return fail(EP_UNSUPPORTED, "the gradients need more than 2^31 workgroups");
     if (gated) {
         a.grad = workspace;
-        a.ld_grad = glu_workspace_ld(out_features);
+        a.ld_grad = expert_workspace_ld(out_features);
         a.padded = true;
         const ep::GluBackwardArgs g = {grad_out, ld_grad_out, pre, ld_pre, num_rows, out_features,
                                        workspace, a.ld_grad};
@@ -1371,12 +1389,13 @@ ep_status_t ep_expert_matmul_backward(const void* grad_out, int dtype, int64_t l
                                       int out_features, int in_features, const int32_t* offsets,
                                       const int32_t* counts, int64_t num_rows, void* grad_rows,
                                       int64_t ld_grad_rows, void* grad_weights,
-                                      int grad_weights_dtype, void* stream)
+                                      int grad_weights_dtype, void* workspace, size_t workspace_bytes,
+                                      void* stream)
 {
     return expert_backward(grad_out, dtype, ld_grad_out, nullptr, 0, x, ld_x, num_x_rows, src, weights,
                            num_experts, out_features, in_features, false, offsets, counts, num_rows,
-                           grad_rows, ld_grad_rows, grad_weights, grad_weights_dtype, nullptr, 0, stream,
-                           "ep_expert_matmul_backward launch");
+                           grad_rows, ld_grad_rows, grad_weights, grad_weights_dtype, workspace,
+                           workspace_bytes, stream, "ep_expert_matmul_backward launch");
 }
 
 ep_status_t ep_expert_glu_backward(const void* grad_out, int dtype, int64_t ld_grad_out,

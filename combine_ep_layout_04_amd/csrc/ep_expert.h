@@ -37,6 +37,7 @@ struct ExpertBackwardArgs {
     const void* x;
     int64_t ld_x, x_rows;
     const int32_t* src;
+    bool x_padded;          // x's rows are
     const void* w;
     int num_experts, n, k;
     const int32_t* offsets;
@@ -46,6 +47,10 @@ struct ExpertBackwardArgs {
     int64_t ld_grad_rows;
     void* grad_w;           // [num_experts, n, k] or NULL
     bool wide_w;            // grad_w in fp32, else in dtype
+    // where to lay rows out first, padded to 8 columns with zeros, or NULL;
+    // with src x has to be
+    void* grad_copy;
+    void* x_copy;
 };
 hipError_t launch_expert_backward(int dtype, const ExpertBackwardArgs& a, hipStream_t stream);
 

@@ -39,7 +39,7 @@ void rows_grad_kernel(RowsGrad<T> a)
     constexpr int kThreads = WP * WQ * 64;
     constexpr int PB = BP / WP / 32, QB = BQ / WQ / 32;
     using Off = std::conditional_t<DIRECT, uint32_t, uint64_t>;
-    using P = ColOperand<BP, kThreads, false, Off>;
+    using P = ColOperand<BP, kThreads, Off>;
     using Q = RowOperand<BQ, kThreads, Off>;
     using R = Ring<T, P, Q, PB, QB, RING>;
     __shared__ __attribute__((aligned(128))) char lds[DIRECT ? R::kLds : 2 * (P::kBytes + Q::kBytes)];
@@ -95,8 +95,7 @@ struct WeightGrad {
     const T* grad;
     int64_t ld_grad;
     const T* x;
-    int64_t ld_x, x_rows;
-    const int32_t* src;
+    int64_t ld_x;
     int n, k;
     Segments seg;
     void* out;
@@ -106,15 +105,15 @@ struct WeightGrad {
 
 // A tile of BP columns (k) by BQ outputs (n) of one expert; the reduction
 // goes over its rows.  Experts without rows get zeros.
-template <typename T, typename O, bool DIRECT, bool GATHER, int BP, int BQ, int WP, int WQ, int RING>
+template <typename T, typename O, bool DIRECT, int BP, int BQ, int WP, int WQ, int RING>
 __global__ __launch_bounds__(WP * WQ * 64)
 void weight_grad_kernel(WeightGrad<T> a)
 {
     constexpr int kThreads = WP * WQ * 64;
     constexpr int PB = BP / WP / 32, QB = BQ / WQ / 32;
     using Off = std::conditional_t<DIRECT, uint32_t, uint64_t>;
-    using P = ColOperand<BP, kThreads, GATHER, Off>;
-    using Q = ColOperand<BQ, kThreads, false, Off>;
+    using P = ColOperand<BP, kThreads, Off>;
+    using Q = ColOperand<BQ, kThreads, Off>;
     using R = Ring<T, P, Q, PB, QB, RING>;
     __shared__ __attribute__((aligned(128))) char lds[DIRECT ? R::kLds : 2 * (P::kBytes + Q::kBytes)];
 
@@ -159,10 +158,7 @@ void weight_grad_kernel(WeightGrad<T> a)
     };
     auto prepare = [&](Work<P, Q>& w, const Tile& t) {
         const int steps = (t.rb.rows + 63) / 64;
-        if constexpr (GATHER)
-            w.p.init(reinterpret_cast<const char*>(a.x), a.ld_x * 2, t.rb.rows, t.k0, a.k, a.src + t.rb.first, a.x_rows);
-        else
-            w.p.init(reinterpret_cast<const char*>(a.x + t.rb.first * a.ld_x), a.ld_x * 2, t.rb.rows, t.k0, a.k);
+        w.p.init(reinterpret_cast<const char*>(a.x + t.rb.first * a.ld_x), a.ld_x * 2, t.rb.rows, t.k0, a.k);
         w.q.init(reinterpret_cast<const char*>(a.grad + t.rb.first * a.ld_grad), a.ld_grad * 2, t.rb.rows, t.n0, a.n);
         w.steps = DIRECT && steps < R::kFewestSteps ? R::kFewestSteps : steps;
         w.whole = t.rb.rows / 64;
@@ -229,14 +225,14 @@ hipError_t launch_rows(const ExpertBackwardArgs& a, hipStream_t stream)
     return hipGetLastError();
 }
 
-template <typename T, typename O, bool DIRECT, bool GATHER, int BP, int BQ, int WP, int WQ, int RING>
+template <typename T, typename O, bool DIRECT, int BP, int BQ, int WP, int WQ, int RING>
 hipError_t launch_weights(const ExpertBackwardArgs& a, hipStream_t stream)
 {
-    WeightGrad<T> p = {static_cast<const T*>(a.grad), a.ld_grad, static_cast<const T*>(a.x), a.ld_x, a.x_rows, a.src,
+    WeightGrad<T> p = {static_cast<const T*>(a.grad), a.ld_grad, static_cast<const T*>(a.x), a.ld_x,
                        a.n, a.k, {a.offsets, a.counts, a.num_experts, (int)a.num_rows},
                        a.grad_w, (a.k + BP - 1) / BP, (a.n + BQ - 1) / BQ, 0};
     p.tiles = (int64_t)a.num_experts * p.k_tiles * p.n_tiles;
-    hipLaunchKernelGGL((weight_grad_kernel<T, O, DIRECT, GATHER, BP, BQ, WP, WQ, RING>),
+    hipLaunchKernelGGL((weight_grad_kernel<T, O, DIRECT, BP, BQ, WP, WQ, RING>),
                        dim3(tile_grid(p.tiles, BQ <= 128 ? 2 : 1)), dim3(WP * WQ * 64), 0, stream, p);
     return hipGetLastError();
 }
@@ -245,20 +241,62 @@ hipError_t launch_weights(const ExpertBackwardArgs& a, hipStream_t stream)
 bool in_reach(int64_t elements) { return elements <= (int64_t)1 << 31; }
 bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
 
-template <typename T, typename O, bool GATHER>
-hipError_t weights_sized(const ExpertBackwardArgs& a, hipStream_t stream)
+// Rows laid out for the kernels above: gathered, and padded with zeros to
+// whole 16-byte chunks.  A chunk per thread.
+template <typename T>
+__global__ __launch_bounds__(256)
+void lay_out_kernel(const T* __restrict__ x, int64_t ld_x, int64_t x_rows, const int32_t* __restrict__ src,
+                    int64_t num_rows, int cols, int chunks, uint4* __restrict__ out)
 {
-    const bool direct = a.k % 8 == 0 && a.ld_x % 8 == 0 && (a.n % 8 == 0 || a.padded) && a.ld_grad % 8 == 0 &&
-                        in_reach((GATHER ? a.x_rows : 64) * a.ld_x) && in_reach(64 * a.ld_grad) && !off16(a.x) &&
-                        !off16(a.grad);
-    if (!direct) return launch_weights<T, O, false, GATHER, 128, 128, 2, 2, 4>(a, stream);
-    if (a.num_rows / a.num_experts >= 192) return launch_weights<T, O, true, GATHER, 256, 256, 2, 2, 5>(a, stream);
-    return launch_weights<T, O, true, GATHER, 128, 128, 2, 2, 5>(a, stream);
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    int64_t row = at / chunks;
+    if (row >= num_rows) return;
+    const int c = (int)(at % chunks) * 8;
+    if (src != nullptr) {
+        row = src[row];
+        if (row < 0 || row >= x_rows) row = 0;
+    }
+    out[at] = fetch16<T>(reinterpret_cast<const char*>(x + row * ld_x + c), cols - c);
 }
 
 template <typename T>
-hipError_t backward(const ExpertBackwardArgs& a, hipStream_t stream)
+hipError_t lay_out(const void* x, int64_t ld_x, int64_t x_rows, const int32_t* src, int64_t num_rows, int cols,
+                   void* out, hipStream_t stream)
 {
+    const int chunks = (cols + 7) / 8;
+    hipLaunchKernelGGL(lay_out_kernel<T>, dim3((unsigned)((num_rows * chunks + 255) / 256)), dim3(256), 0, stream,
+                       static_cast<const T*>(x), ld_x, x_rows, src, num_rows, cols, chunks, static_cast<uint4*>(out));
+    return hipGetLastError();
+}
+
+template <typename T, typename O>
+hipError_t weights_sized(const ExpertBackwardArgs& a, hipStream_t stream)
+{
+    const bool direct = (a.k % 8 == 0 || a.x_padded) && a.ld_x % 8 == 0 && (a.n % 8 == 0 || a.padded) &&
+                        a.ld_grad % 8 == 0 && in_reach(64 * a.ld_x) && in_reach(64 * a.ld_grad) && !off16(a.x) &&
+                        !off16(a.grad);
+    if (!direct) return launch_weights<T, O, false, 128, 128, 2, 2, 4>(a, stream);
+    if (a.num_rows / a.num_experts >= 192) return launch_weights<T, O, true, 256, 256, 2, 2, 5>(a, stream);
+    return launch_weights<T, O, true, 128, 128, 2, 2, 5>(a, stream);
+}
+
+template <typename T>
+hipError_t backward(ExpertBackwardArgs a, hipStream_t stream)
+{
+    if (a.grad_copy != nullptr) {
+        const hipError_t err = lay_out<T>(a.grad, a.ld_grad, a.num_rows, nullptr, a.num_rows, a.n, a.grad_copy, stream);
+        if (err != hipSuccess) return err;
+        a.grad = a.grad_copy;
+        a.ld_grad = (a.n + 7) / 8 * 8;
+        a.padded = true;
+    }
+    if (a.x_copy != nullptr && a.grad_w != nullptr) {
+        const hipError_t err = lay_out<T>(a.x, a.ld_x, a.x_rows, a.src, a.num_rows, a.k, a.x_copy, stream);
+        if (err != hipSuccess) return err;
+        a.x = a.x_copy;
+        a.ld_x = (a.k + 7) / 8 * 8;
+        a.x_padded = true;
+    }
     if (a.grad_rows != nullptr && a.num_rows > 0) {
         const bool direct = a.k % 8 == 0 && (a.n % 8 == 0 || a.padded) && a.ld_grad % 8 == 0 &&
                             in_reach(256 * a.ld_grad) && !off16(a.w) && !off16(a.grad);
@@ -269,9 +307,7 @@ hipError_t backward(const ExpertBackwardArgs& a, hipStream_t stream)
         if (err != hipSuccess) return err;
     }
     if (a.grad_w == nullptr) return hipSuccess;
-    if (a.src != nullptr && a.num_rows > 0)
-        return a.wide_w ? weights_sized<T, float, true>(a, stream) : weights_sized<T, T, true>(a, stream);
-    return a.wide_w ? weights_sized<T, float, false>(a, stream) : weights_sized<T, T, false>(a, stream);
+    return a.wide_w ? weights_sized<T, float>(a, stream) : weights_sized<T, T>(a, stream);
 }
 
 }  // namespace

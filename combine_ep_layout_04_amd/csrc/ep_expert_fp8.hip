@@ -43,30 +43,37 @@ __device__ __forceinline__ f32x16_t mma32x8(const Codes& a, const Codes& b, f32x
 }
 // Eight codes as bf16 (every one is a bf16 value).
 template <int FORMAT>
+__device__ __forceinline__ uint32_t widen2(uint32_t codes, std::integral_constant<bool, false>)
+{
+    if constexpr (FORMAT == 0)
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, 1.0f, false));
+    else
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(codes, 1.0f, false));
+}
+template <int FORMAT>
+__device__ __forceinline__ uint32_t widen2(uint32_t codes, std::integral_constant<bool, true>)
+{
+    if constexpr (FORMAT == 0)
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, 1.0f, true));
+    else
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(codes, 1.0f, true));
+}
+template <int FORMAT>
 __device__ __forceinline__ bf16x8_t widen(uint32_t lo, uint32_t hi)
 {
-    bf16x2_t v[4];
-    if constexpr (FORMAT == 0) {
-        v[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
-        v[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
-        v[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
-        v[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
-    } else {
-        v[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, false);
-        v[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, true);
-        v[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, false);
-        v[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, true);
-    }
-    return bf16x8_t{v[0][0], v[0][1], v[1][0], v[1][1], v[2][0], v[2][1], v[3][0], v[3][1]};
+    constexpr std::integral_constant<bool, false> low{};
+    constexpr std::integral_constant<bool, true> high{};
+    return __builtin_bit_cast(bf16x8_t, make_uint4(widen2<FORMAT>(lo, low), widen2<FORMAT>(lo, high),
+                                                   widen2<FORMAT>(hi, low), widen2<FORMAT>(hi, high)));
 }
-struct Widened {
-    bf16x8_t part[4];
-};
-template <int FORMAT>
-__device__ __forceinline__ Widened widen(const Codes& c)
+// 128 codes of 16 rows by 128 of 16 columns; xw: the columns' widened.
+__device__ __forceinline__ f32x4_t mma_block(const Codes& w, const bf16x8_t (&xw)[4])
 {
-    return Widened{{widen<FORMAT>(c.lo.x, c.lo.y), widen<FORMAT>(c.lo.z, c.lo.w),
-                    widen<FORMAT>(c.hi.x, c.hi.y), widen<FORMAT>(c.hi.z, c.hi.w)}};
+    f32x4_t d = {0.0f, 0.0f, 0.0f, 0.0f};
+    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen<0>(w.lo.x, w.lo.y), xw[0], d, 0, 0, 0);
+    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen<0>(w.lo.z, w.lo.w), xw[1], d, 0, 0, 0);
+    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen<0>(w.hi.x, w.hi.y), xw[2], d, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen<0>(w.hi.z, w.hi.w), xw[3], d, 0, 0, 0);
 }
 
 struct Scaled {
@@ -282,7 +289,9 @@ void fp8_kernel(Scaled a)
 }
 
 // Few rows an expert: as ep_expert_few.hip, a step of 128 codes at a time.
-template <typename T, int FORMAT, bool GLU, int RT, int CT, int WAVES>
+// SPLIT as above, for halves that are not whole blocks of 16 outputs: a block
+// of 16 then may lie in two scales.
+template <typename T, int FORMAT, bool GLU, bool SPLIT, int RT, int CT, int WAVES>
 __global__ __launch_bounds__(WAVES * 64)
 void fp8_few_kernel(Scaled a)
 {
@@ -298,7 +307,8 @@ void fp8_few_kernel(Scaled a)
     const int half_n = a.n / kHalves;
 
     const char* wr[RT];
-    const float* ws[RT][4];     // scales of the four outputs a lane holds of a row block
+    constexpr int kS = SPLIT ? 4 : 1;
+    const float* ws[RT][kS];    // scales of the (four) outputs a lane holds of a row block
     const float* ws0 = a.w_scales + (int64_t)it.expert * a.n_blocks * a.k_blocks;
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
@@ -307,14 +317,56 @@ void fp8_few_kernel(Scaled a)
         const int mine = n + col < half_n ? n + col : half_n - 1;
         wr[r] = a.w + ((int64_t)it.expert * a.n + mine + up) * a.k + quad * 16;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int o = n + quad * 4 + i < half_n ? n + quad * 4 + i : half_n - 1;
-            ws[r][i] = ws0 + (int64_t)((o + up) / 128) * a.k_blocks;
+        for (int i = 0; i < kS; ++i) {
+            const int o = n + (SPLIT ? quad * 4 + i : 0);
+            ws[r][i] = ws0 + (int64_t)(((o < half_n ? o : half_n - 1) + up) / 128) * a.k_blocks;
         }
     }
+    struct Step {
+        Codes w[RT], x[CT];
+        float s[RT][kS];
+        uint32_t xs[CT];
+    };
     const char* xr[CT];
     int64_t xs_at[CT];
-    // Rows past the item's repeat its first row; their results are dropped.
+    // 128 codes of a row from k on: two chunks of 16 in this lane.  Chunks past
+    // a.k are read from the row's start, and taken as 0.
+    auto load_codes = [&](const char* row, int k) {
+        const bool lo = k + quad * 16 < a.k, hi = k + 64 + quad * 16 < a.k;
+        return Codes{*reinterpret_cast<const uint4*>(row + (lo ? k : -quad * 16)),
+                     *reinterpret_cast<const uint4*>(row + (hi ? k + 64 : -quad * 16))};
+    };
+    auto drop = [&](Codes& c, int k) {
+        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+        if (k + quad * 16 >= a.k) c.lo = none;
+        if (k + 64 + quad * 16 >= a.k) c.hi = none;
+    };
+    auto load_weights = [&](Step& t, int kt) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            t.w[r] = load_codes(wr[r], kt * 128);
+#pragma unroll
+            for (int i = 0; i < kS; ++i) t.s[r][i] = ws[r][i][kt];
+        }
+    };
+    auto load_x = [&](Step& t, int kt) {
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+            t.x[c] = load_codes(xr[c], kt * 128);
+            t.xs[c] = raw_scale(a, xs_at[c] + kt * a.scale_block);
+        }
+    };
+
+    f32x4_t acc[RT][CT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) acc[r][c] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    // The weights' first loads go out before the rows of x are known.  Rows
+    // past the item's repeat its first row; their results are dropped.
+    Step t;
+    int kt = wave;
+    load_weights(t, kt);
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
         const int in = c * 16 + col;
@@ -326,46 +378,36 @@ void fp8_few_kernel(Scaled a)
         xr[c] = a.x + r * a.ld_x + quad * 16;
         xs_at[c] = r * a.scale_row;
     }
-
-    f32x4_t acc[RT][CT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int c = 0; c < CT; ++c) acc[r][c] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int kt = wave; kt < a.k_blocks; kt += waves) {
-        const int k = kt * 128;
-        // chunks of 16 codes past k: read at 0, taken as 0
-        const bool lo = k + quad * 16 < a.k, hi = k + 64 + quad * 16 < a.k;
-        Codes w[RT], x[CT];
-        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            w[r].lo = lo ? *reinterpret_cast<const uint4*>(wr[r] + k) : none;
-            w[r].hi = hi ? *reinterpret_cast<const uint4*>(wr[r] + k + 64) : none;
+    load_x(t, kt);
+    while (true) {
+        const int next = kt + waves;
+        Step n;
+        if (next < a.k_blocks) {
+            load_weights(n, next);
+            load_x(n, next);
         }
-        float s[RT][4], xs[CT];
+        if (kt * 128 + 128 > a.k) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r) drop(t.w[r], kt * 128);
+#pragma unroll
+            for (int c = 0; c < CT; ++c) drop(t.x[c], kt * 128);
+        }
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
-            x[c].lo = lo ? *reinterpret_cast<const uint4*>(xr[c] + k) : none;
-            x[c].hi = hi ? *reinterpret_cast<const uint4*>(xr[c] + k + 64) : none;
-            xs[c] = scale_value(a, raw_scale(a, xs_at[c] + kt * a.scale_block));
-        }
+            const bf16x8_t xw[4] = {widen<FORMAT>(t.x[c].lo.x, t.x[c].lo.y), widen<FORMAT>(t.x[c].lo.z, t.x[c].lo.w),
+                                    widen<FORMAT>(t.x[c].hi.x, t.x[c].hi.y), widen<FORMAT>(t.x[c].hi.z, t.x[c].hi.w)};
+            const float xs = scale_value(a, t.xs[c]);
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[r][i] = ws[r][i][kt];
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int c = 0; c < CT; ++c) {
-                const Widened wv = widen<0>(w[r]), xv = widen<FORMAT>(x[c]);
-                f32x4_t d = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int r = 0; r < RT; ++r) {
+                const f32x4_t d = mma_block(t.w[r], xw);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv.part[i], xv.part[i], d, 0, 0, 0);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[r][c][i] = __builtin_fmaf(d[i], xs[c] * s[r][i], acc[r][c][i]);
+                    acc[r][c][i] = __builtin_fmaf(d[i], xs * t.s[r][SPLIT ? i : 0], acc[r][c][i]);
             }
+        }
+        if (next >= a.k_blocks) break;
+        kt = next;
+        t = n;
     }
 
 #pragma unroll
@@ -418,7 +460,7 @@ hipError_t launch(const ExpertFp8Args& a, hipStream_t stream)
     return hipGetLastError();
 }
 
-template <typename T, int FORMAT, bool GLU, int RT, int CT, int WAVES>
+template <typename T, int FORMAT, bool GLU, bool SPLIT, int RT, int CT, int WAVES>
 hipError_t launch_few(const ExpertFp8Args& a, hipStream_t stream)
 {
     Scaled p = scaled(a);
@@ -426,9 +468,20 @@ hipError_t launch_few(const ExpertFp8Args& a, hipStream_t stream)
     p.col_tiles = (((GLU ? a.n / 2 : a.n) + 15) / 16 + kBlocks - 1) / kBlocks;
     const int waves = WAVES < p.k_blocks ? WAVES : p.k_blocks;
     const int64_t items = max_row_blocks(a.num_rows, a.num_experts, 16 * CT);
-    hipLaunchKernelGGL((fp8_few_kernel<T, FORMAT, GLU, RT, CT, WAVES>), dim3((unsigned)(items * p.col_tiles)),
+    hipLaunchKernelGGL((fp8_few_kernel<T, FORMAT, GLU, SPLIT, RT, CT, WAVES>), dim3((unsigned)(items * p.col_tiles)),
                        dim3(waves * 64), (size_t)waves * RT * CT * 1024, stream, p);
     return hipGetLastError();
+}
+
+template <typename T, int FORMAT, bool GLU, bool SPLIT>
+hipError_t few_sized(const ExpertFp8Args& a, hipStream_t stream)
+{
+    const int64_t hold = a.num_rows < a.num_experts ? a.num_rows : a.num_experts;
+    if (a.num_rows / hold > 16) return launch_few<T, FORMAT, GLU, SPLIT, 2, 2, 4>(a, stream);
+    const int64_t blocks = max_row_blocks(a.num_rows, a.num_experts, 16) * ((a.n + 15) / 16);
+    if (blocks >= 8192) return launch_few<T, FORMAT, GLU, SPLIT, 4, 1, 4>(a, stream);
+    if (blocks >= 1024) return launch_few<T, FORMAT, GLU, SPLIT, 2, 1, 2>(a, stream);
+    return launch_few<T, FORMAT, GLU, SPLIT, 2, 1, 8>(a, stream);
 }
 
 template <typename T, int FORMAT, bool GLU>
@@ -436,8 +489,10 @@ hipError_t sized(const ExpertFp8Args& a, hipStream_t stream)
 {
     const int64_t hold = a.num_rows < a.num_experts ? a.num_rows : a.num_experts;
     const int64_t each = a.num_rows / hold;
-    if (each <= 16) return launch_few<T, FORMAT, GLU, 2, 1, 8>(a, stream);
-    if (each <= 32) return launch_few<T, FORMAT, GLU, 2, 2, 4>(a, stream);
+    if (each <= 32) {
+        if (GLU && a.n / 2 % 16 != 0) return few_sized<T, FORMAT, GLU, GLU>(a, stream);
+        return few_sized<T, FORMAT, GLU, false>(a, stream);
+    }
     // rows that 32-bit offsets do not reach, or two scales a tile: the general form
     const int64_t reach = (a.src != nullptr ? a.x_rows : 256) * a.ld_x, gate = GLU ? (a.n / 2 + 256) * (int64_t)a.k : 0;
     if ((GLU && a.n / 2 % 128 != 0) || reach >= (int64_t)1 << 32 || gate >= (int64_t)1 << 32)

@@ -318,15 +318,19 @@ struct RowOperand {
     {
         load_lds_or_zero<I * THREADS * 16>(lds, base + (int64_t)s * 128, off[I], s * 128 + chunk * 16 < bytes);
     }
-    __device__ __forceinline__ void found() const {}
     // By way of registers, for rows that do not start on 16 bytes or do not
     // end with a chunk.
     template <typename T>
     __device__ __forceinline__ void fetch(uint4 (&v)[kLoads], int s) const
     {
+        if (s * 128 + 128 <= bytes) {       // no branch between the loads
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            v[i] = fetch16<T>(base + (int64_t)s * 128 + off[i], (bytes - s * 128 - chunk * 16) / 2);
+            for (int i = 0; i < kLoads; ++i) v[i] = fetch16<T>(base + (int64_t)s * 128 + off[i], 8);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                v[i] = fetch16<T>(base + (int64_t)s * 128 + off[i], (bytes - s * 128 - chunk * 16) / 2);
+        }
     }
     // Chunk c of the row of this lane in block b of the wavefront's rows.
     __device__ __forceinline__ static uint4 chunk_of(const char* lds, int row0, int b, int c)
@@ -343,109 +347,60 @@ struct RowOperand {
 };
 
 // An operand of 16-bit elements that lies across the reduction: 64 rows (its
-// steps) by COLS columns.  With GATHER the rows are picked by an index each.
-template <int COLS, int THREADS, bool GATHER = false, typename OFF = uint32_t>
+// steps) by COLS columns.
+template <int COLS, int THREADS, typename OFF = uint32_t>
 struct ColOperand {
     static constexpr int kChunks = COLS / 8;
     static constexpr int kLoads = 64 * kChunks / THREADS;
     static constexpr int kBytes = 64 * COLS * 2;
     static constexpr int kRowStep = THREADS / kChunks;  // a multiple of 4: the turn is the same for all
-    static constexpr int kSide = 64 / kChunks;          // rows a wavefront loads at a time
     static_assert(kRowStep % 4 == 0, "rows of a thread share their turn");
-    typedef const __attribute__((address_space(4))) int32_t* scalar_ptr;
     const char* base;
     OFF off[kLoads];
     int64_t ld;                 // bytes
     int row, rows;              // of the tile this thread's first; of the reduction
     int valid;                  // elements of its chunk that are there
-    int wave_row;
-    scalar_ptr index;           // GATHER: of the reduction's rows, below `bound`
-    int64_t bound;
-    int next[GATHER ? kLoads : 1][kSide];   // of the coming step's rows
+    bool inside;                // all columns are
 
-    // `count` rows, `stride` bytes apart, from `from` on (GATHER: picked by
-    // `pick`, below `limit`); columns first .. of `cols`.
-    __device__ __forceinline__ void init(const char* from, int64_t stride, int count, int64_t first, int64_t cols,
-                                         const int32_t* pick = nullptr, int64_t limit = 0)
+    // `count` rows, `stride` bytes apart, from `from` on; columns first .. of
+    // `cols`.
+    __device__ __forceinline__ void init(const char* from, int64_t stride, int count, int64_t first, int64_t cols)
     {
         const int t = opaque(threadIdx.x), p = t % kChunks;
         row = t / kChunks;
-        wave_row = __builtin_amdgcn_readfirstlane(row);
         base = uniform(from);
         ld = stride;
         rows = count;
-        index = (scalar_ptr)pick;
-        bound = limit;
         const int64_t c = first + ((((p >> 2) ^ (row & 3)) << 2) | (p & 3)) * 8;
         valid = c + 8 <= cols ? 8 : c < cols ? (int)(cols - c) : 0;
+        inside = first + COLS <= cols;
         const OFF column = valid > 0 ? (OFF)c * 2 : 0;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) off[i] = (GATHER ? 0 : (OFF)((row + i * kRowStep) * ld)) + column;
-        if constexpr (GATHER) {
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) find(0, i);
-        }
+        for (int i = 0; i < kLoads; ++i) off[i] = (OFF)((row + i * kRowStep) * ld) + column;
     }
-    // GATHER: the indices are read ahead, by scalar loads, whose waiting does
-    // not touch the loads into LDS.
-    __device__ __forceinline__ void find(int s, int i)
-    {
-#pragma unroll
-        for (int j = 0; j < kSide; ++j) {
-            const int in = s * 64 + wave_row + i * kRowStep + j;
-            next[i][j] = index[in < rows ? in : 0];
-        }
-    }
-    // Makes the compiler wait for them here.
-    __device__ __forceinline__ void found()
-    {
-        if constexpr (GATHER) {
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-#pragma unroll
-                for (int j = 0; j < kSide; ++j)
-                    asm volatile("" ::"s"(__builtin_amdgcn_readfirstlane(next[i][j])));
-        }
-    }
-    // The offset of this thread's i-th row of the coming step, from `base`;
-    // reads the index after it.
-    __device__ __forceinline__ uint32_t gathered(int s, int i)
-    {
-        uint32_t o = 0;
-#pragma unroll
-        for (int j = 0; j < kSide; ++j) {
-            const int r = next[i][j];
-            const uint32_t at = r < 0 || r >= bound ? 0u : (uint32_t)r * (uint32_t)ld;
-            o = j == 0 || (int)(threadIdx.x & 63) / kChunks == j ? at : o;
-        }
-        find(s + 1, i);
-        return o;
-    }
+    // This thread's I-th chunk of step s into LDS.
     template <int I>
-    __device__ __forceinline__ void load(uint32_t lds, int s)
+    __device__ __forceinline__ void load(uint32_t lds, int s) const
     {
-        if constexpr (GATHER) load_lds<I * THREADS * 16>(lds, base, gathered(s, I) + off[I]);
-        else load_lds<I * THREADS * 16>(lds, base + s * 64 * ld, off[I]);
+        load_lds<I * THREADS * 16>(lds, base + s * 64 * ld, off[I]);
     }
+    // The same for a step that may be the last.
     template <int I>
-    __device__ __forceinline__ void load_end(uint32_t lds, int s)
+    __device__ __forceinline__ void load_end(uint32_t lds, int s) const
     {
-        const bool live = s * 64 + row + I * kRowStep < rows;
-        if constexpr (GATHER) load_lds_or_zero<I * THREADS * 16>(lds, base, gathered(s, I) + off[I], live);
-        else load_lds_or_zero<I * THREADS * 16>(lds, base + s * 64 * ld, off[I], live);
+        load_lds_or_zero<I * THREADS * 16>(lds, base + s * 64 * ld, off[I], s * 64 + row + I * kRowStep < rows);
     }
     template <typename T>
-    __device__ __forceinline__ void fetch(uint4 (&v)[kLoads], int s)
+    __device__ __forceinline__ void fetch(uint4 (&v)[kLoads], int s) const
     {
+        const char* from = base + (int64_t)s * 64 * ld;
+        if (inside && s * 64 + 64 <= rows) {        // no branch between the loads
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int in = s * 64 + row + i * kRowStep;
-            const char* from = base + (int64_t)s * 64 * ld + off[i];
-            if constexpr (GATHER) {
-                const int r = index[in < rows ? in : 0];
-                from = base + (r < 0 || r >= bound ? 0 : r * ld) + off[i];
-            }
-            v[i] = fetch16<T>(from, in < rows ? valid : 0);
+            for (int i = 0; i < kLoads; ++i) v[i] = fetch16<T>(from + off[i], 8);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                v[i] = fetch16<T>(from + off[i], s * 64 + row + i * kRowStep < rows ? valid : 0);
         }
     }
     // Operand of a 32-column matrix instruction: part s of the step, columns
@@ -607,8 +562,6 @@ struct Ring {
         part<1, true, KIND, 2>(acc, w, nw, now, 2, s - 1, before);
         part<0, true, KIND, 3>(acc, w, nw, now, 3, s - 1, before);
         wait_barrier<kLeft>();
-        w.p.found();
-        if constexpr (KIND == 2) nw.p.found();
         part<1, true, KIND, 0>(acc, w, nw, then, 0, s, now);
         now = then;
     }

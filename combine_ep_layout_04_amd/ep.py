@@ -61,7 +61,7 @@ SYMBOLS = ("ep_version", "ep_status_string", "ep_last_error", "ep_layout_workspa
            "ep_router", "ep_router_backward", "ep_permute", "ep_permute_backward", "ep_unpermute",
            "ep_unpermute_backward", "ep_w4_packed_size", "ep_w4_pack", "ep_expert_matmul_w4",
            "ep_expert_matmul", "ep_expert_glu", "ep_expert_matmul_backward",
-           "ep_expert_glu_backward_workspace_size", "ep_expert_glu_backward", "ep_expert_matmul_fp8")
+           "ep_expert_backward_workspace_size", "ep_expert_glu_backward", "ep_expert_matmul_fp8")
 
 
 class EpError(RuntimeError):
@@ -172,10 +172,10 @@ def lib() -> ctypes.CDLL:
                                     P]
         L.ep_expert_glu.restype = i32
         L.ep_expert_matmul_backward.argtypes = [P, i32, i64, P, i64, i64, P, P, i32, i32, i32, P, P,
-                                                i64, P, i64, P, i32, P]
+                                                i64, P, i64, P, i32, P, sz, P]
         L.ep_expert_matmul_backward.restype = i32
-        L.ep_expert_glu_backward_workspace_size.argtypes = [i64, i32]
-        L.ep_expert_glu_backward_workspace_size.restype = sz
+        L.ep_expert_backward_workspace_size.argtypes = [i64, i32, i32, i32, i32]
+        L.ep_expert_backward_workspace_size.restype = sz
         L.ep_expert_glu_backward.argtypes = [P, i32, i64, P, i64, P, i64, i64, P, P, i32, i32, i32, P,
                                              P, i64, P, i64, P, i32, P, sz, P]
         L.ep_expert_glu_backward.restype = i32
@@ -1555,16 +1555,23 @@ def ep_expert_glu(x: torch.Tensor, weights: torch.Tensor, offsets: Optional[torc
     return out, pre
 
 
-def ep_expert_glu_backward_workspace_size(num_rows: int, out_features: int) -> int:
-    """Bytes of ep_expert_glu_backward's workspace (0 if the shape is invalid)."""
-    return int(lib().ep_expert_glu_backward_workspace_size(int(num_rows), int(out_features)))
+def ep_expert_backward_workspace_size(num_rows: int, out_features: int, in_features: int,
+                                      gated: bool = False, gathered: bool = False) -> int:
+    """Bytes of the backward's workspace, of ep_expert_glu_backward with
+    ``gated``, of a call with ``src`` with ``gathered`` (0 if none is needed or
+    the shape is invalid)."""
+    return int(lib().ep_expert_backward_workspace_size(int(num_rows), int(out_features), int(in_features),
+                                                       int(bool(gated)), int(bool(gathered))))
 
 
 def _expert_backward(grad_out, x, weights, offsets, src, counts, grad_rows, grad_weights, want_rows,
-                     want_weights, weights_dtype, stream, cols_of):
+                     want_weights, weights_dtype, workspace, stream,
+                     gated):
     E, N, K, ld_x, _ = _expert_rows(x, weights, offsets, src, counts, None)
     dev, dt = x.device, x.dtype
-    ld_g = _rows_of(grad_out, "grad_out", dt, cols_of(N), dev)
+    if gated and N % 2:
+        raise ValueError(f"gated weights have two halves, got {N} rows")
+    ld_g = _rows_of(grad_out, "grad_out", dt, N // 2 if gated else N, dev)
     R = grad_out.shape[0]
     if src is not None and src.numel() < R:
         raise ValueError(f"src has {src.numel()} elements, needs {R}")
@@ -1588,16 +1595,22 @@ def _expert_backward(grad_out, x, weights, offsets, src, counts, grad_rows, grad
             _need_on(grad_weights, "grad_weights", weights_dtype, dev)
             if tuple(grad_weights.shape) != (E, N, K):
                 raise ValueError(f"grad_weights must be {(E, N, K)}, is {tuple(grad_weights.shape)}")
+    need = ep_expert_backward_workspace_size(R, N, K, gated, src is not None)
+    if workspace is not None:
+        _need_on(workspace, "workspace", torch.uint8, dev, need)
+    elif need:
+        workspace = on.empty(need, torch.uint8)
     tail = (x.data_ptr(), ld_x, x.shape[0], _ptr(src), weights.data_ptr(), E, N, K, _ptr(offsets),
-            _ptr(counts), R, _ptr(grad_rows), ld_gr, _ptr(grad_weights), _DTYPES[weights_dtype])
-    return on, N, R, ld_g, tail, grad_rows, grad_weights
+            _ptr(counts), R, _ptr(grad_rows), ld_gr, _ptr(grad_weights), _DTYPES[weights_dtype],
+            _ptr(workspace), 0 if workspace is None else workspace.numel())
+    return on, N, R, ld_g, tail, grad_rows, grad_weights, workspace
 
 
 def ep_expert_matmul_backward(grad_out: torch.Tensor, x: torch.Tensor, weights: torch.Tensor,
                               offsets: Optional[torch.Tensor] = None, *,
                               src: Optional[torch.Tensor] = None, counts=None, grad_rows=None,
                               grad_weights=None, want_rows: bool = True, want_weights: bool = True,
-                              weights_dtype: Optional[torch.dtype] = None, stream=None):
+                              weights_dtype: Optional[torch.dtype] = None, workspace=None, stream=None):
     """Backward of ep_expert_matmul from ``grad_out`` [rows, N]: (grad_rows
     [rows, K], grad_weights [E, N, K]); the latter in ``weights_dtype``, the
     weights' own type or float32 (summed in fp32 either way), zeros for experts
@@ -1605,10 +1618,14 @@ def ep_expert_matmul_backward(grad_out: torch.Tensor, x: torch.Tensor, weights: 
 
     With ``src`` the rows' gradients still come per row of the layout;
     ep_permute_backward sums them per token.  ``want_rows`` / ``want_weights``
-    False leaves one out (None).  Rows of no expert are not written."""
-    on, N, R, ld_g, tail, grad_rows, grad_weights = _expert_backward(
+    False leaves one out (None).  Rows of no expert are not written.
+
+    ``workspace`` (uint8, ep_expert_backward_workspace_size bytes) holds rows
+    that are gathered or padded first; torch allocates it when it is not
+    given."""
+    on, N, R, ld_g, tail, grad_rows, grad_weights, workspace = _expert_backward(
         grad_out, x, weights, offsets, src, counts, grad_rows, grad_weights, want_rows, want_weights,
-        weights_dtype, stream, lambda n: n)
+        weights_dtype, workspace, stream, False)
     on.call("ep_expert_matmul_backward", lib().ep_expert_matmul_backward, grad_out.data_ptr(),
             _DTYPES[grad_out.dtype], ld_g, *tail)
     return grad_rows, grad_weights
@@ -1622,26 +1639,16 @@ def ep_expert_glu_backward(grad_out: torch.Tensor, pre: torch.Tensor, x: torch.T
     """Backward of ep_expert_glu from ``grad_out`` [rows, N/2] and the ``pre``
     [rows, N] that it left; otherwise as ep_expert_matmul_backward.
 
-    ``workspace`` (uint8, ep_expert_glu_backward_workspace_size bytes) holds
-    the gradients of gate and up, in the rows' type; torch allocates it when
-    it is not given."""
-    on, N, R, ld_g, tail, grad_rows, grad_weights = _expert_backward(
+    ``workspace`` (uint8, ep_expert_backward_workspace_size bytes) also holds
+    the gradients of gate and up, in the rows' type."""
+    on, N, R, ld_g, tail, grad_rows, grad_weights, workspace = _expert_backward(
         grad_out, x, weights, offsets, src, counts, grad_rows, grad_weights, want_rows, want_weights,
-        weights_dtype, stream, lambda n: n // 2)
-    if N % 2:
-        raise ValueError(f"gated weights have two halves, got {N} rows")
-    dev = x.device
-    ld_p = _rows_of(pre, "pre", x.dtype, N, dev)
+        weights_dtype, workspace, stream, True)
+    ld_p = _rows_of(pre, "pre", x.dtype, N, x.device)
     if pre.shape[0] < R:
         raise ValueError(f"pre has {pre.shape[0]} rows, grad_out {R}")
-    need = ep_expert_glu_backward_workspace_size(R, N)
-    if workspace is None:
-        workspace = on.empty(need, torch.uint8)
-    else:
-        _need_on(workspace, "workspace", torch.uint8, dev, need)
     on.call("ep_expert_glu_backward", lib().ep_expert_glu_backward, grad_out.data_ptr(),
-            _DTYPES[grad_out.dtype], ld_g, pre.data_ptr(), ld_p, *tail, workspace.data_ptr(),
-            workspace.numel())
+            _DTYPES[grad_out.dtype], ld_g, pre.data_ptr(), ld_p, *tail)
     return grad_rows, grad_weights
 
 

@@ -972,8 +972,7 @@ ep_status_t ep_expert_glu(const void *x, int dtype, int64_t ld_x, int64_t num_x_
  *                     an expert without rows)
  *
  * d is grad_out for ep_expert_matmul; for ep_expert_glu it is made from
- * grad_out and pre in fp32 and rounded to dtype (the matrix cores' type), and
- * lies in the workspace.
+ * grad_out and pre in fp32 and rounded to dtype (the matrix cores' type).
  *
  * In:  grad_out   dtype [num_rows, out_features] (out_features / 2 columns
  *                 for ep_expert_glu), row stride ld_grad_out.
@@ -985,14 +984,17 @@ ep_status_t ep_expert_glu(const void *x, int dtype, int64_t ld_x, int64_t num_x_
  *                 to no expert are not written.
  *      grad_weights  NULL, or [num_experts, out_features, in_features], packed,
  *                 of grad_weights_dtype: dtype or EP_FP32.
- *      workspace  ep_expert_glu_backward_workspace_size(...) bytes, 16-byte
- *                 aligned, for the call's duration (two calls that may overlap
- *                 in time need one each).
+ *      workspace  ep_expert_backward_workspace_size(...) bytes, 16-byte
+ *                 aligned (NULL where these are 0), for the call's duration:
+ *                 two calls that may overlap in time need one each.  It holds
+ *                 the gated product's d, and rows that are laid out first: x
+ *                 gathered by src, rows that are not whole 16-byte vectors.
  * At least one of grad_rows and grad_weights is given; weights may be NULL
  * without grad_rows, x without grad_weights.  Sums are fp32, in a fixed order,
  * rounded once.
- * ep_expert_glu_backward_workspace_size is host arithmetic; 0 for an invalid
- * shape.
+ * ep_expert_backward_workspace_size is host arithmetic (gated: for
+ * ep_expert_glu_backward; gathered: with src); 0 for an invalid shape, and
+ * where none is needed.
  */
 ep_status_t ep_expert_matmul_backward(const void *grad_out, int dtype, int64_t ld_grad_out,
                                       const void *x, int64_t ld_x, int64_t num_x_rows,
@@ -1000,8 +1002,10 @@ ep_status_t ep_expert_matmul_backward(const void *grad_out, int dtype, int64_t l
                                       int out_features, int in_features, const int32_t *offsets,
                                       const int32_t *counts, int64_t num_rows, void *grad_rows,
                                       int64_t ld_grad_rows, void *grad_weights,
-                                      int grad_weights_dtype, void *stream);
-size_t ep_expert_glu_backward_workspace_size(int64_t num_rows, int out_features);
+                                      int grad_weights_dtype, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+size_t ep_expert_backward_workspace_size(int64_t num_rows, int out_features, int in_features, int gated,
+                                         int gathered);
 ep_status_t ep_expert_glu_backward(const void *grad_out, int dtype, int64_t ld_grad_out,
                                    const void *pre, int64_t ld_pre, const void *x, int64_t ld_x,
                                    int64_t num_x_rows, const int32_t *src, const void *weights,

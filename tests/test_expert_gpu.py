@@ -179,7 +179,8 @@ def test_glu_backward(case, wide_w):
     c.untouched(buf, c.K)
     d, ed = glu_gradient(dh, c.pre, c.dtype)
     check_backward(c, d, ed, gr, gw, "fp32" if wide_w else c.dtype)
-    work = torch.empty(ep.ep_expert_glu_backward_workspace_size(c.R, c.N), dtype=torch.uint8, device=DEV)
+    need = ep.ep_expert_backward_workspace_size(c.R, c.N, c.K, True, c.tsrc is not None)
+    work = torch.empty(need, dtype=torch.uint8, device=DEV)
     none, w2 = ep.ep_expert_glu_backward(g, p, c.tx, c.tw, c.offsets, want_rows=False, workspace=work, **kw)
     assert none is None and bits_equal(w2, gw)
 

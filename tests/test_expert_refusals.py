@@ -54,7 +54,7 @@ def test_glu_rejects(over, code):
 
 
 BACKWARD = dict(g=FAKE, dtype=0, ldg=32, x=FAKE, ldx=64, M=8, src=None, w=FAKE, E=2, N=32, K=64, offsets=FAKE,
-                counts=None, R=8, gr=FAKE, ldgr=64, gw=FAKE, gwt=0)
+                counts=None, R=8, gr=FAKE, ldgr=64, gw=FAKE, gwt=0, work=None, bytes=0)
 GRADS = SHAPES + [
     (dict(g=None), 1), (dict(g=FAKE + 1), 1), (dict(gr=None, gw=None), 1), (dict(gwt=1), 1),
     (dict(dtype=1, gwt=0), 1), (dict(gw=FAKE + 1), 1), (dict(gwt=2, gw=FAKE + 2), 1), (dict(x=None), 1),
@@ -64,7 +64,11 @@ GRADS = SHAPES + [
 
 
 @no_gpu
-@pytest.mark.parametrize("over,code", GRADS + [(dict(ldg=31), 1)])
+@pytest.mark.parametrize("over,code", GRADS + [
+    (dict(ldg=31), 1), (dict(src=FAKE), 1), (dict(src=FAKE, work=FAKE, bytes=1023), 1),
+    (dict(src=FAKE, work=FAKE + 8, bytes=1024), 1), (dict(N=30), 1), (dict(K=63), 1),
+    (dict(R=(1 << 31) - 1, M=1 << 31, N=1 << 20, ldg=1 << 20), 2),
+])
 def test_matmul_backward_rejects(over, code):
     assert call("ep_expert_matmul_backward", BACKWARD, over) == code, ep.last_error()
     assert ep.last_error()
@@ -86,10 +90,14 @@ def test_glu_backward_rejects(over, code):
 
 
 def test_workspace_size():
-    size = ep.ep_expert_glu_backward_workspace_size
-    assert size(8, 32) == 512 and size(3, 34) == 3 * 40 * 2 and size(0, 32) == 0
-    assert size(-1, 32) == size(8, 33) == size(8, 0) == size(1 << 31, 32) == size(8, (1 << 20) + 2) == 0
-    assert size((1 << 31) - 1, 1 << 20) == ((1 << 31) - 1) << 21
+    size = ep.ep_expert_backward_workspace_size
+    assert size(8, 32, 64) == size(0, 32, 64) == 0
+    assert size(8, 32, 64, gated=True) == 512 and size(8, 32, 64, gathered=True) == 1024
+    assert size(3, 34, 64) == 3 * 40 * 2 and size(3, 32, 65) == 3 * 72 * 2
+    assert size(3, 34, 65, gated=True, gathered=True) == 3 * (40 + 72) * 2
+    assert size(-1, 33, 64) == size(8, 33, 64, gated=True) == size(8, 0, 63) == size(8, 33, 0) == 0
+    assert size(1 << 31, 33, 64) == size(8, (1 << 20) + 1, 63) == size(8, 33, 65537) == 0
+    assert size((1 << 31) - 1, 1 << 20, 65535, gated=True) == ((1 << 31) - 1) * ((1 << 21) + (1 << 17))
 
 
 FP8 = dict(x=FAKE, fmt=1, ldx=128, M=8, xs=FAKE, sf=0, sr=1, sb=8, src=None, w=FAKE, ws=FAKE, E=2, N=32, K=128,
@@ -116,7 +124,7 @@ def test_no_rows_reads_nothing():
     assert call("ep_expert_matmul", MATMUL, null) == 0
     assert call("ep_expert_glu", GLU, null) == 0
     assert call("ep_expert_matmul_fp8", FP8, dict(null, xs=None, ws=None)) == 0
-    assert call("ep_expert_matmul_backward", BACKWARD, dict(R=0, g=None, x=None, w=None, gw=None)) == 0
+    assert call("ep_expert_matmul_backward", BACKWARD, dict(R=0, g=None, x=None, w=None, gw=None, src=FAKE)) == 0
     assert call("ep_expert_glu_backward", GLU_B, dict(R=0, g=None, x=None, w=None, gw=None, work=None)) == 0
 
 
