@@ -42,7 +42,7 @@ void expert_kernel(Product<T> a)
     using Off = std::conditional_t<DIRECT, uint32_t, uint64_t>;
     using P = RowOperand<BP, kThreads, Off>;
     using Q = RowOperand<BQ, kThreads, Off>;
-    using R = Ring<T, P, Q, PB, QB, RING>;
+    using R = Ring<P, Q, RING>;
     __shared__ __attribute__((aligned(128))) char lds[DIRECT ? R::kLds : 2 * (P::kBytes + Q::kBytes)];
 
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -134,7 +134,7 @@ hipError_t launch(const ExpertArgs& a, hipStream_t stream)
     p.walk.col_tiles = (n + kCols - 1) / kCols;
     p.walk.tiles = tile_count(max_row_blocks(a.num_rows, a.num_experts, BQ), p.walk.group, p.walk.col_tiles);
     hipLaunchKernelGGL((expert_kernel<T, GLU, DIRECT, BP, BQ, WP, WQ, RING>),
-                       dim3(tile_grid(p.walk.tiles, BQ <= 128 ? 2 : 1)), dim3(WP * WQ * 64), 0, stream, p);
+                       dim3(tile_grid(p.walk.tiles, DIRECT ? 1 : 2)), dim3(WP * WQ * 64), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -150,7 +150,7 @@ hipError_t sized(const ExpertArgs& a, hipStream_t stream)
     if (!direct) return launch<T, GLU, false, 128, 128, 2, 2, 4>(a, stream);
     const int64_t hold = a.num_rows < a.num_experts ? a.num_rows : a.num_experts;
     if (a.num_rows / hold >= 192) return launch<T, GLU, true, 256, 256, 2, 2, 5>(a, stream);
-    return launch<T, GLU, true, 128, 128, 2, 2, 5>(a, stream);
+    return launch<T, GLU, true, 256, 128, 2, 2, 5>(a, stream);
 }
 
 }  // namespace

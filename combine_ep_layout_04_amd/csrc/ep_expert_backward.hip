@@ -41,7 +41,7 @@ void rows_grad_kernel(RowsGrad<T> a)
     using Off = std::conditional_t<DIRECT, uint32_t, uint64_t>;
     using P = ColOperand<BP, kThreads, Off>;
     using Q = RowOperand<BQ, kThreads, Off>;
-    using R = Ring<T, P, Q, PB, QB, RING>;
+    using R = Ring<P, Q, RING>;
     __shared__ __attribute__((aligned(128))) char lds[DIRECT ? R::kLds : 2 * (P::kBytes + Q::kBytes)];
 
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -114,7 +114,7 @@ void weight_grad_kernel(WeightGrad<T> a)
     using Off = std::conditional_t<DIRECT, uint32_t, uint64_t>;
     using P = ColOperand<BP, kThreads, Off>;
     using Q = ColOperand<BQ, kThreads, Off>;
-    using R = Ring<T, P, Q, PB, QB, RING>;
+    using R = Ring<P, Q, RING>;
     __shared__ __attribute__((aligned(128))) char lds[DIRECT ? R::kLds : 2 * (P::kBytes + Q::kBytes)];
 
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -165,6 +165,95 @@ void weight_grad_kernel(WeightGrad<T> a)
         w.turn = 0;
     };
     tiles<T, DIRECT, P, Q, PB, QB, RING, kThreads, Tile>(lds, p0, q0, find, prepare, store, 0);
+}
+
+// The same for experts of few rows, where the time is that of writing the
+// gradients: one place in LDS for a step's operands, and as many workgroups on
+// a CU as keep its memory pipeline busy instead of loads ahead.  Results leave
+// through LDS, so that a store covers whole lines: rows of 128 columns, chunk c
+// of row n at place c ^ (n % 16).
+template <typename T, typename O>
+__global__ __launch_bounds__(256, 4)
+void weight_grad_short_kernel(WeightGrad<T> a)
+{
+    constexpr int kThreads = 256, PB = 2, QB = 2;
+    using P = ColOperand<128, kThreads>;
+    using Q = ColOperand<128, kThreads>;
+    __shared__ __attribute__((aligned(128))) char lds[P::kBytes + Q::kBytes];
+
+    const int64_t at = tile_of(0), per = (int64_t)a.k_tiles * a.n_tiles;
+    if (at >= a.tiles) return;
+    const int expert = (int)(at / per);
+    const unsigned of = (unsigned)(at % per);
+    const int64_t n0 = (int64_t)(of / (unsigned)a.k_tiles) * 128, k0 = (int64_t)(of % (unsigned)a.k_tiles) * 128;
+    RowBlock rb = {expert, 0, a.seg.num_rows};
+    if (a.seg.offsets != nullptr) {
+        rb.first = uniform(a.seg.offsets[expert]);
+        rb.rows = uniform(a.seg.counts != nullptr ? a.seg.counts[expert] : a.seg.offsets[expert + 1] - rb.first);
+        bound_rows(rb, a.seg.num_rows);
+    }
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int p0 = wave / 2 * 64, q0 = wave % 2 * 64, lane = threadIdx.x & 63;
+    f32x16_t acc[PB][QB];
+    clear(acc);
+    if (rb.rows > 0) {
+        P p;
+        Q q;
+        p.init(reinterpret_cast<const char*>(a.x + rb.first * a.ld_x), a.ld_x * 2, rb.rows, k0, a.k);
+        q.init(reinterpret_cast<const char*>(a.grad + rb.first * a.ld_grad), a.ld_grad * 2, rb.rows, n0, a.n);
+        const uint32_t to = lds_address(lds) + wave * 1024;
+        const int steps = (rb.rows + 63) / 64;
+        for (int s = 0; s < steps; ++s) {
+            if (s > 0) wait_barrier();
+            load_operand<0>(p, to, s);
+            load_operand<0>(q, to + P::kBytes, s);
+            wait_barrier();
+            const int parts = (rb.rows - s * 64 + 15) / 16;
+#pragma unroll
+            for (int part = 0; part < 4; ++part) {
+                if (part >= parts) break;
+                uint4 pv[PB], qv[QB];
+#pragma unroll
+                for (int j = 0; j < QB; ++j) qv[j] = Q::part(lds + P::kBytes, q0, j, part);
+#pragma unroll
+                for (int i = 0; i < PB; ++i) pv[i] = P::part(lds, p0, i, part);
+#pragma unroll
+                for (int i = 0; i < PB; ++i)
+#pragma unroll
+                    for (int j = 0; j < QB; ++j)
+                        acc[i][j] = mma32(pv[i], qv[j], acc[i][j], static_cast<const T*>(nullptr));
+            }
+        }
+        wait_barrier();
+    }
+    O* out = static_cast<O*>(a.out) + (int64_t)expert * a.n * a.k;
+    if constexpr (std::is_same_v<O, float>) {
+#pragma unroll
+        for (int j = 0; j < QB; ++j) {
+            const int64_t n = n0 + q0 + j * 32 + (lane & 31);
+            const bool live = n < a.n;
+#pragma unroll
+            for (int i = 0; i < PB; ++i)
+                store_block(acc[i][j], out + (live ? n : 0) * a.k, k0 + p0 + i * 32, a.k, live);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < QB; ++j)
+#pragma unroll
+            for (int i = 0; i < PB; ++i) {
+                const int n = q0 + j * 32 + (lane & 31);
+                put_block<T>(acc[i][j], [&](int c) {
+                    return lds + n * 256 + ((((p0 + i * 32 + c) / 8) ^ (n & 15)) << 4);
+                });
+            }
+        wait_barrier();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int n = i * 16 + (threadIdx.x >> 4), c = threadIdx.x & 15;
+            const uint4 v = *reinterpret_cast<const uint4*>(lds + n * 256 + ((c ^ (n & 15)) << 4));
+            if (n0 + n < a.n) store_chunk(v, out + (n0 + n) * a.k, k0 + c * 8, a.k);
+        }
+    }
 }
 
 // Both halves' gradients, a row's units of 8 outputs per thread.  Memory
@@ -221,7 +310,7 @@ hipError_t launch_rows(const ExpertBackwardArgs& a, hipStream_t stream)
     p.walk.col_tiles = (a.k + BP - 1) / BP;
     p.walk.tiles = tile_count(max_row_blocks(a.num_rows, a.num_experts, BQ), p.walk.group, p.walk.col_tiles);
     hipLaunchKernelGGL((rows_grad_kernel<T, DIRECT, BP, BQ, WP, WQ, RING>),
-                       dim3(tile_grid(p.walk.tiles, BQ <= 128 ? 2 : 1)), dim3(WP * WQ * 64), 0, stream, p);
+                       dim3(tile_grid(p.walk.tiles, DIRECT ? 1 : 2)), dim3(WP * WQ * 64), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -233,7 +322,19 @@ hipError_t launch_weights(const ExpertBackwardArgs& a, hipStream_t stream)
                        a.grad_w, (a.k + BP - 1) / BP, (a.n + BQ - 1) / BQ, 0};
     p.tiles = (int64_t)a.num_experts * p.k_tiles * p.n_tiles;
     hipLaunchKernelGGL((weight_grad_kernel<T, O, DIRECT, BP, BQ, WP, WQ, RING>),
-                       dim3(tile_grid(p.tiles, BQ <= 128 ? 2 : 1)), dim3(WP * WQ * 64), 0, stream, p);
+                       dim3(tile_grid(p.tiles, DIRECT ? 1 : 2)), dim3(WP * WQ * 64), 0, stream, p);
+    return hipGetLastError();
+}
+
+template <typename T, typename O>
+hipError_t launch_weights_short(const ExpertBackwardArgs& a, hipStream_t stream)
+{
+    WeightGrad<T> p = {static_cast<const T*>(a.grad), a.ld_grad, static_cast<const T*>(a.x), a.ld_x,
+                       a.n, a.k, {a.offsets, a.counts, a.num_experts, (int)a.num_rows},
+                       a.grad_w, (a.k + 127) / 128, (a.n + 127) / 128, 0};
+    p.tiles = (int64_t)a.num_experts * p.k_tiles * p.n_tiles;
+    hipLaunchKernelGGL((weight_grad_short_kernel<T, O>), dim3(tile_grid(p.tiles, INT32_MAX / 8192)), dim3(256), 0,
+                       stream, p);
     return hipGetLastError();
 }
 
@@ -276,8 +377,8 @@ hipError_t weights_sized(const ExpertBackwardArgs& a, hipStream_t stream)
                         a.ld_grad % 8 == 0 && in_reach(64 * a.ld_x) && in_reach(64 * a.ld_grad) && !off16(a.x) &&
                         !off16(a.grad);
     if (!direct) return launch_weights<T, O, false, 128, 128, 2, 2, 4>(a, stream);
-    if (a.num_rows / a.num_experts >= 192) return launch_weights<T, O, true, 256, 256, 2, 2, 5>(a, stream);
-    return launch_weights<T, O, true, 128, 128, 2, 2, 5>(a, stream);
+    if (a.num_rows / a.num_experts < 400) return launch_weights_short<T, O>(a, stream);
+    return launch_weights<T, O, true, 256, 256, 2, 2, 5>(a, stream);
 }
 
 template <typename T>
@@ -303,7 +404,7 @@ hipError_t backward(ExpertBackwardArgs a, hipStream_t stream)
         const int64_t hold = a.num_rows < a.num_experts ? a.num_rows : a.num_experts;
         const hipError_t err = !direct ? launch_rows<T, false, 128, 128, 2, 2, 4>(a, stream)
                                : a.num_rows / hold >= 192 ? launch_rows<T, true, 256, 256, 2, 2, 5>(a, stream)
-                                                          : launch_rows<T, true, 128, 128, 2, 2, 5>(a, stream);
+                                                          : launch_rows<T, true, 256, 128, 2, 2, 5>(a, stream);
         if (err != hipSuccess) return err;
     }
     if (a.grad_w == nullptr) return hipSuccess;

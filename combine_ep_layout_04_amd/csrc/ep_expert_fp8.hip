@@ -115,15 +115,6 @@ __device__ __forceinline__ Codes codes_part(const char* lds, int row0, int b, in
                  *reinterpret_cast<const uint4*>(p + (((4 * s + 2 + h) ^ turn) << 4))};
 }
 
-template <int I, typename O>
-__device__ __forceinline__ void load_operand(O& o, uint32_t to, int s)
-{
-    if constexpr (I < O::kLoads) {
-        o.template load_end<I>(to, s);
-        load_operand<I + 1>(o, to, s);
-    }
-}
-
 // SPLIT: the gated product's halves whose second does not start with a block
 // of 128 outputs; a tile's rows of it then lie in two blocks.
 template <typename T, int FORMAT, bool GLU, bool SPLIT, typename OFF, int BP, int BQ, int WP, int WQ>

@@ -419,6 +419,16 @@ struct ColOperand {
     }
 };
 
+// All of a thread's chunks of a step that may be the last into LDS.
+template <int I, typename O>
+__device__ __forceinline__ void load_operand(O& o, uint32_t to, int s)
+{
+    if constexpr (I < O::kLoads) {
+        o.template load_end<I>(to, s);
+        load_operand<I + 1>(o, to, s);
+    }
+}
+
 // A thread's chunks from registers to its operand's place in LDS.
 template <int THREADS, int LOADS>
 __device__ __forceinline__ void put_chunks(char* lds, const uint4 (&v)[LOADS])
@@ -441,14 +451,94 @@ struct Work {
     __device__ __forceinline__ int step(int s) const { return s + turn < steps ? s + turn : s + turn - steps; }
 };
 
-// Tiles one after another: PB x QB blocks of 32 x 32 per wavefront over the
-// reduction, 128 bytes of it a step, from LDS.
+// The ring of operand tiles in LDS that a workgroup's tiles go through one
+// after another, 128 bytes of the reduction a step.
 //
-// The two operands' tiles of a step take turns in a ring of RING places
-// (P of step 0, Q of 0, P of 1, ...; with 5 places of 32 KiB all of LDS): an
-// odd ring keeps more than a step in flight where LDS does not hold three.
-// The ring does not stop between tiles: the last steps of one send the loads
-// of the first steps of the next, which arrive while results are stored.
+// P has (RING + 1) / 2 places, Q RING / 2 (256 x 256 with 3 and 2: all of
+// LDS), and P is loaded a step further ahead where it has one more.  The ring
+// does not stop between tiles: the last steps of one send the loads of the
+// first steps of the next, which arrive while results are stored.
+template <typename P, typename Q, int RING>
+struct Ring {
+    using W = Work<P, Q>;
+    static constexpr int kP = (RING + 1) / 2, kQ = RING / 2;    // places
+    static constexpr int kQAt = kP * P::kBytes;                 // where Q's begin
+    static constexpr int kLds = kQAt + kQ * Q::kBytes;
+    static constexpr int kLoads = P::kLoads + Q::kLoads;
+    // loads that may be under way when a step changes: those behind the next
+    // step's
+    static constexpr int kLeft = (kQ - 2) * kLoads + (kP - kQ) * P::kLoads;
+    static constexpr int kAhead = kP;           // steps to the last load that follows a step
+    static constexpr int kFewestSteps = kAhead; // so that loads never reach past the next tile
+    static_assert(kQ >= 2, "two steps at least");
+
+    char* lds;
+    uint32_t at;
+    int p_now, q_now;       // the step's places, from lds
+
+    __device__ __forceinline__ Ring(char* shared) : lds(shared), p_now(0), q_now(kQAt)
+    {
+        at = lds_address(lds) + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) * 1024;
+    }
+    __device__ __forceinline__ static int p_after(int v) { return v + P::kBytes < kQAt ? v + P::kBytes : 0; }
+    __device__ __forceinline__ static int q_after(int v) { return v + Q::kBytes < kLds ? v + Q::kBytes : kQAt; }
+    __device__ __forceinline__ static int p_before(int v) { return v > 0 ? v - P::kBytes : kQAt - P::kBytes; }
+    __device__ __forceinline__ static int q_before(int v) { return v > kQAt ? v - Q::kBytes : kLds - Q::kBytes; }
+    __device__ __forceinline__ void advance()
+    {
+        p_now = p_after(p_now);
+        q_now = q_after(q_now);
+    }
+
+    template <int I, typename O>
+    __device__ __forceinline__ static void load_near(O& mine, O& next, const W& w, const W& nw, uint32_t to, int s)
+    {
+        if (s < w.steps) mine.template load_end<I>(to, w.step(s));
+        else next.template load_end<I>(to, nw.step(s - w.steps));
+    }
+    // The I-th of the loads that follow step s with its places p_at and q_at:
+    // Q's, then P's.  KIND 1: of whole steps of this tile; 2: of steps that may
+    // be the last, or the next tile's.
+    template <int I, int KIND>
+    __device__ __forceinline__ void load_one(W& w, W& nw, int s, int p_at, int q_at)
+    {
+        if constexpr (I < Q::kLoads) {
+            if constexpr (KIND == 1) w.q.template load<I>(at + q_at, w.step(s + kQ));
+            else load_near<I>(w.q, nw.q, w, nw, at + q_at, s + kQ);
+        } else {
+            if constexpr (KIND == 1) w.p.template load<I - Q::kLoads>(at + p_at, w.step(s + kP));
+            else load_near<I - Q::kLoads>(w.p, nw.p, w, nw, at + p_at, s + kP);
+        }
+    }
+    template <int I, int UPTO, int KIND>
+    __device__ __forceinline__ void load_some(W& w, W& nw, int s, int p_at, int q_at)
+    {
+        if constexpr (I < UPTO) {
+            load_one<I, KIND>(w, nw, s, p_at, q_at);
+            load_some<I + 1, UPTO, KIND>(w, nw, s, p_at, q_at);
+        }
+    }
+    // The first tile's first loads: what the steps before it would have sent,
+    // of the last of them the first SENT only.
+    template <int SENT>
+    __device__ __forceinline__ void begin(W& w)
+    {
+        start<0>(w);
+        load_some<0, SENT, 2>(w, w, -1, p_before(p_now), q_before(q_now));
+        wait_barrier<kLeft + SENT>();
+    }
+    template <int S>
+    __device__ __forceinline__ void start(W& w)
+    {
+        if constexpr (S + 1 < kP) {
+            load_operand<0>(w.p, at + S * P::kBytes, w.step(S));
+            if constexpr (S + 1 < kQ) load_operand<0>(w.q, at + kQAt + S * Q::kBytes, w.step(S));
+            start<S + 1>(w);
+        }
+    }
+};
+
+// PB x QB blocks of 32 x 32 per wavefront of 16-bit operands from the ring.
 //
 // Two sets of operands in registers: those of a part (16 elements of the
 // reduction, 32 bytes) are read while the part before it is multiplied.  The
@@ -459,137 +549,66 @@ struct Work {
 // and the wavefront stands still before its matrix instructions.  Reads and
 // loads take their turns after matrix instructions, by hand.
 template <typename T, typename P, typename Q, int PB, int QB, int RING>
-struct Ring {
+struct Steps : Ring<P, Q, RING> {
+    using R = Ring<P, Q, RING>;
     using W = Work<P, Q>;
-    static constexpr int kPlace = P::kBytes > Q::kBytes ? P::kBytes : Q::kBytes;
+    using R::kLoads;
     static constexpr int kMuls = PB * QB, kReads = PB + QB;
-    static constexpr int kLds = kPlace * RING;
-    static constexpr int kLoads = P::kLoads + Q::kLoads;
-    static constexpr bool kOdd = RING % 2 == 1;
-    // loads that may be under way when a step changes: those of the tiles
-    // behind the next step's
-    static constexpr int kLeft = (RING - 4) / 2 * kLoads + (kOdd ? P::kLoads : 0);
-    static constexpr int kAhead = (RING + 1) / 2;   // steps to the last load that follows a step
-    static constexpr int kFewestSteps = kAhead;     // so that loads never reach past the next tile
-    static_assert(RING >= 4, "two steps at least");
 
-    char* lds;
-    uint32_t at;
-    int p0, q0, now;        // now: the place of the step's P; Q's is behind it
+    int p0, q0;
     uint4 p[2][PB], q[2][QB];
 
-    __device__ __forceinline__ Ring(char* shared, int p_row, int q_row) : lds(shared), p0(p_row), q0(q_row), now(0)
-    {
-        at = lds_address(lds) + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) * 1024;
-    }
+    __device__ __forceinline__ Steps(char* shared, int p_row, int q_row) : R(shared), p0(p_row), q0(q_row) {}
 
-    __device__ __forceinline__ static int place(int v) { return v >= RING * kPlace ? v - RING * kPlace : v; }
-
-    template <int I, typename O>
-    __device__ __forceinline__ static void load_near(O& mine, O& next, const W& w, const W& nw, uint32_t to, int s)
-    {
-        if (s < w.steps) mine.template load_end<I>(to, w.step(s));
-        else next.template load_end<I>(to, nw.step(s - w.steps));
-    }
-    // The I-th of the loads that follow step s, whose P lies at `here`.  KIND
-    // 1: of whole steps of this tile; 2: of steps that may be the last, or the
-    // next tile's.
-    template <int I, int KIND>
-    __device__ __forceinline__ void load_one(W& w, W& nw, int s, int here)
-    {
-        // in an odd ring Q's next tile falls on P's place and comes first
-        constexpr bool kIsQ = kOdd ? I < Q::kLoads : I >= P::kLoads;
-        constexpr int kOf = kOdd ? (kIsQ ? I : I - Q::kLoads) : (kIsQ ? I - P::kLoads : I);
-        constexpr int kSecond = kOdd ? !kIsQ : kIsQ;
-        const int to = s + RING / 2 + (kOdd && !kIsQ ? 1 : 0);
-        const uint32_t where = at + (kSecond ? place(here + kPlace) : here);
-        if constexpr (KIND == 1) {
-            if constexpr (kIsQ) w.q.template load<kOf>(where, w.step(to));
-            else w.p.template load<kOf>(where, w.step(to));
-        } else {
-            if constexpr (kIsQ) load_near<kOf>(w.q, nw.q, w, nw, where, to);
-            else load_near<kOf>(w.p, nw.p, w, nw, where, to);
-        }
-    }
-    template <int I, int UPTO, int KIND>
-    __device__ __forceinline__ void load_some(W& w, W& nw, int s, int here)
+    template <int I, int UPTO>
+    __device__ __forceinline__ void read_some(int set, int p_at, int q_at, int part)
     {
         if constexpr (I < UPTO) {
-            load_one<I, KIND>(w, nw, s, here);
-            load_some<I + 1, UPTO, KIND>(w, nw, s, here);
-        }
-    }
-    template <int R, int UPTO>
-    __device__ __forceinline__ void read_some(int set, int here, int part)
-    {
-        if constexpr (R < UPTO) {
-            if constexpr (R < QB) q[set][R] = Q::part(lds + place(here + kPlace), q0, R, part);
-            else p[set][R - QB] = P::part(lds + here, p0, R - QB, part);
-            read_some<R + 1, UPTO>(set, here, part);
+            if constexpr (I < QB) q[set][I] = Q::part(this->lds + q_at, q0, I, part);
+            else p[set][I - QB] = P::part(this->lds + p_at, p0, I - QB, part);
+            read_some<I + 1, UPTO>(set, p_at, q_at, part);
         }
     }
 
     // Matrix instruction M of a part and what takes its turn after it: reads of
-    // part `next` of the step at `there` into the other set, and the SHARE-th
-    // quarter of the loads that follow step s at `here`.
-    template <int SET, bool READ, int KIND, int SHARE, int M = 0>
-    __device__ __forceinline__ void part(f32x16_t (&acc)[PB][QB], W& w, W& nw, int there, int next, int s,
-                                         int here)
+    // part `next` of the step at p_to and q_to into the other set, and the
+    // SHARE-th quarter of the loads that follow step s at p_at and q_at.
+    template <int SET, int KIND, int SHARE, int M = 0>
+    __device__ __forceinline__ void part(f32x16_t (&acc)[PB][QB], W& w, W& nw, int p_to, int q_to, int next, int s,
+                                         int p_at, int q_at)
     {
         if constexpr (M < kMuls) {
             constexpr int i = M / QB, j = M % QB;
             acc[i][j] = mma32(p[SET][i], q[SET][j], acc[i][j], static_cast<const T*>(nullptr));
-            if constexpr (READ) {
-                // all reads within the first three quarters
-                constexpr int kFrom = kReads * M * 4 / (kMuls * 3), kTo = kReads * (M + 1) * 4 / (kMuls * 3);
-                read_some<(kFrom < kReads ? kFrom : kReads), (kTo < kReads ? kTo : kReads)>(SET ^ 1, there, next);
-            }
-            if constexpr (KIND != 0) {
-                constexpr int kOf = kLoads * SHARE / 4, kCount = kLoads * (SHARE + 1) / 4 - kOf;
-                load_some<kOf + kCount * M / kMuls, kOf + kCount * (M + 1) / kMuls, KIND>(w, nw, s, here);
-            }
+            // all reads within the first three quarters
+            constexpr int kFrom = kReads * M * 4 / (kMuls * 3), kTo = kReads * (M + 1) * 4 / (kMuls * 3);
+            read_some<(kFrom < kReads ? kFrom : kReads), (kTo < kReads ? kTo : kReads)>(SET ^ 1, p_to, q_to, next);
+            constexpr int kOf = kLoads * SHARE / 4, kCount = kLoads * (SHARE + 1) / 4 - kOf;
+            this->template load_some<kOf + kCount * M / kMuls, kOf + kCount * (M + 1) / kMuls, KIND>(w, nw, s, p_at,
+                                                                                                     q_at);
             __builtin_amdgcn_sched_barrier(0);
-            part<SET, READ, KIND, SHARE, M + 1>(acc, w, nw, there, next, s, here);
+            part<SET, KIND, SHARE, M + 1>(acc, w, nw, p_to, q_to, next, s, p_at, q_at);
         }
     }
 
     template <int KIND>
     __device__ __forceinline__ void step(f32x16_t (&acc)[PB][QB], W& w, W& nw, int s)
     {
-        const int before = now - 2 * kPlace < 0 ? now + (RING - 2) * kPlace : now - 2 * kPlace;
-        const int then = place(now + 2 * kPlace);
-        part<0, true, KIND, 1>(acc, w, nw, now, 1, s - 1, before);
-        part<1, true, KIND, 2>(acc, w, nw, now, 2, s - 1, before);
-        part<0, true, KIND, 3>(acc, w, nw, now, 3, s - 1, before);
-        wait_barrier<kLeft>();
-        part<1, true, KIND, 0>(acc, w, nw, then, 0, s, now);
-        now = then;
+        const int p_at = this->p_now, q_at = this->q_now;
+        const int p_old = R::p_before(p_at), q_old = R::q_before(q_at);
+        const int p_next = R::p_after(p_at), q_next = R::q_after(q_at);
+        part<0, KIND, 1>(acc, w, nw, p_at, q_at, 1, s - 1, p_old, q_old);
+        part<1, KIND, 2>(acc, w, nw, p_at, q_at, 2, s - 1, p_old, q_old);
+        part<0, KIND, 3>(acc, w, nw, p_at, q_at, 3, s - 1, p_old, q_old);
+        wait_barrier<R::kLeft>();
+        part<1, KIND, 0>(acc, w, nw, p_next, q_next, 0, s, p_at, q_at);
+        this->advance();
     }
 
-    // The first tile's first loads: what the steps before it would have sent.
     __device__ __forceinline__ void begin(W& w)
     {
-        start<0>(w);
-        load_some<0, kLoads / 4, 2>(w, w, -1, place(now + (RING - 2) * kPlace));
-        wait_barrier<kLeft + kLoads / 4>();
-        read_some<0, kReads>(0, now, 0);
-    }
-    template <int U>
-    __device__ __forceinline__ void start(W& w)
-    {
-        if constexpr (U < RING - 2) {
-            if constexpr (U % 2 == 0) all<0>(w.p, at + U * kPlace, w.step(U / 2));
-            else all<0>(w.q, at + U * kPlace, w.step(U / 2));
-            start<U + 1>(w);
-        }
-    }
-    template <int I, typename O>
-    __device__ __forceinline__ void all(O& o, uint32_t to, int s)
-    {
-        if constexpr (I < O::kLoads) {
-            o.template load_end<I>(to, s);
-            all<I + 1>(o, to, s);
-        }
+        R::template begin<kLoads / 4>(w);
+        read_some<0, kReads>(0, this->p_now, this->q_now, 0);
     }
 
     // A whole tile, and the first loads of the next, which prepare(nw) finds
@@ -598,7 +617,7 @@ struct Ring {
     __device__ __forceinline__ void tile(f32x16_t (&acc)[PB][QB], W& w, W& nw, Prepare prepare)
     {
         int s = 0;
-        for (; s + kAhead < w.whole; ++s) step<1>(acc, w, w, s);
+        for (; s + R::kAhead < w.whole; ++s) step<1>(acc, w, w, s);
         prepare(nw);
         for (; s < w.steps; ++s) step<2>(acc, w, nw, s);
     }
@@ -674,7 +693,7 @@ __device__ __forceinline__ void tiles(char* lds, int p0, int q0, Find find, Prep
     if constexpr (DIRECT) {
         Tile nt;
         Work<P, Q> w, nw;
-        Ring<T, P, Q, PB, QB, RING> ring(lds, p0, q0);
+        Steps<T, P, Q, PB, QB, RING> ring(lds, p0, q0);
         prepare(w, t);
         ring.begin(w);
         bool more = true;
@@ -725,6 +744,36 @@ __device__ __forceinline__ uint2 pack4(float a, float b, float c, float d)
 // col .. of `cols`.  A lane holds runs of 4 columns, 4 (l / 32) + 8 i; lanes
 // l and l + 32 hold the two halves of the same row and trade them, so that
 // each stores runs of 8.
+template <typename T, typename F>
+__device__ __forceinline__ void put_block(const f32x16_t& v, F chunk_at)
+{
+    // chunk_at(c): where the 8 columns from c on go
+    const int h = (opaque(threadIdx.x) >> 5) & 1;
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        const uint2 a = pack4<T>(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        const uint2 b = pack4<T>(v[4 * i + 4], v[4 * i + 5], v[4 * i + 6], v[4 * i + 7]);
+        const auto x = __builtin_amdgcn_permlane32_swap(a.x, b.x, false, false);
+        const auto y = __builtin_amdgcn_permlane32_swap(a.y, b.y, false, false);
+        *reinterpret_cast<uint4*>(chunk_at(8 * i + 8 * h)) = make_uint4(x[0], y[0], x[1], y[1]);
+    }
+}
+// 8 columns from c on, of `cols`, of a row.
+template <typename T>
+__device__ __forceinline__ void store_chunk(const uint4& q, T* row, int64_t c, int64_t cols)
+{
+    if (c + 8 <= cols) {
+        __builtin_memcpy(row + c, &q, 16);
+    } else if (c < cols) {
+        uint64_t lo = q.x | (uint64_t)q.y << 32, hi = q.z | (uint64_t)q.w << 32;
+#pragma clang loop unroll(disable)
+        for (int64_t k = c; k < cols; ++k) {
+            row[k] = T{(uint16_t)lo};
+            lo = lo >> 16 | hi << 48;
+            hi >>= 16;
+        }
+    }
+}
 template <typename T>
 __device__ __forceinline__ void store_block(const f32x16_t& v, T* row, int64_t col, int64_t cols, bool live)
 {
@@ -735,19 +784,7 @@ __device__ __forceinline__ void store_block(const f32x16_t& v, T* row, int64_t c
         const uint2 b = pack4<T>(v[4 * i + 4], v[4 * i + 5], v[4 * i + 6], v[4 * i + 7]);
         const auto x = __builtin_amdgcn_permlane32_swap(a.x, b.x, false, false);
         const auto y = __builtin_amdgcn_permlane32_swap(a.y, b.y, false, false);
-        const uint4 q = make_uint4(x[0], y[0], x[1], y[1]);
-        const int64_t c = col + 8 * i + 8 * h;
-        if (live && c + 8 <= cols) {
-            __builtin_memcpy(row + c, &q, 16);
-        } else if (live && c < cols) {
-            uint64_t lo = q.x | (uint64_t)q.y << 32, hi = q.z | (uint64_t)q.w << 32;
-#pragma clang loop unroll(disable)
-            for (int64_t k = c; k < cols; ++k) {
-                row[k] = T{(uint16_t)lo};
-                lo = lo >> 16 | hi << 48;
-                hi >>= 16;
-            }
-        }
+        if (live) store_chunk(make_uint4(x[0], y[0], x[1], y[1]), row, col + 8 * i + 8 * h, cols);
     }
     __builtin_amdgcn_sched_barrier(0);      // one block's values at a time
 }
