@@ -279,6 +279,281 @@ void fp8_kernel(Scaled a)
     }
 }
 
+// A tile's work with its scales: where this lane's rows' scales and the
+// weights' lie (ws[1]: of the up half), and how many blocks there are.
+struct ScaledWork : Work<RowOperand<256, 512>, RowOperand<128, 512>> {
+    const char* xs;
+    const float* ws[2];
+    int blocks;
+};
+
+// Tiles of 256 outputs by 128 rows, eight wavefronts of 64 by 64 (PB x QB
+// blocks), through the ring of ep_product.h: a step is a block of 128 codes.
+//
+// A pair of matrix instructions makes a block's sum over the step, from 0; it
+// is scaled and added while the next pair runs (a lane's 16 values belong to
+// one row, so one factor does).  The operands of the next row block are read
+// meanwhile; those of the rows change, as their last pair has read them, with
+// the step.  Scales of rows are loaded like operands, 64 a wavefront, into a
+// place of its own for each of 4 steps; those of weights are scalar loads.
+template <int FORMAT, bool GLU, bool BYTES>
+struct ScaledSteps : Ring<RowOperand<256, 512>, RowOperand<128, 512>, 5> {
+    using P = RowOperand<256, 512>;
+    using Q = RowOperand<128, 512>;
+    using R = Ring<P, Q, 5>;
+    using W = ScaledWork;
+    typedef const __attribute__((address_space(4))) float* scalar_ptr;
+    static constexpr int PB = 2, QB = 2, kPairs = PB * QB, kHalves = GLU ? 2 : 1;
+    static constexpr int kScalesAt = R::kLds, kAllLds = R::kLds + 8 * 4 * 256;
+    // the first half of the loads that follow a step go out with its last row
+    // block
+    static constexpr int kFirst = R::kLoads / 2;
+
+    int p0, q0;
+    int64_t block_stride;   // bytes between a row's scales
+    Codes p[2][2], q[QB][2];
+    f32x16_t d[2];
+    uint32_t xs[QB];        // of the next step
+    float ws[kHalves];
+    float f[QB][kHalves], last;
+
+    __device__ __forceinline__ ScaledSteps(char* shared, int p_row, int q_row, const Scaled& a)
+        : R(shared), p0(p_row), q0(q_row), block_stride(a.scale_block * (BYTES ? 1 : 4)), last(0.0f)
+    {
+    }
+
+    // The scales of step s to their place: lane l those of the wavefront's row l.
+    __device__ __forceinline__ void load_scales(const W& w, const W& nw, int s)
+    {
+        const bool mine = s < w.steps;
+        const int step = mine ? s : s - w.steps, blocks = mine ? w.blocks : nw.blocks;
+        const char* from = (mine ? w.xs : nw.xs) + (step < blocks ? step : 0) * block_stride;
+        const uint32_t to = lds_address(lds) + kScalesAt + (at_wave() * 4 + (place(s, w) & 3)) * 256;
+        if constexpr (BYTES)
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, off" ::"s"(uniform((int)to)),
+                         "v"(from)
+                         : "m0");
+        else
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(uniform((int)to)),
+                         "v"(from)
+                         : "m0");
+    }
+    __device__ __forceinline__ static int at_wave() { return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6); }
+    // steps are counted through all tiles
+    int done = 0;
+    __device__ __forceinline__ int place(int s, const W&) const { return done + s; }
+
+    __device__ __forceinline__ void read_scales(const W& w, const W& nw, int s)
+    {
+        const char* from = lds + kScalesAt + (at_wave() * 4 + (place(s, w) & 3)) * 256 + (threadIdx.x & 31) * 4;
+#pragma unroll
+        for (int j = 0; j < QB; ++j) xs[j] = *reinterpret_cast<const uint32_t*>(from + j * 128);
+        const bool mine = s < w.steps;
+        const int step = mine ? s : s - w.steps;
+        const W& of = mine ? w : nw;
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) ws[h] = ((scalar_ptr)of.ws[h])[step < of.blocks ? step : 0];
+        live = step < of.blocks;
+    }
+    bool live;
+    __device__ __forceinline__ void factors()
+    {
+#pragma unroll
+        for (int j = 0; j < QB; ++j) {
+            const float x = !BYTES ? __uint_as_float(xs[j])
+                                   : __uint_as_float(xs[j] == 0 ? 0x00400000u : xs[j] << 23);
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) f[j][h] = live ? x * ws[h] : 0.0f;
+        }
+    }
+    __device__ __forceinline__ void read_p(int set, int p_at, int i)
+    {
+        p[set][0] = codes_part(lds + p_at, p0, i, 0);
+        p[set][1] = codes_part(lds + p_at, p0, i, 1);
+    }
+    __device__ __forceinline__ void read_q(int q_at, int j)
+    {
+        q[j][0] = codes_part(lds + q_at, q0, j, 0);
+        q[j][1] = codes_part(lds + q_at, q0, j, 1);
+    }
+
+    // The pair for block (N / QB, N % QB) of a step, and what takes its turn.
+    template <int KIND, int N>
+    __device__ __forceinline__ void pair(f32x16_t (&acc)[PB][QB], W& w, W& nw, int s, int p_old, int q_old, int p_next,
+                                         int q_next)
+    {
+        constexpr int i = N / QB, j = N % QB, kWas = (N + kPairs - 1) % kPairs;
+        constexpr bool kLastBlock = i == PB - 1;
+        const int p_at = p_now, q_at = q_now;
+        if constexpr (kLastBlock && j == 0) wait_barrier<R::kLeft>();
+        d[N & 1] = mma32x8<FORMAT>(p[i & 1][0], q[j][0], f32x16_t{});
+        if constexpr (j == 0 && !kLastBlock) read_p((i + 1) & 1, p_at, i + 1);
+        if constexpr (j == 0 && kLastBlock) {
+            read_scales(w, nw, s + 1);
+            read_p(0, p_next, 0);
+        }
+        d[N & 1] = mma32x8<FORMAT>(p[i & 1][1], q[j][1], d[N & 1]);
+        if constexpr (kLastBlock) {
+            if constexpr (j == 0) load_scales(w, nw, s + kQ);
+            this->template load_some<kFirst * j / QB, kFirst * (j + 1) / QB, KIND>(w, nw, s, p_at, q_at);
+        } else {
+            constexpr int kRest = R::kLoads - kFirst, kSlots = kPairs - QB;
+            this->template load_some<kFirst + kRest * N / kSlots, kFirst + kRest * (N + 1) / kSlots, KIND>(
+                w, nw, s - 1, p_old, q_old);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            acc[kWas / QB][kWas % QB][e] = __builtin_fmaf(d[(N + 1) & 1][e], last, acc[kWas / QB][kWas % QB][e]);
+        asm volatile("" : "+v"(acc[kWas / QB][kWas % QB]));     // here, not when all pairs are done
+        last = f[j][GLU ? i & 1 : 0];
+        if constexpr (kLastBlock) read_q(q_next, j);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (N + 1 < kPairs) pair<KIND, N + 1>(acc, w, nw, s, p_old, q_old, p_next, q_next);
+    }
+
+    template <int KIND>
+    __device__ __forceinline__ void step(f32x16_t (&acc)[PB][QB], W& w, W& nw, int s)
+    {
+        factors();
+        pair<KIND, 0>(acc, w, nw, s, R::p_before(p_now), R::q_before(q_now), R::p_after(p_now), R::q_after(q_now));
+        advance();
+    }
+
+    __device__ __forceinline__ void begin(W& w)
+    {
+        start<0>(w);
+        load_scales(w, w, 0);
+        load_scales(w, w, 1);
+        load_some<0, kFirst, 2>(w, w, -1, p_before(p_now), q_before(q_now));
+        wait_barrier();
+        read_scales(w, w, 0);
+        read_q(q_now, 0);
+        read_q(q_now, 1);
+        read_p(0, p_now, 0);
+        d[0] = d[1] = f32x16_t{};
+    }
+
+    template <typename Prepare>
+    __device__ __forceinline__ void tile(f32x16_t (&acc)[PB][QB], W& w, W& nw, Prepare prepare)
+    {
+        int s = 0;
+        last = 0.0f;        // nothing to add before the first pair
+        for (; s + kAhead < w.whole; ++s) step<1>(acc, w, w, s);
+        prepare(nw);
+        for (; s < w.steps; ++s) step<2>(acc, w, nw, s);
+        done += w.steps;
+        // the last pair's sum
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[PB - 1][QB - 1][e] = __builtin_fmaf(d[1][e], last, acc[PB - 1][QB - 1][e]);
+        d[1] = f32x16_t{};
+    }
+};
+
+template <typename T, int FORMAT, bool GLU, bool BYTES>
+__global__ __launch_bounds__(512)
+void fp8_tiles_kernel(Scaled a)
+{
+    using S = ScaledSteps<FORMAT, GLU, BYTES>;
+    using W = ScaledWork;
+    constexpr int BP = 256, BQ = 128, PB = S::PB, QB = S::QB;
+    __shared__ __attribute__((aligned(128))) char lds[S::kAllLds];
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int p0 = wave / 2 * 64, q0 = wave % 2 * 64;
+    const int half = a.n / 2;
+
+    struct Tile {
+        RowBlock rb;
+        int n0;
+    };
+    int i = 0;
+    const TileWalk walk = {a.tiles, a.col_tiles, a.group};
+    auto find = [&](Tile& t) {
+        int col;
+        if (!next_tile(walk, a.seg, BQ, i, t.rb, col)) return false;
+        t.n0 = col * (GLU ? BP / 2 : BP);
+        return true;
+    };
+    auto prepare = [&](W& w, const Tile& t) {
+        w.p.init(a.w + ((int64_t)t.rb.expert * a.n + t.n0) * a.k, a.k, [&](int r) {
+            int n;
+            if constexpr (GLU) {
+                n = r / 64 * 32 + (r & 31);
+                n = (t.n0 + n < half ? n : half - 1 - t.n0) + (r & 32 ? half : 0);
+            } else {
+                n = t.n0 + r < a.n ? r : a.n - 1 - t.n0;
+            }
+            return (uint32_t)n * (uint32_t)a.k;
+        });
+        auto x_row = [&](int i) {
+            int r = i < t.rb.rows ? i : 0;
+            if (a.src != nullptr) {
+                r = a.src[t.rb.first + r];
+                if (r < 0 || r >= a.x_rows) r = 0;
+            }
+            return r;
+        };
+        const int64_t x0 = a.src != nullptr ? 0 : t.rb.first;
+        w.q.init(a.x + x0 * a.ld_x, a.k, [&](int i) { return (uint32_t)x_row(i) * (uint32_t)a.ld_x; });
+        w.xs = static_cast<const char*>(a.x_scales) +
+               (x0 + x_row(q0 + (opaque(threadIdx.x) & 63))) * a.scale_row * (BYTES ? 1 : 4);
+        const float* ws = a.w_scales + (int64_t)t.rb.expert * a.n_blocks * a.k_blocks;
+        const int b = GLU ? t.n0 / 128 : (t.n0 + p0) / 128;
+        w.ws[0] = ws + (int64_t)(b < a.n_blocks ? b : a.n_blocks - 1) * a.k_blocks;
+        w.ws[1] = GLU ? ws + (int64_t)((half + t.n0) / 128) * a.k_blocks : w.ws[0];
+        w.blocks = a.k_blocks;
+        w.steps = a.k_blocks > S::kFewestSteps ? a.k_blocks : S::kFewestSteps;
+        w.whole = a.k / 128;
+        w.turn = 0;
+    };
+    T* out = static_cast<T*>(a.out);
+    auto store = [&](const f32x16_t (&acc)[PB][QB], const Tile& t) {
+        const int lane = opaque(threadIdx.x) & 63;
+#pragma unroll
+        for (int j = 0; j < QB; ++j) {
+            const int r = q0 + j * 32 + (lane & 31);
+            const bool live = r < t.rb.rows;
+            T* row = out + (t.rb.first + (live ? r : 0)) * a.ld_out;
+            if constexpr (GLU) {
+#pragma unroll
+                for (int i = 0; i < PB; i += 2) {
+                    f32x16_t f;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) f[e] = silu_of(acc[i][j][e]) * acc[i + 1][j][e];
+                    store_block(f, row, t.n0 + (p0 + i * 32) / 2, half, live);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < PB; ++i) store_block(acc[i][j], row, t.n0 + p0 + i * 32, a.n, live);
+            }
+        }
+    };
+
+    Tile t, nt;
+    if (!find(t)) return;
+    W w, nw;
+    f32x16_t acc[PB][QB];
+    S ring(lds, p0, q0, a);
+    prepare(w, t);
+    ring.begin(w);
+    bool more = true;
+    clear(acc);
+    for (;;) {
+        ring.tile(acc, w, nw, [&](W& next) {
+            nt = t;
+            Tile found;
+            more = find(found);
+            if (more) nt = found;
+            prepare(next, nt);
+        });
+        store(acc, t);
+        if (!more) break;
+        clear(acc);
+        w = nw;
+        t = nt;
+    }
+    wait_barrier();
+}
+
 // Few rows an expert: as ep_expert_few.hip, a step of 128 codes at a time.
 // SPLIT as above, for halves that are not whole blocks of 16 outputs: a block
 // of 16 then may lie in two scales.
@@ -488,8 +763,15 @@ hipError_t sized(const ExpertFp8Args& a, hipStream_t stream)
     const int64_t reach = (a.src != nullptr ? a.x_rows : 256) * a.ld_x, gate = GLU ? (a.n / 2 + 256) * (int64_t)a.k : 0;
     if ((GLU && a.n / 2 % 128 != 0) || reach >= (int64_t)1 << 32 || gate >= (int64_t)1 << 32)
         return launch<T, FORMAT, GLU, GLU, uint64_t, 128, 128, 2, 2>(a, stream);
-    if (each >= 192) return launch<T, FORMAT, GLU, false, uint32_t, 256, 256, 2, 4>(a, stream);
-    return launch<T, FORMAT, GLU, false, uint32_t, 128, 128, 2, 2>(a, stream);
+    Scaled p = scaled(a);
+    p.col_tiles = GLU ? (a.n / 2 + 127) / 128 : (a.n + 255) / 256;
+    p.tiles = tile_count(max_row_blocks(a.num_rows, a.num_experts, 128), p.group, p.col_tiles);
+    const dim3 grid(tile_grid(p.tiles, 1));
+    if (a.scale_bytes)
+        hipLaunchKernelGGL((fp8_tiles_kernel<T, FORMAT, GLU, true>), grid, dim3(512), 0, stream, p);
+    else
+        hipLaunchKernelGGL((fp8_tiles_kernel<T, FORMAT, GLU, false>), grid, dim3(512), 0, stream, p);
+    return hipGetLastError();
 }
 
 template <typename T>
