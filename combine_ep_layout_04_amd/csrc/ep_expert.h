@@ -90,4 +90,20 @@ struct ExpertFp8Args {
 hipError_t launch_expert_fp8(int dtype, const ExpertFp8Args& a, hipStream_t stream);
 int64_t expert_fp8_max_blocks(const ExpertFp8Args& a);
 
+// Whether the kernels for few rows take a call, or the tiles.  The former read
+// the weights once per 16 or 32 rows, in one workgroup per 32 to 64 of their
+// rows; the latter hold 256 of them, so they need as many tiles to fill the
+// chip.  us, few against tiles: 64 experts 2048 -> 2x1408 (704 tiles), 8 rows
+// an expert 132 to 136, 16 rows 158 to 138, 32 rows 180 to 142, 8-bit 68 to 76,
+// 91 to 77, 139 to 80; 16 experts 2048 -> 4096 (256 tiles) 12 rows 59 to 51;
+// 8 experts (128 tiles) 24 rows 38 to 45, 32 rows 41 to 46; 1 expert (16 tiles)
+// 64 rows 10.7 to 24.5, 128 rows 17.6 to 25.0; 2 experts (32 tiles) 64 rows
+// 22.0 to 24.7, 128 rows 35.8 to 25.8.
+inline bool few_rows(int64_t num_rows, int num_experts, int n)
+{
+    const int64_t hold = num_rows < num_experts ? num_rows : num_experts;  // experts that can have a row
+    const int64_t tiles = hold * n / 256;
+    return num_rows / hold <= (tiles > 128 ? 8 : tiles > 32 ? 32 : 64);
+}
+
 }  // namespace ep

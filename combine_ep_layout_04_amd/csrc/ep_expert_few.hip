@@ -7,6 +7,10 @@
 // straight into the matrix instruction's operand (a lane 16 bytes of its
 // row), and are joined through LDS in a fixed order: the few outputs of a
 // single token still fill the chip, and results do not depend on timing.
+//
+// 512 rows of 64 experts, 2048 -> 7168, 1.88 GB of weights: 319 us, 5.9 TB/s
+// (a large copy moves 6.6).  One token through 4 experts, gated 2048 -> 2x1408,
+// 46 MB: 12 us, of which a launch and the first loads' way are the most.
 #include "ep_expert.h"
 #include "ep_product.h"
 
@@ -180,8 +184,16 @@ template <typename T, bool GLU>
 hipError_t sized(const ExpertArgs& a, hipStream_t stream)
 {
     const int64_t hold = a.num_rows < a.num_experts ? a.num_rows : a.num_experts;
-    if (a.num_rows / hold <= 16)
-        return launch<T, GLU, 2, 1, 8>(a, max_row_blocks(a.num_rows, a.num_experts, 16), stream);
+    const int64_t items = max_row_blocks(a.num_rows, a.num_experts, 16);
+    if (a.num_rows / hold <= 16) {
+        // us, 64 outputs a workgroup against 32 with twice the wavefronts: 64
+        // experts 2048 -> 2x1408, 1 row an expert 88.9 to 88.1, 8 rows 132 to
+        // 142; one row, 4096 -> 14336 (896 blocks of 16 x 16 outputs) 26.7 to
+        // 29.6, 4096 -> 4096 (256 blocks) 18.2 to 12.3
+        if (items * ((a.n + 15) / 16) >= 768) return launch<T, GLU, 4, 1, 4>(a, items, stream);
+        return launch<T, GLU, 2, 1, 8>(a, items, stream);
+    }
+    // 24 rows of one expert, 4096 -> 4096: 16.8 us, with 64 outputs 24.2
     return launch<T, GLU, 2, 2, 4>(a, max_row_blocks(a.num_rows, a.num_experts, 32), stream);
 }
 
