@@ -189,8 +189,9 @@ hipError_t sized(const ExpertArgs& a, hipStream_t stream)
         // us, 64 outputs a workgroup against 32 with twice the wavefronts: 64
         // experts 2048 -> 2x1408, 1 row an expert 88.9 to 88.1, 8 rows 132 to
         // 142; one row, 4096 -> 14336 (896 blocks of 16 x 16 outputs) 26.7 to
-        // 29.6, 4096 -> 4096 (256 blocks) 18.2 to 12.3
-        if (items * ((a.n + 15) / 16) >= 768) return launch<T, GLU, 4, 1, 4>(a, items, stream);
+        // 29.6, 4096 -> 4096 (256 blocks) 18.2 to 12.3; 4 rows of 4 experts, 2048 ->
+        // 2x1408 (704 blocks) 12.1 to 13.5
+        if (items * ((a.n + 15) / 16) >= 640) return launch<T, GLU, 4, 1, 4>(a, items, stream);
         return launch<T, GLU, 2, 1, 8>(a, items, stream);
     }
     // 24 rows of one expert, 4096 -> 4096: 16.8 us, with 64 outputs 24.2

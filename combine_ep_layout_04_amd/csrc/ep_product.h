@@ -28,7 +28,7 @@
 // 1024 products.  32768 rows of 32 experts, 7168 -> 4096 gated: 1630 us, 1.18
 // PFLOP/s, and 1.33 with the rows that fill the last tiles of the experts up;
 // the clock falls to about 1.65 GHz under this load, and the matrix cores are
-// busy 73 to 77% of the cycles.  Slower at this size: 8 wavefronts and two
+// busy 82% of the cycles.  Slower at this size: 8 wavefronts and two
 // stages 1990 us, steps of 64 bytes 1877 (twice the requests to L2), all loads
 // of a step in one go 1987, tiles of 128 x 128 2372.  Within 2%: 2, 4, 8 or 16
 // row blocks taken together, a workgroup per tile in place of ones that stay.
