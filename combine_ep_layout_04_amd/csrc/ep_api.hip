@@ -1367,6 +1367,10 @@ static ep_status_t expert_backward(const void* grad_out, int dtype, int64_t ld_g
     if (num_rows > 0 && grad_there && !gated) a.grad_copy = work;
     if (num_rows > 0 && lays_out_x(in_features, src != nullptr))
         a.x_copy = work + (grad_there ? num_rows * expert_workspace_ld(out_features) * 2 : 0);
+    // counted as the other calls' rows are: 16-byte vectors, 256 a workgroup
+    if (num_rows * (expert_workspace_ld(out_features > in_features ? out_features : in_features) / 8) / 256 >=
+        INT32_MAX)
+        return fail(EP_UNSUPPORTED, "the gradients need more than 2^31 workgroups");
     if (gated) {
         a.grad = workspace;
         a.ld_grad = expert_workspace_ld(out_features);
