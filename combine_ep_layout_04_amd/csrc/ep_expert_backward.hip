@@ -13,7 +13,7 @@
 // (ColOperand), so nothing is transposed in memory.  Sums are fp32 in a fixed
 // order, no atomics.
 //
-// 32768 rows of 32 experts, 7168 -> 4096 gated, bf16: 3740 us, 1.03 PFLOP/s:
+// 32768 rows of 32 experts, 7168 -> 4096 gated, bf16: 3770 us, 1.02 PFLOP/s:
 // the activation's gradient 105 to 120, the rows' 1650 (matrix cores busy 78% of
 // the cycles), the weights' 2130 (53%: both operands by transposing reads of 8
 // bytes, and 13% for the stores, 1.9 GB of which one covers 16 bytes of a line).

@@ -17,9 +17,9 @@
 // few rows the time is that of the weights' bytes, so there the codes are
 // widened to bf16, exactly, and nothing is dropped.
 //
-// 32768 rows of 32 experts, gated 7168 -> 4096: 1163 us, 1.65 PFLOP/s; bound by
-// the vector instructions that scale a block's sum (16 fma for 2 matrix
-// instructions of 16 passes) beside the matrix cores.  512 rows of 256 experts,
+// 32768 rows of 32 experts, gated 7168 -> 4096: 1175 us, 1.64 PFLOP/s; the
+// matrix cores are busy 47% of the cycles, the vector units, which scale each
+// block's sum (16 multiply-adds for 2 matrix instructions), 42%.  512 rows of 256 experts,
 // 2048 -> 7168: 516 us, 6.2 TB/s of weights read.  One token through 8 experts,
 // gated 7168 -> 4096: 44 us, 5.3 TB/s.
 //

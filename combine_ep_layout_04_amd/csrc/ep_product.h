@@ -25,8 +25,8 @@
 //
 // Many rows are bound by the matrix cores: 256 x 256 results by 4 wavefronts
 // of 128 x 128, which is what the registers hold, take 16 bytes from LDS per
-// 1024 products.  32768 rows of 32 experts, 7168 -> 4096 gated: 1630 us, 1.18
-// PFLOP/s, and 1.33 with the rows that fill the last tiles of the experts up;
+// 1024 products.  32768 rows of 32 experts, 7168 -> 4096 gated: 1670 us, 1.15
+// PFLOP/s, and 1.30 with the rows that fill the last tiles of the experts up;
 // the clock falls to about 1.65 GHz under this load, and the matrix cores are
 // busy 82% of the cycles.  Slower at this size: 8 wavefronts and two
 // stages 1990 us, steps of 64 bytes 1877 (twice the requests to L2), all loads

@@ -1668,7 +1668,10 @@ def ep_expert_matmul_fp8(x: torch.Tensor, x_scales: torch.Tensor, weights: torch
     column-major ones); ``weights`` uint8 [E, N, K] E4M3 codes;
     ``weight_scales`` fp32 [E, ceil(N / 128), ceil(K / 128)].  The rest as
     ep_expert_matmul.  Returns out [rows, N] (N/2 if gated) in ``dtype``
-    (bfloat16 or float16), outside autograd and without a backward call."""
+    (bfloat16 or float16), outside autograd and without a backward call.
+
+    Sums are fp32; with more than a few rows per expert, of each 8 neighbouring
+    products what lies 2^-13 below the largest is dropped."""
     if fmt not in _FORMATS:
         raise ValueError(f"unknown fmt {fmt!r} (e4m3 or e5m2)")
     if not isinstance(x, torch.Tensor) or x.dtype != torch.uint8:
