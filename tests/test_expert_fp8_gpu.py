@@ -30,6 +30,10 @@ CASES = [
     (260, 3, 272, 500, "e5m2", "fp32", True, False, "fp16", False, 1),
     (500, 1, 1040, 768, "e4m3", "ue8m0", False, False, "bf16", False, 1),
     (220, 2, 256, 202, "e4m3", "fp32", False, True, "bf16", False, 1),
+    (6, 40, 272, 1030, "e5m2", "fp32", True, False, "fp16", True, 1),      # many experts: few rows, tiles from 9 on
+    (14, 16, 272, 2560, "e4m3", "fp32", False, True, "bf16", True, 1),
+    (20, 40, 144, 1000, "e4m3", "ue8m0", False, False, "fp16", False, 1),
+    (64, 1, 528, 300, "e4m3", "fp32", False, True, "bf16", False, 1),      # one expert: few rows up to 64
     (20, 4, 128, 64, "e4m3", "fp32", False, True, "bf16", False, 32),
     (200, 4, 128, 256, "e4m3", "fp32", False, True, "bf16", True, 128),
 ]
@@ -103,7 +107,8 @@ def test_product(case):
         w = vw[e] * ws[e].astype(np.float64).repeat(128, 0)[:N].repeat(128, 1)[:, :K]
         xe = x[a:b] if src is None else x[src[a:b]]
         ref, err = product(xe, w)
-        if R // min(R, E) > 32:
+        # the tiles: with many of them from 9 rows an expert on, else from 33
+        if R // min(R, E) > (8 if min(R, E) * N // 256 > 128 else 32):
             err += aligned(xe, w)
         if gated:
             ref, err = glu(ref, err)

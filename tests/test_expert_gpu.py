@@ -37,6 +37,14 @@ CASES = [
     (300, 2, 320, 512, "bf16", True, 0, 0, 1),
     (257, 3, 72, 258, "fp16", False, 8, 0, 1),
     (700, 1, 1000, 770, "bf16", False, 0, 0, 1),
+    # few rows of many experts: 64 outputs a workgroup, and tiles from 9 rows on
+    (6, 40, 200, 1026, "bf16", True, 0, 0, 1),
+    (7, 40, 135, 1030, "fp16", False, 1, 0, 1),
+    (14, 16, 264, 2560, "bf16", True, 0, 0, 1),
+    (20, 40, 131, 1000, "fp16", False, 3, 1, 1),
+    # up to 64 rows of one expert
+    (64, 1, 520, 300, "bf16", False, 0, 0, 1),
+    (47, 1, 264, 258, "fp16", True, 1, 0, 1),
     # segments with gaps
     (20, 4, 96, 48, "bf16", False, 0, 0, 32),
     (100, 4, 96, 48, "bf16", True, 0, 0, 64),
