@@ -274,9 +274,11 @@ unsigned flat_grid(int64_t units)
 
 // Both halves' gradients, a row's units of 8 outputs per thread.  Memory
 // bound: reads 3, writes 2 values an output; 32768 rows of 2048 outputs 120 us,
-// 5.6 TB/s.  d is rounded to 16 bits, the
-// type the matrix cores take; it costs half a step relative to each term of
-// the sums that follow.
+// 5.6 TB/s.  d is rounded to 16 bits, the type the matrix cores take: half a
+// step relative to each term of the sums that follow, so that gradients of
+// bf16 are off by 0.0024 (root of the mean square, relative) where one rounding
+// of the result alone is 0.0017.  d in two parts of 16 bits would double the
+// matrix work of both products, which is their time.
 template <typename T>
 __global__ __launch_bounds__(256)
 void glu_backward_kernel(const T* __restrict__ grad, int64_t ld_grad, const T* __restrict__ pre, int64_t ld_pre,
