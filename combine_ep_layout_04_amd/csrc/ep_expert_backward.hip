@@ -162,7 +162,7 @@ void weight_grad_kernel(WeightGrad<T> a)
         return true;
     };
     auto prepare = [&](Work<P, Q>& w, const Tile& t) {
-        const int steps = (t.rb.rows + 63) / 64;
+        const int steps = blocks_of(t.rb.rows, 64);
         w.p.init(reinterpret_cast<const char*>(a.x + t.rb.first * a.ld_x), a.ld_x * 2, t.rb.rows, t.k0, a.k);
         w.q.init(reinterpret_cast<const char*>(a.grad + t.rb.first * a.ld_grad), a.ld_grad * 2, t.rb.rows, t.n0, a.n);
         w.steps = DIRECT && steps < R::kFewestSteps ? R::kFewestSteps : steps;
@@ -210,7 +210,7 @@ void weight_grad_short_kernel(WeightGrad<T> a)
         p.init(reinterpret_cast<const char*>(a.x + rb.first * a.ld_x), a.ld_x * 2, rb.rows, k0, a.k);
         q.init(reinterpret_cast<const char*>(a.grad + rb.first * a.ld_grad), a.ld_grad * 2, rb.rows, n0, a.n);
         const uint32_t to = lds_address(lds) + wave * 1024;
-        const int steps = (rb.rows + 63) / 64;
+        const int steps = blocks_of(rb.rows, 64);
         for (int s = 0; s < steps; ++s) {
             if (s > 0) wait_barrier();
             load_operand<0>(p, to, s);

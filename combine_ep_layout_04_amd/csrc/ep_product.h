@@ -37,6 +37,7 @@
 
 #include <type_traits>
 
+#include "ep_count.h"
 #include "ep_device.h"
 #include "ep_types.h"
 
@@ -110,7 +111,7 @@ __device__ __forceinline__ RowBlock find_rows(const Segments& s, int TM, int ite
     RowBlock b = {-1, 0, 0};
     if (s.offsets == nullptr) {
         const int64_t first = (int64_t)item * TM;
-        b.first = (s.num_rows + TM - 1) / TM;
+        b.first = blocks_of(s.num_rows, TM);
         if (first >= s.num_rows) return b;
         b.expert = 0;
         b.first = (int)first;
@@ -134,7 +135,7 @@ __device__ __forceinline__ RowBlock find_rows(const Segments& s, int TM, int ite
         int mine = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            blocks[i] = n[i] > 0 ? (n[i] + TM - 1) / TM : 0;
+            blocks[i] = blocks_of(n[i], TM);
             mine += blocks[i];
         }
         const int upto = done + lanes_upto(mine);
@@ -163,13 +164,6 @@ __device__ __forceinline__ RowBlock find_rows(const Segments& s, int TM, int ite
     if (b.expert < 0) b.first = done;
     else bound_rows(b, s.num_rows);
     return b;
-}
-
-// Blocks of TM rows there can be at most: one for every full block of rows
-// and a part of one for every expert that holds rows.
-inline int64_t max_row_blocks(int64_t num_rows, int num_experts, int TM)
-{
-    return num_rows / TM + (num_rows < num_experts ? num_rows : num_experts);
 }
 
 // Workgroup b runs on XCD b % 8.  Each XCD takes runs of kRun tiles, which
@@ -411,7 +405,7 @@ struct ColOperand {
     __device__ __forceinline__ void fetch(uint4 (&v)[kLoads], int s) const
     {
         const char* from = base + (int64_t)s * 64 * ld;
-        if (inside && s * 64 + 64 <= rows) {        // no branch between the loads
+        if (inside && whole_step(s, rows)) {        // no branch between the loads
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) v[i] = fetch16<T>(from + off[i], 8);
         } else {

@@ -1,0 +1,38 @@
+"""The experts' products at the ends of what a call may have."""
+
+import pytest
+import torch
+
+from combine_ep_layout_04_amd import ep
+
+from moe_util import DEV
+
+pytestmark = pytest.mark.gpu
+
+
+def small(shape, most, seed):
+    """Whole numbers up to `most`: their products' sums below are exact."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randint(-most, most + 1, shape, generator=g, device=DEV).float()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "8 bits"])
+def test_most_rows(kind):
+    """2^31 - 1 rows, all but three of them one expert's."""
+    R, first, M, K = (1 << 31) - 1, 3, 7, 16
+    x, w = small((M, K), 2, 1), small((2, 1, K), 1, 2)
+    table = (x.double() @ w[:, 0].double().t()).t().bfloat16()      # of 16 terms up to 2: exact
+    src = torch.arange(R, dtype=torch.int32, device=DEV).remainder_(M)
+    off = torch.tensor([0, first, R], dtype=torch.int32, device=DEV)
+    out = torch.full((R, 1), 77.0, dtype=torch.bfloat16, device=DEV)
+    if kind == "bf16":
+        ep.ep_expert_matmul(x.bfloat16(), w.bfloat16(), off, src=src, out=out)
+    else:
+        codes = [t.to(torch.float8_e4m3fn).view(torch.uint8) for t in (x, w)]
+        ep.ep_expert_matmul_fp8(codes[0], torch.ones(M, 1, device=DEV), codes[1], torch.ones(2, 1, 1, device=DEV),
+                                off, src=src, out=out)
+    assert torch.equal(out[:first, 0], table[0][src[:first].long()])
+    step = 1 << 28
+    for a in range(first, R, step):
+        b = min(a + step, R)
+        assert torch.equal(out[a:b, 0], table[1].index_select(0, src[a:b])), a
