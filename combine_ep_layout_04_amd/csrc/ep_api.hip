@@ -1453,8 +1453,8 @@ ep_status_t ep_expert_matmul_fp8(const void* x, int x_format, int64_t ld_x, int6
                                  scale_format == EP_SCALE_UE8M0, scale_row_stride, scale_block_stride,
                                  weights, weight_scales, num_experts, out_features, in_features,
                                  offsets, counts, num_rows, gated != 0, out, ld_out};
-    if (ep::expert_fp8_max_blocks(a) > INT32_MAX)
-        return fail(EP_UNSUPPORTED, "the product needs more than 2^31 workgroups");
+    if (!ep::expert_fp8_fits(a))
+        return fail(EP_UNSUPPORTED, "the product needs more workgroups or threads than a launch can have");
     return from_hip(ep::launch_expert_fp8(out_dtype, a, static_cast<hipStream_t>(stream)),
                     "ep_expert_matmul_fp8 launch");
 }

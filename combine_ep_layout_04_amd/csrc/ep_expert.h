@@ -88,7 +88,8 @@ struct ExpertFp8Args {
     int64_t ld_out;
 };
 hipError_t launch_expert_fp8(int dtype, const ExpertFp8Args& a, hipStream_t stream);
-int64_t expert_fp8_max_blocks(const ExpertFp8Args& a);
+// Whether a launch can hold the call's workgroups and threads (else it is refused).
+bool expert_fp8_fits(const ExpertFp8Args& a);
 
 // Whether the kernels for few rows take a call, or the tiles.  The former read
 // the weights once per 16 or 32 rows, in one workgroup per 32 to 64 of their

@@ -353,7 +353,7 @@ hipError_t launch_weights_short(const ExpertBackwardArgs& a, hipStream_t stream)
                        a.n, a.k, {a.offsets, a.counts, a.num_experts, (int)a.num_rows},
                        a.grad_w, (a.k + 127) / 128, (a.n + 127) / 128, 0};
     p.tiles = (int64_t)a.num_experts * p.k_tiles * p.n_tiles;
-    hipLaunchKernelGGL((weight_grad_short_kernel<T, O>), dim3(tile_grid(p.tiles, INT32_MAX / 8192)), dim3(256), 0,
+    hipLaunchKernelGGL((weight_grad_short_kernel<T, O>), dim3((unsigned)((p.tiles + 255) / 256 * 256)), dim3(256), 0,
                        stream, p);
     return hipGetLastError();
 }
@@ -398,8 +398,10 @@ hipError_t weights_sized(const ExpertBackwardArgs& a, hipStream_t stream)
                         a.ld_grad % 8 == 0 && in_reach(64 * a.ld_x) && in_reach(64 * a.ld_grad) && !off16(a.x) &&
                         !off16(a.grad);
     if (!direct) return launch_weights<T, O, false, 128, 128, 2, 2, 4>(a, stream);
-    // few rows an expert: the time of writing, else that of multiplying
-    if (a.num_rows / a.num_experts < 400) return launch_weights_short<T, O>(a, stream);
+    // few rows an expert: the time of writing, else that of multiplying; a
+    // workgroup per tile, as long as a launch can have their threads (2^32)
+    const int64_t tiles = (int64_t)a.num_experts * ((a.n + 127) / 128) * ((a.k + 127) / 128);
+    if (a.num_rows / a.num_experts < 400 && tiles < (1 << 24) - 256) return launch_weights_short<T, O>(a, stream);
     return launch_weights<T, O, true, 256, 256, 2, 2, 5>(a, stream);
 }
 

@@ -41,6 +41,7 @@ struct Few {
     T* pre;
     int64_t ld_pre;
     int units, k_tiles;
+    unsigned first_block;   // of this launch
 };
 
 // With the gated activation the RT row blocks are RT / 2 of the gate half,
@@ -51,8 +52,9 @@ void few_kernel(Few<T> a)
 {
     extern __shared__ f32x4_t part[];       // [wave][RT][CT][64]
     constexpr int kHalves = GLU ? 2 : 1, kBlocks = RT / kHalves;
-    const int unit = blockIdx.x % a.units;
-    const RowBlock it = find_rows(a.seg, CT * 16, (int)(blockIdx.x / a.units));
+    const unsigned block = a.first_block + blockIdx.x, units = a.units;
+    const int unit = (int)(block % units);
+    const RowBlock it = find_rows(a.seg, CT * 16, (int)(block / units));
     if (it.rows <= 0) return;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -172,11 +174,16 @@ hipError_t launch(const ExpertArgs& a, int64_t items, hipStream_t stream)
     const int units = ((half_n + 15) / 16 + kBlocks - 1) / kBlocks;
     const int k_tiles = (a.k + 127) / 128;
     const int waves = WAVES < k_tiles ? WAVES : k_tiles;
-    const Few<T> f = {static_cast<const T*>(a.x), a.ld_x, a.x_rows, a.src, static_cast<const T*>(a.w), a.n, a.k,
+    Few<T> f = {static_cast<const T*>(a.x), a.ld_x, a.x_rows, a.src, static_cast<const T*>(a.w), a.n, a.k,
                       half_n, {a.offsets, a.counts, a.num_experts, (int)a.num_rows},
-                      static_cast<T*>(a.out), a.ld_out, static_cast<T*>(a.pre), a.ld_pre, units, k_tiles};
-    hipLaunchKernelGGL((few_kernel<T, GLU, RT, CT, WAVES>), dim3((unsigned)(items * units)), dim3(waves * 64),
-                       (size_t)waves * RT * CT * 1024, stream, f);
+                      static_cast<T*>(a.out), a.ld_out, static_cast<T*>(a.pre), a.ld_pre, units, k_tiles, 0};
+    const int64_t blocks = items * units;
+    for (int64_t first = 0; first < blocks; first += kMostBlocks) {
+        f.first_block = (unsigned)first;
+        const int64_t count = blocks - first < kMostBlocks ? blocks - first : kMostBlocks;
+        hipLaunchKernelGGL((few_kernel<T, GLU, RT, CT, WAVES>), dim3((unsigned)count), dim3(waves * 64),
+                           (size_t)waves * RT * CT * 1024, stream, f);
+    }
     return hipGetLastError();
 }
 

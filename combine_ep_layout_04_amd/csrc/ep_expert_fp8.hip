@@ -99,6 +99,7 @@ struct Scaled {
     int64_t ld_out;
     int col_tiles, group;
     int64_t tiles;
+    unsigned first_block;   // of this launch, few rows
 };
 
 // A scale as it lies in memory, and its value: 2^(byte - 127).
@@ -571,8 +572,9 @@ void fp8_few_kernel(Scaled a)
 {
     extern __shared__ f32x4_t part[];       // [wave][RT][CT][64]
     constexpr int kHalves = GLU ? 2 : 1, kBlocks = RT / kHalves;
-    const int unit = blockIdx.x % a.col_tiles;
-    const RowBlock it = find_rows(a.seg, CT * 16, (int)(blockIdx.x / a.col_tiles));
+    const unsigned block = a.first_block + blockIdx.x, units = a.col_tiles;
+    const int unit = (int)(block % units);
+    const RowBlock it = find_rows(a.seg, CT * 16, (int)(block / units));
     if (it.rows <= 0) return;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -719,7 +721,21 @@ Scaled scaled(const ExpertFp8Args& a)
     return Scaled{static_cast<const char*>(a.x), a.ld_x, a.x_rows, a.src, a.x_scales, a.scale_bytes,
                   a.scale_row, a.scale_block, static_cast<const char*>(a.w), a.w_scales, a.n, a.k,
                   (a.n + 127) / 128, (a.k + 127) / 128,
-                  {a.offsets, a.counts, a.num_experts, (int)a.num_rows}, a.out, a.ld_out, 0, 8, 0};
+                  {a.offsets, a.counts, a.num_experts, (int)a.num_rows}, a.out, a.ld_out, 0, 8, 0, 0};
+}
+
+// Rows that 32-bit offsets do not reach, or two scales a tile: fp8_kernel.
+bool general(const ExpertFp8Args& a)
+{
+    const int64_t reach = (a.src != nullptr ? a.x_rows : 256) * a.ld_x;
+    const int64_t gate = a.gated ? (a.n / 2 + 256) * (int64_t)a.k : 0;
+    return (a.gated && a.n / 2 % 128 != 0) || reach >= (int64_t)1 << 32 || gate >= (int64_t)1 << 32;
+}
+// Workgroups of fp8_kernel, each of 256 threads.
+int64_t general_blocks(const ExpertFp8Args& a)
+{
+    const int cols = a.gated ? (a.n / 2 + 63) / 64 : (a.n + 127) / 128;
+    return (tile_count(max_row_blocks(a.num_rows, a.num_experts, 128), 8, cols) + 255) / 256 * 256;
 }
 
 template <typename T, int FORMAT, bool GLU, bool SPLIT, typename OFF, int BP, int BQ, int WP, int WQ>
@@ -730,7 +746,7 @@ hipError_t launch(const ExpertFp8Args& a, hipStream_t stream)
     p.col_tiles = ((GLU ? a.n / 2 : a.n) + kCols - 1) / kCols;
     p.tiles = tile_count(max_row_blocks(a.num_rows, a.num_experts, BQ), p.group, p.col_tiles);
     hipLaunchKernelGGL((fp8_kernel<T, FORMAT, GLU, SPLIT, OFF, BP, BQ, WP, WQ>),
-                       dim3((unsigned)((p.tiles + 255) / 256 * 256)), dim3(WP * WQ * 64), 0, stream, p);
+                       dim3((unsigned)general_blocks(a)), dim3(WP * WQ * 64), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -742,8 +758,13 @@ hipError_t launch_few(const ExpertFp8Args& a, hipStream_t stream)
     p.col_tiles = (((GLU ? a.n / 2 : a.n) + 15) / 16 + kBlocks - 1) / kBlocks;
     const int waves = WAVES < p.k_blocks ? WAVES : p.k_blocks;
     const int64_t items = max_row_blocks(a.num_rows, a.num_experts, 16 * CT);
-    hipLaunchKernelGGL((fp8_few_kernel<T, FORMAT, GLU, SPLIT, RT, CT, WAVES>), dim3((unsigned)(items * p.col_tiles)),
-                       dim3(waves * 64), (size_t)waves * RT * CT * 1024, stream, p);
+    const int64_t blocks = items * p.col_tiles;
+    for (int64_t first = 0; first < blocks; first += kMostBlocks) {
+        p.first_block = (unsigned)first;
+        const int64_t count = blocks - first < kMostBlocks ? blocks - first : kMostBlocks;
+        hipLaunchKernelGGL((fp8_few_kernel<T, FORMAT, GLU, SPLIT, RT, CT, WAVES>), dim3((unsigned)count),
+                           dim3(waves * 64), (size_t)waves * RT * CT * 1024, stream, p);
+    }
     return hipGetLastError();
 }
 
@@ -769,9 +790,7 @@ hipError_t sized(const ExpertFp8Args& a, hipStream_t stream)
         if (GLU && a.n / 2 % 16 != 0) return few_sized<T, FORMAT, GLU, GLU>(a, stream);
         return few_sized<T, FORMAT, GLU, false>(a, stream);
     }
-    // rows that 32-bit offsets do not reach, or two scales a tile: the general form
-    const int64_t reach = (a.src != nullptr ? a.x_rows : 256) * a.ld_x, gate = GLU ? (a.n / 2 + 256) * (int64_t)a.k : 0;
-    if ((GLU && a.n / 2 % 128 != 0) || reach >= (int64_t)1 << 32 || gate >= (int64_t)1 << 32)
+    if (general(a))
         return launch<T, FORMAT, GLU, GLU, uint64_t, 128, 128, 2, 2>(a, stream);
     Scaled p = scaled(a);
     p.col_tiles = GLU ? (a.n / 2 + 127) / 128 : (a.n + 255) / 256;
@@ -799,11 +818,11 @@ hipError_t launch_expert_fp8(int dtype, const ExpertFp8Args& a, hipStream_t stre
     return dtype == 0 ? typed<Bf16>(a, stream) : typed<Fp16>(a, stream);
 }
 
-int64_t expert_fp8_max_blocks(const ExpertFp8Args& a)
+bool expert_fp8_fits(const ExpertFp8Args& a)
 {
-    const int64_t few = max_row_blocks(a.num_rows, a.num_experts, 16) * ((a.n + 31) / 32 + 1);
-    const int64_t tiles = tile_count(max_row_blocks(a.num_rows, a.num_experts, 128), 8, (a.n + 127) / 128 + 1);
-    return few > tiles ? few : tiles;
+    if (max_row_blocks(a.num_rows, a.num_experts, 16) * ((a.n + 31) / 32 + 1) > INT32_MAX) return false;
+    return a.num_rows == 0 || few_rows(a.num_rows, a.num_experts, a.n) || !general(a) ||
+           general_blocks(a) * 256 <= UINT32_MAX;
 }
 
 }  // namespace ep

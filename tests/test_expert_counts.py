@@ -1,12 +1,15 @@
 """How the experts' products count blocks and steps of rows, up to the most
 rows that a call can have: in constant expressions, where the compiler refuses
-what overflows."""
+what overflows.  And a call that no launch can hold."""
 
 import os
 import shutil
 import subprocess
 
 import pytest
+import torch
+
+from combine_ep_layout_04_amd import ep
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "combine_ep_layout_04_amd", "csrc")
@@ -50,3 +53,15 @@ def test_counts_of_rows(tmp_path):
     res = subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-fsyntax-only", f"-I{CSRC}", str(src)],
                          capture_output=True, text=True)
     assert res.returncode == 0, res.stderr
+
+
+@pytest.mark.skipif(torch.cuda.device_count() > 0, reason="fake pointers must never reach a launch on a real GPU")
+def test_more_threads_than_a_launch_can_have():
+    """8-bit gated halves that are not whole blocks of 128 take a workgroup per
+    tile: a call of 2^24 tiles is refused before any launch."""
+    fake, R = 0x100000, (1 << 31) - 1
+
+    def call(rows):
+        return ep.lib().ep_expert_matmul_fp8(fake, 1, 16, 1, fake, 0, 1, 1, fake, fake, fake, 2, 2, 16, 1, fake, None,
+                                             rows, fake, 0, 1, None)
+    assert call(R) == 2 and "threads" in ep.last_error()

@@ -36,3 +36,25 @@ def test_most_rows(kind):
     for a in range(first, R, step):
         b = min(a + step, R)
         assert torch.equal(out[a:b, 0], table[1].index_select(0, src[a:b])), a
+
+
+@pytest.mark.parametrize("kind", ["bf16", "8 bits"])
+def test_all_experts_of_the_widest_output(kind):
+    """1024 experts of 2^20 outputs, a row each: more than 2^32 threads."""
+    E, N, K = 1024, 1 << 20, 16 if kind == "8 bits" else 8
+    x = small((E, K), 2, 3)
+    some = small((61, K), 1, 4)         # weights' rows; which of them an output takes: (expert + output) % 61
+    x8 = x.to(torch.float8_e4m3fn).view(torch.uint8)
+    held = some.to(torch.float8_e4m3fn).view(torch.uint8) if kind == "8 bits" else some.bfloat16()
+    w = torch.empty(E, N, K, dtype=held.dtype, device=DEV)
+    at = torch.arange(N, device=DEV)
+    for e in range(E):
+        w[e] = held[(e + at) % 61]
+    off = torch.arange(E + 1, dtype=torch.int32, device=DEV)
+    if kind == "8 bits":
+        got = ep.ep_expert_matmul_fp8(x8, torch.ones(E, 1, device=DEV), w, torch.ones(E, N // 128, 1, device=DEV), off)
+    else:
+        got = ep.ep_expert_matmul(x.bfloat16(), w, off)
+    table = (x.double() @ some.double().t()).bfloat16()             # exact
+    for e in range(E):
+        assert torch.equal(got[e], table[e][(e + at) % 61]), e
