@@ -1351,8 +1351,9 @@ static ep_status_t expert_backward(const void* grad_out, int dtype, int64_t ld_g
             st = check_matrix(pre, ld_pre, out_features, dtype, "pre");
             if (st) return st;
         }
-        const size_t need = ep_expert_backward_workspace_size(num_rows, out_features, in_features, gated,
-                                                              src != nullptr);
+        // without grad_weights x is not read, so not laid out either
+        const size_t need = ep_expert_backward_workspace_size(num_rows, out_features, grad_weights ? in_features : 8,
+                                                              gated, grad_weights && src);
         if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need))
             return fail(EP_INVALID_ARGUMENT,
                         "workspace must be 16-byte aligned and hold %zu bytes, holds %zu", need,
@@ -1365,7 +1366,7 @@ static ep_status_t expert_backward(const void* grad_out, int dtype, int64_t ld_g
     char* const work = static_cast<char*>(workspace);
     const bool grad_there = lays_out_grad(out_features, gated);
     if (num_rows > 0 && grad_there && !gated) a.grad_copy = work;
-    if (num_rows > 0 && lays_out_x(in_features, src != nullptr))
+    if (num_rows > 0 && grad_weights && lays_out_x(in_features, src != nullptr))
         a.x_copy = work + (grad_there ? num_rows * expert_workspace_ld(out_features) * 2 : 0);
     // counted as the other calls' rows are: 16-byte vectors, 256 a workgroup
     if (num_rows * (expert_workspace_ld(out_features > in_features ? out_features : in_features) / 8) / 256 >=

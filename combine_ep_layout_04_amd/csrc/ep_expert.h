@@ -48,7 +48,7 @@ struct ExpertBackwardArgs {
     void* grad_w;           // [num_experts, n, k] or NULL
     bool wide_w;            // grad_w in fp32, else in dtype
     // where to lay rows out first, padded to 8 columns with zeros, or NULL;
-    // with src x has to be
+    // with src and grad_w x has to be
     void* grad_copy;
     void* x_copy;
 };

@@ -415,7 +415,7 @@ hipError_t backward(ExpertBackwardArgs a, hipStream_t stream)
         a.ld_grad = (a.n + 7) / 8 * 8;
         a.padded = true;
     }
-    if (a.x_copy != nullptr && a.grad_w != nullptr) {
+    if (a.x_copy != nullptr) {
         const hipError_t err = lay_out<T>(a.x, a.ld_x, a.x_rows, a.src, a.num_rows, a.k, a.x_copy, stream);
         if (err != hipSuccess) return err;
         a.x = a.x_copy;

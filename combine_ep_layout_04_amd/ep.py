@@ -1559,7 +1559,8 @@ def ep_expert_backward_workspace_size(num_rows: int, out_features: int, in_featu
                                       gated: bool = False, gathered: bool = False) -> int:
     """Bytes of the backward's workspace, of ep_expert_glu_backward with
     ``gated``, of a call with ``src`` with ``gathered`` (0 if none is needed or
-    the shape is invalid)."""
+    the shape is invalid).  A call without the weights' gradient takes those of
+    ``in_features`` 8 and no ``gathered``."""
     return int(lib().ep_expert_backward_workspace_size(int(num_rows), int(out_features), int(in_features),
                                                        int(bool(gated)), int(bool(gathered))))
 
@@ -1595,7 +1596,8 @@ def _expert_backward(grad_out, x, weights, offsets, src, counts, grad_rows, grad
             _need_on(grad_weights, "grad_weights", weights_dtype, dev)
             if tuple(grad_weights.shape) != (E, N, K):
                 raise ValueError(f"grad_weights must be {(E, N, K)}, is {tuple(grad_weights.shape)}")
-    need = ep_expert_backward_workspace_size(R, N, K, gated, src is not None)
+    # x is laid out for the weights' gradient only
+    need = ep_expert_backward_workspace_size(R, N, K if want_weights else 8, gated, want_weights and src is not None)
     if workspace is not None:
         _need_on(workspace, "workspace", torch.uint8, dev, need)
     elif need:
@@ -1621,8 +1623,8 @@ def ep_expert_matmul_backward(grad_out: torch.Tensor, x: torch.Tensor, weights: 
     False leaves one out (None).  Rows of no expert are not written.
 
     ``workspace`` (uint8, ep_expert_backward_workspace_size bytes) holds rows
-    that are gathered or padded first; torch allocates it when it is not
-    given."""
+    that are gathered or padded first, those of x for grad_weights only; torch
+    allocates it when it is not given."""
     on, N, R, ld_g, tail, grad_rows, grad_weights, workspace = _expert_backward(
         grad_out, x, weights, offsets, src, counts, grad_rows, grad_weights, want_rows, want_weights,
         weights_dtype, workspace, stream, False)

@@ -990,8 +990,9 @@ ep_status_t ep_expert_glu(const void *x, int dtype, int64_t ld_x, int64_t num_x_
  *                 the gated product's d, and rows that are laid out first: x
  *                 gathered by src, rows that are not whole 16-byte vectors.
  * At least one of grad_rows and grad_weights is given; weights may be NULL
- * without grad_rows, x without grad_weights.  Sums are fp32, in a fixed order,
- * rounded once.
+ * without grad_rows, x without grad_weights (the workspace then holds no rows
+ * of x: its size is that of in_features 8 and gathered 0).  Sums are fp32, in a
+ * fixed order, rounded once.
  * ep_expert_backward_workspace_size is host arithmetic (gated: for
  * ep_expert_glu_backward; gathered: with src); 0 for an invalid shape, and
  * where none is needed.
