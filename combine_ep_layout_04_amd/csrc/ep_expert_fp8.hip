@@ -124,16 +124,16 @@ __device__ __forceinline__ Codes codes_part(const char* lds, int row0, int b, in
                  *reinterpret_cast<const uint4*>(p + (((4 * s + 2 + h) ^ turn) << 4))};
 }
 
-// SPLIT: the gated product's halves whose second does not start with a block
-// of 128 outputs; a tile's rows of it then lie in two blocks.
-template <typename T, int FORMAT, bool GLU, bool SPLIT, typename OFF, int BP, int BQ, int WP, int WQ>
-__global__ __launch_bounds__(WP * WQ * 64)
+// Any sizes: tiles of 128 x 128, two stages.  The second of the gated product's
+// halves need not start with a block of 128 outputs: a tile's rows of it lie in
+// two blocks.
+template <typename T, int FORMAT, bool GLU>
+__global__ __launch_bounds__(256)
 void fp8_kernel(Scaled a)
 {
-    constexpr int kThreads = WP * WQ * 64;
-    constexpr int PB = BP / WP / 32, QB = BQ / WQ / 32;
-    using P = RowOperand<BP, kThreads, OFF>;
-    using Q = RowOperand<BQ, kThreads, OFF>;
+    constexpr int BP = 128, BQ = 128, WQ = 2, PB = 2, QB = 2;
+    using P = RowOperand<BP, 256, uint64_t>;
+    using Q = RowOperand<BQ, 256, uint64_t>;
     constexpr int kStage = P::kBytes + Q::kBytes;
     __shared__ __attribute__((aligned(128))) char lds[2 * kStage];
 
@@ -157,7 +157,7 @@ void fp8_kernel(Scaled a)
         } else {
             n = n0 + i < a.n ? i : a.n - 1 - n0;
         }
-        return (OFF)n * (OFF)a.k;
+        return (uint64_t)n * (uint64_t)a.k;
     });
     // a row of the tile, from the first (of all of x with src)
     auto x_row = [&](int i) {
@@ -169,25 +169,23 @@ void fp8_kernel(Scaled a)
         return r;
     };
     const int64_t x0 = a.src != nullptr ? 0 : rb.first;
-    q.init(a.x + x0 * a.ld_x, a.k, [&](int i) { return (OFF)x_row(i) * (OFF)a.ld_x; });
+    q.init(a.x + x0 * a.ld_x, a.k, [&](int i) { return (uint64_t)x_row(i) * (uint64_t)a.ld_x; });
 
     // scales: of this lane's rows, and of the tile's weights (the gate's and
-    // the up's, or the first and second 128 outputs of this wavefront's)
+    // the up's two)
     int64_t xs_at[QB];
 #pragma unroll
     for (int j = 0; j < QB; ++j) xs_at[j] = (x0 + x_row(q0 + j * 32 + (lane & 31))) * a.scale_row;
-    constexpr int kW = GLU ? (SPLIT ? 3 : 2) : 1;
+    constexpr int kW = GLU ? 3 : 1;
     const float* ws_row[kW];
     const float* ws = a.w_scales + (int64_t)rb.expert * a.n_blocks * a.k_blocks;
-    int up_bound = 0;       // SPLIT: outputs of the up half from here on take the next block
+    int up_bound = 0;       // outputs of the up half from here on take the next block
     if constexpr (GLU) {
         ws_row[0] = ws + (int64_t)(n0 / 128) * a.k_blocks;
         const int b = (half + n0) / 128;
         ws_row[1] = ws + (int64_t)b * a.k_blocks;
-        if constexpr (SPLIT) {
-            ws_row[2] = ws + (int64_t)(b + 1 < a.n_blocks ? b + 1 : b) * a.k_blocks;
-            up_bound = (b + 1) * 128 - half;
-        }
+        ws_row[2] = ws + (int64_t)(b + 1 < a.n_blocks ? b + 1 : b) * a.k_blocks;
+        up_bound = (b + 1) * 128 - half;
     } else {
         const int b = (n0 + p0) / 128;
         ws_row[0] = ws + (int64_t)(b < a.n_blocks ? b : a.n_blocks - 1) * a.k_blocks;
@@ -250,7 +248,7 @@ void fp8_kernel(Scaled a)
             for (int j = 0; j < QB; ++j) {
                 f32x16_t d = mma32x8<FORMAT>(c0, qc[j][0], f32x16_t{});
                 d = mma32x8<FORMAT>(c1, qc[j][1], d);
-                if constexpr (SPLIT) {
+                if constexpr (GLU) {
                     if (i & 1) {
                         const float f = xs[j] * wsv[1], g = xs[j] * wsv[2];
                         const int n = n0 + (p0 + (i - 1) * 32) / 2 + 4 * (lane >> 5);
@@ -260,7 +258,7 @@ void fp8_kernel(Scaled a)
                         continue;
                     }
                 }
-                const float f = xs[j] * wsv[GLU ? i & 1 : 0];
+                const float f = xs[j] * wsv[0];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[i][j][e] = __builtin_fmaf(d[e], f, acc[i][j][e]);
             }
@@ -564,8 +562,8 @@ void fp8_tiles_kernel(Scaled a)
 }
 
 // Few rows an expert: as ep_expert_few.hip, a step of 128 codes at a time.
-// SPLIT as above, for halves that are not whole blocks of 16 outputs: a block
-// of 16 then may lie in two scales.
+// SPLIT: gated halves that are not whole blocks of 16 outputs, so that a block
+// of 16 may lie in two scales.
 template <typename T, int FORMAT, bool GLU, bool SPLIT, int RT, int CT, int WAVES>
 __global__ __launch_bounds__(WAVES * 64)
 void fp8_few_kernel(Scaled a)
@@ -731,22 +729,20 @@ bool general(const ExpertFp8Args& a)
     const int64_t gate = a.gated ? (a.n / 2 + 256) * (int64_t)a.k : 0;
     return (a.gated && a.n / 2 % 128 != 0) || reach >= (int64_t)1 << 32 || gate >= (int64_t)1 << 32;
 }
+int general_cols(const ExpertFp8Args& a) { return a.gated ? (a.n / 2 + 63) / 64 : (a.n + 127) / 128; }
 // Workgroups of fp8_kernel, each of 256 threads.
 int64_t general_blocks(const ExpertFp8Args& a)
 {
-    const int cols = a.gated ? (a.n / 2 + 63) / 64 : (a.n + 127) / 128;
-    return (tile_count(max_row_blocks(a.num_rows, a.num_experts, 128), 8, cols) + 255) / 256 * 256;
+    return (tile_count(max_row_blocks(a.num_rows, a.num_experts, 128), 8, general_cols(a)) + 255) / 256 * 256;
 }
 
-template <typename T, int FORMAT, bool GLU, bool SPLIT, typename OFF, int BP, int BQ, int WP, int WQ>
+template <typename T, int FORMAT, bool GLU>
 hipError_t launch(const ExpertFp8Args& a, hipStream_t stream)
 {
     Scaled p = scaled(a);
-    constexpr int kCols = GLU ? BP / 2 : BP;
-    p.col_tiles = ((GLU ? a.n / 2 : a.n) + kCols - 1) / kCols;
-    p.tiles = tile_count(max_row_blocks(a.num_rows, a.num_experts, BQ), p.group, p.col_tiles);
-    hipLaunchKernelGGL((fp8_kernel<T, FORMAT, GLU, SPLIT, OFF, BP, BQ, WP, WQ>),
-                       dim3((unsigned)general_blocks(a)), dim3(WP * WQ * 64), 0, stream, p);
+    p.col_tiles = general_cols(a);
+    p.tiles = tile_count(max_row_blocks(a.num_rows, a.num_experts, 128), p.group, p.col_tiles);
+    hipLaunchKernelGGL((fp8_kernel<T, FORMAT, GLU>), dim3((unsigned)general_blocks(a)), dim3(256), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -790,8 +786,7 @@ hipError_t sized(const ExpertFp8Args& a, hipStream_t stream)
         if (GLU && a.n / 2 % 16 != 0) return few_sized<T, FORMAT, GLU, GLU>(a, stream);
         return few_sized<T, FORMAT, GLU, false>(a, stream);
     }
-    if (general(a))
-        return launch<T, FORMAT, GLU, GLU, uint64_t, 128, 128, 2, 2>(a, stream);
+    if (general(a)) return launch<T, FORMAT, GLU>(a, stream);
     Scaled p = scaled(a);
     p.col_tiles = GLU ? (a.n / 2 + 127) / 128 : (a.n + 255) / 256;
     p.tiles = tile_count(max_row_blocks(a.num_rows, a.num_experts, 128), p.group, p.col_tiles);

@@ -320,12 +320,11 @@ struct RowOperand {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) off[i] = off_of(t / 8 + i * kRowStep) + chunk * 16;
     }
-    // This thread's I-th chunk of step s into LDS.
+    // This thread's I-th chunk of step s into LDS (32-bit offsets).
     template <int I>
     __device__ __forceinline__ void load(uint32_t lds, int s) const
     {
-        if constexpr (sizeof(OFF) == 4) load_lds<I * THREADS * 16>(lds, base + (int64_t)s * 128, off[I]);
-        else load_lds_or_zero<I * THREADS * 16>(lds, base + (int64_t)s * 128, off[I], true);
+        load_lds<I * THREADS * 16>(lds, base + (int64_t)s * 128, off[I]);
     }
     // The same for a step that may be the last, of a reduction that is a whole
     // number of chunks.
