@@ -193,12 +193,15 @@ hipError_t sized(const ExpertArgs& a, hipStream_t stream)
     const int64_t hold = a.num_rows < a.num_experts ? a.num_rows : a.num_experts;
     const int64_t items = max_row_blocks(a.num_rows, a.num_experts, 16);
     if (a.num_rows / hold <= 16) {
-        // us, 64 outputs a workgroup against 32 with twice the wavefronts: 64
-        // experts 2048 -> 2x1408, 1 row an expert 88.9 to 88.1, 8 rows 132 to
-        // 142; one row, 4096 -> 14336 (896 blocks of 16 x 16 outputs) 26.7 to
-        // 29.6, 4096 -> 4096 (256 blocks) 18.2 to 12.3; 4 rows of 4 experts, 2048 ->
-        // 2x1408 (704 blocks) 12.1 to 13.5
-        if (items * ((a.n + 15) / 16) >= 640) return launch<T, GLU, 4, 1, 4>(a, items, stream);
+        // 32 outputs a workgroup and 8 wavefronts while there are no more than one
+        // such workgroup a CU (512 blocks of 16 x 16 outputs), else 64 and 4.  us,
+        // the former to the latter: one row, K 4096, 256 blocks 12.5 to 19.4, 384
+        // blocks 14.5 to 19.8, 512 blocks 17.9 to 20.9, 576 blocks 25.3 to 22.3, 640
+        // blocks 26.0 to 22.7, 896 blocks 28.9 to 27.2; 8 rows of 8 experts, gated, K
+        // 2048, 512 blocks 10.3 to 12.6, 640 blocks 14.4 to 13.1; 4 rows of 4
+        // experts, K 7168, 512 blocks 24.5 to 37.2, 640 blocks 38.0 to 36.9; 64
+        // experts 2048 -> 2x1408, 1 row an expert 88.1 to 88.9, 8 rows 142 to 132
+        if (items * ((a.n + 15) / 16) > 512) return launch<T, GLU, 4, 1, 4>(a, items, stream);
         return launch<T, GLU, 2, 1, 8>(a, items, stream);
     }
     // 24 rows of one expert, 4096 -> 4096: 16.8 us, with 64 outputs 24.2
