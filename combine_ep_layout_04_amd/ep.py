@@ -1642,7 +1642,8 @@ def ep_expert_glu_backward(grad_out: torch.Tensor, pre: torch.Tensor, x: torch.T
     [rows, N] that it left; otherwise as ep_expert_matmul_backward.
 
     ``workspace`` (uint8, ep_expert_backward_workspace_size bytes) also holds
-    the gradients of gate and up, in the rows' type."""
+    the gradients of gate and up, in the rows' type (fp16: infinite past 65504,
+    0 below 2^-25)."""
     on, N, R, ld_g, tail, grad_rows, grad_weights, workspace = _expert_backward(
         grad_out, x, weights, offsets, src, counts, grad_rows, grad_weights, want_rows, want_weights,
         weights_dtype, workspace, stream, True)
@@ -1673,7 +1674,8 @@ def ep_expert_matmul_fp8(x: torch.Tensor, x_scales: torch.Tensor, weights: torch
     (bfloat16 or float16), outside autograd and without a backward call.
 
     Sums are fp32; with more than a few rows per expert, of each 8 neighbouring
-    products what lies 2^-13 below the largest is dropped."""
+    products what lies 2^-13 below the largest is dropped, so that a row's last
+    bits may differ with the number of rows around it."""
     if fmt not in _FORMATS:
         raise ValueError(f"unknown fmt {fmt!r} (e4m3 or e5m2)")
     if not isinstance(x, torch.Tensor) or x.dtype != torch.uint8:

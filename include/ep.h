@@ -947,7 +947,8 @@ ep_status_t ep_expert_matmul_w4(const void *x, int dtype, int64_t ld_x, int64_t 
  *      pre      ep_expert_glu: NULL, or dtype [num_rows, out_features], row
  *               stride ld_pre: gate and up, for the backward.
  * Rows that belong to no expert are not written.  Sums are fp32, in a fixed
- * order; the result (after the activation, in fp32) is rounded once.  src
+ * order; the result (after the activation, in fp32) is rounded once.  silu of a
+ * gate below about -87 counts as 0 (it is less than 1e-35).  src
  * outside [0, num_x_rows) reads row 0.  No output may overlap an input.
  * Rows and weights that start on 16 bytes and are whole 16-byte vectors are
  * fastest.
@@ -972,7 +973,10 @@ ep_status_t ep_expert_glu(const void *x, int dtype, int64_t ld_x, int64_t num_x_
  *                     an expert without rows)
  *
  * d is grad_out for ep_expert_matmul; for ep_expert_glu it is made from
- * grad_out and pre in fp32 and rounded to dtype (the matrix cores' type).
+ * grad_out and pre in fp32 and rounded to dtype (the matrix cores' type), as a
+ * gradient handed from one call to the next is: half a step relative to each
+ * term of the sums, and in fp16 infinite past 65504 and 0 below 2^-25 also where
+ * the sums over it are neither (loss scaling is the caller's).
  *
  * In:  grad_out   dtype [num_rows, out_features] (out_features / 2 columns
  *                 for ep_expert_glu), row stride ld_grad_out.
@@ -1044,9 +1048,12 @@ ep_status_t ep_expert_glu_backward(const void *grad_out, int dtype, int64_t ld_g
  * in_features: a multiple of 16, at most EP_MAX_HIDDEN.  Products of codes
  * are exact; their sums over a block, the product of the two scales and the
  * sums over blocks are fp32, in a fixed order, and the result is rounded once.
- * With more than a few rows per expert the matrix cores' 8-bit instructions
- * are taken, which of each 8 neighbouring products drop what lies 2^-13 below
- * the largest.  A scale byte of 255 counts as infinity.
+ * With more than a few rows per expert (num_rows / num_experts, 8 to 64) the
+ * matrix cores' 8-bit instructions are taken, which of each 8 neighbouring
+ * products drop what lies 2^-13 below the largest: less than the result's own
+ * rounding, but where products of one 8 cancel 2^-13 of these and not of the
+ * result.  So a row's last bits may differ with the number of rows around it;
+ * with few rows nothing is dropped.  A scale byte of 255 counts as infinity.
  * Rows that belong to no expert are not written.
  */
 ep_status_t ep_expert_matmul_fp8(const void *x, int x_format, int64_t ld_x, int64_t num_x_rows,

@@ -58,3 +58,25 @@ def test_all_experts_of_the_widest_output(kind):
     table = (x.double() @ some.double().t()).bfloat16()             # exact
     for e in range(E):
         assert torch.equal(got[e], table[e][(e + at) % 61]), e
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("each", [3, 500])
+def test_range_of_the_gated_gradient(dtype, each):
+    """The gradient of gate and up is of the rows' type between the activation
+    and the products: in fp16 infinite past 65504 and 0 below 2^-25, also where
+    the sums over it are neither; bf16 has the range of fp32."""
+    K, half = 16, 8
+    w = torch.full((1, 2 * half, K), 2.0 ** -10, dtype=dtype, device=DEV)
+    x = torch.full((each, K), 1024.0, dtype=dtype, device=DEV)
+    pre = torch.zeros(each, 2 * half, dtype=dtype, device=DEV)
+    for g, up, d in ((32768.0, 8.0, 2.0 ** 17), (2.0 ** -24, 2.0 ** -3, 2.0 ** -28)):
+        # gate 0: d_gate = g up / 2, d_up = 0; in one row, so all sums are exact
+        grad = torch.zeros(each, half, dtype=dtype, device=DEV)
+        grad[0] = g
+        pre[:, half:] = up
+        gr, gw = ep.ep_expert_glu_backward(grad, pre, x, w, weights_dtype=torch.float32)
+        if dtype == torch.float16:
+            d = float("inf") if d > 1 else 0.0
+        assert bool((gr[0] == half * d * 2.0 ** -10).all()) and bool((gw[0, :half] == d * 1024).all())
+        assert bool((gr[1:] == 0).all()) and bool((gw[0, half:] == 0).all())
