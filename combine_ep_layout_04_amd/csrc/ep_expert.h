@@ -99,7 +99,9 @@ bool expert_fp8_fits(const ExpertFp8Args& a);
 // 91 to 77, 139 to 80; 16 experts 2048 -> 4096 (256 tiles) 12 rows 59 to 51;
 // 8 experts (128 tiles) 24 rows 38 to 45, 32 rows 41 to 46; 1 expert (16 tiles)
 // 64 rows 10.7 to 24.5, 128 rows 17.6 to 25.0; 2 experts (32 tiles) 64 rows
-// 22.0 to 24.7, 128 rows 35.8 to 25.8.
+// 22.0 to 24.7, 128 rows 35.8 to 25.8.  The last border, 64 rows, is that of 32
+// tiles; 16 tiles and fewer lose by it from 65 to 128 rows.  It would move with
+// the walk of ep_product.h, which gives so few tiles to a few XCDs only.
 inline bool few_rows(int64_t num_rows, int num_experts, int n)
 {
     const int64_t hold = num_rows < num_experts ? num_rows : num_experts;  // experts that can have a row

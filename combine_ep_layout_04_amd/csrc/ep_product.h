@@ -175,7 +175,10 @@ constexpr int64_t kMostBlocks = 1 << 22;
 // its 32 CUs work on together: `group` row blocks by kRun / group column
 // tiles, so both operands are read into that XCD's L2 a few times only.  A
 // workgroup takes its place in every run of its XCD in turn; two or more to a
-// CU take neighbouring runs.
+// CU take neighbouring runs.  A run is 32 tiles however few there are, and row
+// blocks are rounded up to whole groups: fewer than 256 tiles leave XCDs idle (8
+// experts of 60 rows and 2048 outputs, 64 tiles, are on two of the eight), so
+// calls of middle size run at a half to a quarter of what the chip could.
 constexpr int kRun = 32, kXcds = 8;
 
 inline int64_t tile_count(int64_t items, int group, int col_tiles)
